@@ -13,6 +13,11 @@
  *   up_slot_mapping  KV slot ids of a (compacted) stream from a layer's block table         [UP 3.5, Eq. 16]
  *   up_seqused       per-layer KV length seen by decode, from the drop history              [UP 3.5, Eq. 17]
  *
+ * The paged key-value cache those slots and lengths belong to:
+ *   up_kv_write      new keys and values into the cache rows of a slot mapping, bf16 or quantised to e4m3
+ *   up_kv_read       cache rows back to a packed bf16 stream (the K of up_score_blocks)
+ *   up_paged_decode  attention of one new token per request over its pages, with up_seqused's lengths
+ *
  * Conventions shared by every call:
  *  - All array pointers are DEVICE pointers owned by the caller; the library
  *    never allocates, frees or keeps a pointer after a call returns.
@@ -66,6 +71,9 @@ typedef enum {
 #define UP_DEV_BAD_POSITION     5   /* Eq. 16: a position beyond its block-table row (slot = -1) */
 #define UP_DEV_BAD_TOKEN_COUNT  6   /* num_actual_tokens outside [0, T_upper]                     */
 #define UP_DEV_BOUNDS           7   /* bounds-checked build only: an index outside its array      */
+#define UP_DEV_BAD_SLOT         8   /* a cache slot outside [-1, num_blocks * B)                  */
+#define UP_DEV_BAD_PAGE         9   /* a block-table entry in use lies outside [0, num_blocks)    */
+#define UP_DEV_BAD_LENGTH      10   /* seqused outside [0, max_blocks * B]                        */
 
 #define UP_MAX_BLOCKS_PER_REQUEST 8192   /* up to this many blocks up_select_topp sorts a request in
                                             shared memory; longer requests need its workspace */
@@ -225,6 +233,83 @@ up_status up_seqused(const int32_t* kept_len, const uint8_t* drop_layer, int L, 
                      const int32_t* orig_len, const int32_t* kv_len, int32_t* seqused, void* stream);
 
 /* ------------------------------------------------------------------------------------------- */
+/* the paged key-value cache                                                                    */
+
+/* How a cache holds its rows (one row = one token and KV head, dk numbers). */
+#define UP_KV_BF16 0   /* bf16                                                                    */
+#define UP_KV_E4M3 1   /* e4m3 codes (4 exponent, 3 mantissa bits, bias 7; largest 448) and one scale byte a row */
+
+/* One layer's cache: num_blocks pages of B tokens.  Slot s (up_slot_mapping) is token s mod B of page
+ * floor(s / B).  Keys and values lie apart at the same strides: row (page, head, token) starts at element
+ * page * stride_block + head * stride_head + token * stride_token of k (v) and is contiguous.  The
+ * layout the kernels read best is [num_blocks, Hkv, B, dk] (a head's page is one run); any other order of
+ * the first three axes works too.  k and v are 16-byte aligned and every stride is a multiple of 16
+ * bytes.  dk in {64, 128, 256}.
+ * UP_KV_E4M3: k_scale and v_scale are uint8 [num_blocks, Hkv, up_kv_scale_row(B)], 16-byte aligned (the
+ * bytes past the B-th of a row are not used); byte b of a row means the row's numbers are code * 2^(b-127).
+ * UP_KV_BF16: k_scale and v_scale are ignored. */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int64_t num_blocks;
+    int64_t stride_block, stride_head, stride_token;   /* in elements */
+    int32_t Hkv, B, dk, format;
+} up_kv_cache;
+
+/* Scale bytes of one page and head: B rounded up to a multiple of 16 (0 for B <= 0). */
+int up_kv_scale_row(int B);
+
+/* Write new keys and values into the cache: row slots[t] of every head <- k[t], v[t].
+ * Tokens t < *num_tokens (or < T if num_tokens is NULL; a count outside [0, T] sets
+ * UP_DEV_BAD_TOKEN_COUNT and nothing is written).  slots: int64 [T]; -1 skips the token (a padded row, or
+ * a position up_slot_mapping refused); any other slot outside [0, num_blocks * B) is skipped and sets
+ * UP_DEV_BAD_SLOT.  Two tokens of a call must not name the same slot.
+ * k, v: bf16, token t's heads at k + t * k_stride, packed [Hkv, dk] (k_stride in elements, a multiple of 8,
+ * >= Hkv * dk when T > 1: a slice of a fused projection's output needs no copy); 16-byte aligned; either may
+ * be NULL, which leaves that side of the cache alone.
+ * UP_KV_BF16 copies the bits.  UP_KV_E4M3 quantises each row with the least power of two 2^e (e in
+ * [-126, 127]) that brings its largest finite magnitude to 448 or below (e = 0 for a row of zeros):
+ * scale byte e + 127, codes = x * 2^-e rounded to nearest even (the scaling is exact, so this is the only
+ * rounding).  Infinities and NaN become NaN codes. */
+up_status up_kv_write(const up_kv_cache* cache, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                      int64_t v_stride, const int64_t* slots, int64_t T, const int32_t* num_tokens,
+                      int32_t* dev_status, void* stream);
+
+/* Read cache rows back to a packed stream: k[t], v[t] (bf16 [T, Hkv, dk], 16-byte aligned) <- row
+ * slots[t] of every head.  num_tokens and slots as in up_kv_write, except that the row of a skipped token
+ * (slot -1, or one outside the cache) is written as zeros.  k or v may be NULL.  UP_KV_E4M3 rows are
+ * code * 2^(b-127), exact in bf16 but at the ends of its range: results below its normal numbers are
+ * rounded to nearest even, and magnitudes written as 248 * 2^120 or more (rounded to 2^128) come back infinite. */
+up_status up_kv_read(const up_kv_cache* cache, const int64_t* slots, int64_t T, const int32_t* num_tokens,
+                     uint16_t* k, uint16_t* v, int32_t* dev_status, void* stream);
+
+/* Workspace of up_paged_decode for R requests whose block-table rows have max_blocks entries; 0 when the
+ * arguments are invalid.  window as in the call. */
+size_t up_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window);
+
+/* Attention of one new token per request over its cached tokens, at one layer:
+ *   out[r, h] = sum_i softmax_i(q[r, h] . K_i * sm_scale) V_i   over positions i in [lo, len),
+ *   len = seqused[r] (up_seqused's Eq. 17 length, the new token's own row included when it has been
+ *   written), lo = window > 0 ? max(0, len - window) : 0; position i is token i mod B of page
+ *   block_table[r * max_blocks + floor(i / B)]; query head h reads KV head h / (Hq / Hkv).
+ * lse[r, h] (fp32, optional) = ln sum_i exp(q . K_i * sm_scale).  A request with no position (len = 0) gets
+ * zeros and -inf.  Rows of the cache at positions outside [lo, len) have no influence, whatever they hold.
+ * q: bf16, request r's heads at q + r * q_stride, packed [Hq, dk] (q_stride in elements, a multiple of 8);
+ * out: bf16 [R, Hq, dk]; both 16-byte aligned.  seqused: int32 [R]; block_table: int32 [R, max_blocks]
+ * (requests may share pages; entries past a request's last page are not read).
+ * A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a table entry outside
+ * [0, num_blocks) sets UP_DEV_BAD_PAGE and its keys and values count as zeros.
+ * Arithmetic: products of the cache's numbers with q in full, fp32 accumulation and softmax.  The range
+ * of a request is split by its own length alone, so a request's result does not depend on the others.
+ * ws: device workspace of up_paged_decode_workspace_bytes(...) bytes, 16-byte aligned, no initialisation. */
+up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const up_kv_cache* cache,
+                          const int32_t* block_table, const int32_t* seqused, int R, int max_blocks, int Hq,
+                          float sm_scale, int window, uint16_t* out, float* lse,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------------- */
 /* status and introspection                                                                     */
 
 /* Synchronises `stream`, copies *dev_status to *host_out, returns UP_ERR_DEVICE if it is not 0. */
@@ -236,7 +321,8 @@ const char* up_status_string(int code, int device);
 /* Number of kernels this library has launched in this process (for launch accounting). */
 uint64_t up_kernel_launches(void);
 
-/* ABI version of this header: 2 (up_select_topp takes a workspace). */
+/* ABI version of this header: 2 (up_select_topp takes a workspace; the cache's entry points were added
+ * without changing an older one). */
 int up_abi_version(void);
 
 /* 1 in the bounds-checked build of the library (compiled with -DUP_DEBUG_BOUNDS, a development aid:

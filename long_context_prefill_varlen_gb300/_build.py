@@ -14,7 +14,7 @@ LIB = os.path.join(PKG, "libuniprefill.so")
 # a violation in the status word; a development aid, not loaded by the package
 DEBUG_LIB = os.path.join(PKG, "libuniprefill_debug.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["up_score.cu", "up_select.cu", "up_compact.cu", "up_meta.cu"]
+SOURCES = ["up_score.cu", "up_select.cu", "up_compact.cu", "up_meta.cu", "up_kv.cu", "up_decode.cu"]
 
 
 def nvcc():
@@ -34,7 +34,7 @@ def _stale(out, deps):
 def build(verbose=False, force=False, ptxas_verbose=False, debug_bounds=False):
     """Compile every translation unit for sm_103a and link the shared library; returns its path.
     debug_bounds=True builds the bounds-checked variant (libuniprefill_debug.so) instead."""
-    deps_common = [os.path.join(CSRC, "up_internal.cuh"),
+    deps_common = [os.path.join(CSRC, "up_internal.cuh"), os.path.join(CSRC, "up_kv.cuh"),
                    os.path.join(os.path.dirname(PKG), "include", "uniprefill.h"), __file__]
     objdir = os.path.join(PKG, "_build", "debug" if debug_bounds else "")
     os.makedirs(objdir, exist_ok=True)

@@ -1,0 +1,304 @@
+// up_kv_write and up_kv_read: rows between a packed bf16 stream and the paged cache that up_slot_mapping's
+// slots name (section 3.5, Eq. 16 of "UniPrefill: Universal Long-Context Prefill Acceleration via
+// Block-wise Dynamic Sparsification", arXiv 2605.06221, gives the slots; the quantised form is this
+// library's own).
+//
+// e4m3 rows: one power of two 2^e per row, the least with max|x| 2^-e <= 448 = 1.75 * 2^8.  For a bf16
+// maximum of exponent field E and mantissa field M that is e + 127 = E - 8 + [M > 0x60] (1.75 has mantissa
+// 0x60): two integer operations on the row's largest bit pattern.  Scaling by a power of two is exact in
+// fp32, so a code has one rounding, and reading back is exact: a scale that is not a power of two would
+// round on both sides and take four bytes instead of one.
+//
+// Both kernels only move bytes (write: 2 dk in, dk + 1 or 2 dk out per row; read: the reverse): HBM-bound.  A
+// row belongs to dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that a row's maximum is a few
+// shuffles and every access is a whole run; each lane has kUnroll rows in flight.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "up_kv.cuh"
+
+namespace up {
+namespace kv {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+struct Side {              // keys or values of a call
+    const uint8_t* src;    // write: the stream; read: the cache
+    uint8_t* dst;
+    uint8_t* scale;
+    int64_t stride;        // bytes from token to token of the stream
+};
+
+struct Args {
+    Side side[2];
+    Cache c;
+    FastDiv by_b, by_heads;
+    const int64_t* slots;
+    int64_t T;
+    const int32_t* num_tokens;
+    int32_t* status;
+};
+
+// tokens of the call, -1 if the device's count is not in [0, T]
+__device__ __forceinline__ int64_t token_count(const Args& a) {
+    if (!a.num_tokens) return a.T;
+    const int c = *a.num_tokens;
+    if (c >= 0 && c <= a.T) return c;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, UP_DEV_BAD_TOKEN_COUNT);
+    return -1;
+}
+
+// page and token of a slot; false (with the status) for one outside the cache
+__device__ __forceinline__ bool place(const Args& a, int64_t slot, int64_t* page, int* tok) {
+    if (slot >= 0 && slot < (int64_t{1} << 31)) {
+        const uint32_t p = div_of(static_cast<uint32_t>(slot), a.by_b);
+        *page = p;
+        *tok = static_cast<int>(static_cast<uint32_t>(slot) - p * a.by_b.d);
+    } else if (slot >= 0) {
+        *page = slot / a.c.B;
+        *tok = static_cast<int>(slot - *page * a.c.B);
+    } else {
+        if (slot != -1) set_status(a.status, UP_DEV_BAD_SLOT);
+        return false;
+    }
+    if (*page < a.c.num_blocks) return true;
+    set_status(a.status, UP_DEV_BAD_SLOT);
+    return false;
+}
+
+__device__ __forceinline__ float f_of(uint32_t bits) { return __uint_as_float(bits); }
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// largest 16-bit half over the LPR lanes of a row
+template <int LPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return max(m & 0xffffu, m >> 16);
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// a pair of halves with every half that is infinite or NaN as zero (for the maximum) or as NaN
+__device__ __forceinline__ uint32_t finite_or(uint32_t w, uint32_t other) {
+    const uint32_t lo = (w & 0x7fffu) >= 0x7f80u ? (other & 0xffffu) : (w & 0xffffu);
+    const uint32_t hi = ((w >> 16) & 0x7fffu) >= 0x7f80u ? (other & 0xffff0000u) : (w & 0xffff0000u);
+    return lo | hi;
+}
+
+template <int DK, bool E4M3>
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Args a) {
+    constexpr int LPR = DK / 8;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = token_count(a);
+    const Side s = a.side[blockIdx.y];
+    if (!s.src || n <= 0) return;
+    const int64_t rows = n * a.c.Hkv;
+    const int lane = threadIdx.x % LPR;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / LPR);
+    // every lane of a warp takes the same number of rounds (the shuffles name all 32)
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int64_t rounds = (rows + step * kUnroll - 1) / (step * kUnroll);
+    for (int64_t i = 0; i < rounds; ++i) {
+        uint4 x[kUnroll];
+        int64_t page[kUnroll];
+        int tok[kUnroll], head[kUnroll];
+        bool live[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t row = first + (i * kUnroll + u) * step;
+            live[u] = row < rows;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (live[u]) {
+                const int64_t t = row < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(row), a.by_heads) : row / a.c.Hkv;
+                head[u] = static_cast<int>(row - t * a.c.Hkv);
+                live[u] = UP_IN(t, a.T, a.status) && place(a, a.slots[t], &page[u], &tok[u]);
+                if (live[u])
+                    x[u] = *reinterpret_cast<const uint4*>(s.src + t * s.stride + (head[u] * DK + lane * 8) * 2);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t at = live[u] ? page[u] * a.c.sb + head[u] * a.c.sh + tok[u] * a.c.st : 0;
+            if constexpr (!E4M3) {
+                if (live[u] && UP_IN(at + lane * 16, a.c.row_limit, a.status))
+                    *reinterpret_cast<uint4*>(s.dst + at + lane * 16) = x[u];
+            } else {
+                uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                       max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                m = row_max<LPR>(m);
+                if (__any_sync(0xffffffffu, m >= 0x7f80u)) {      // a row with infinities or NaN
+                    uint32_t f = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f = max_u16x2(f, finite_or(w[j], 0) & 0x7fff7fffu);
+                        w[j] = finite_or(w[j], 0x7fff7fffu);
+                    }
+                    m = row_max<LPR>(f);
+                }
+                int b = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0);
+                b = m == 0 ? 127 : max(b, 1);
+                const float inv = f_of(static_cast<uint32_t>(254 - b) << 23);      // 2^(127 - b)
+                uint32_t c[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[j] = to_e4m3x2(f_of(w[j] << 16) * inv, f_of(w[j] & 0xffff0000u) * inv);
+                if (live[u] && UP_IN(at + lane * 8, a.c.row_limit, a.status)) {
+                    *reinterpret_cast<uint2*>(s.dst + at + lane * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    const int64_t sc = (page[u] * a.c.Hkv + head[u]) * a.c.Bp + tok[u];
+                    if (lane == 0 && UP_IN(sc, a.c.scale_limit, a.status)) s.scale[sc] = static_cast<uint8_t>(b);
+                }
+            }
+        }
+    }
+}
+
+// two f16 numbers times a power of two, to bf16
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
+    float lo, hi;
+    asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h2));
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi * scale), "f"(lo * scale));
+    return r;
+}
+
+template <int DK, bool E4M3>
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Args a) {
+    constexpr int LPR = DK / 8;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = token_count(a);
+    const Side s = a.side[blockIdx.y];
+    if (!s.dst || n <= 0) return;
+    const int64_t rows = n * a.c.Hkv;
+    const int lane = threadIdx.x % LPR;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / LPR);
+    for (int64_t row0 = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; row0 < rows; row0 += step * kUnroll) {
+        uint4 x[kUnroll];
+        int b[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t row = row0 + u * step;
+            x[u] = make_uint4(0, 0, 0, 0);
+            b[u] = 127;
+            if (row < rows) {
+                const int64_t t = row < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(row), a.by_heads) : row / a.c.Hkv;
+                const int head = static_cast<int>(row - t * a.c.Hkv);
+                int64_t page = 0;
+                int tok = 0;
+                if (UP_IN(t, a.T, a.status) && place(a, a.slots[t], &page, &tok)) {
+                    const int64_t at = page * a.c.sb + head * a.c.sh + tok * a.c.st + lane * (E4M3 ? 8 : 16);
+                    if (UP_IN(at, a.c.row_limit, a.status)) {
+                        if constexpr (E4M3) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(s.src + at);
+                            x[u].x = v.x;
+                            x[u].y = v.y;
+                            const int64_t sc = (page * a.c.Hkv + head) * a.c.Bp + tok;
+                            b[u] = UP_IN(sc, a.c.scale_limit, a.status) ? s.scale[sc] : 0;
+                        } else {
+                            x[u] = *reinterpret_cast<const uint4*>(s.src + at);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t row = row0 + u * step;
+            if (row >= rows) break;
+            if constexpr (E4M3) {
+                const float f = b[u] ? f_of(static_cast<uint32_t>(b[u]) << 23) : f_of(0x00400000u);   // 2^(b - 127)
+                const uint2 v = make_uint2(x[u].x, x[u].y);
+                x[u] = make_uint4(scaled_bf16x2(e4m3x2_to_f16x2(v.x), f), scaled_bf16x2(e4m3x2_to_f16x2(v.x >> 16), f),
+                                  scaled_bf16x2(e4m3x2_to_f16x2(v.y), f), scaled_bf16x2(e4m3x2_to_f16x2(v.y >> 16), f));
+            }
+            if (UP_IN(row * DK + lane * 8, a.T * a.c.Hkv * DK, a.status))
+                *reinterpret_cast<uint4*>(s.dst + (row * DK + lane * 8) * 2) = x[u];
+        }
+    }
+}
+
+template <bool WRITE>
+static up_status launch(const Args& a, int dk, int format, cudaStream_t st) {
+    const int64_t rows = a.T * a.c.Hkv;
+    const int64_t per = kThreads / (dk / 8);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, per), 4 * num_sms())));
+    const dim3 g(grid, 2), b(kThreads);
+    const bool f8 = format == UP_KV_E4M3;
+    cudaError_t e;
+#define UP_KV_CASE(DK)                                                                                      \
+    case DK:                                                                                                \
+        if (WRITE)                                                                                          \
+            e = f8 ? launch_pdl(write_kernel<DK, true>, g, b, 0, st, a) : launch_pdl(write_kernel<DK, false>, g, b, 0, st, a); \
+        else                                                                                                \
+            e = f8 ? launch_pdl(read_kernel<DK, true>, g, b, 0, st, a) : launch_pdl(read_kernel<DK, false>, g, b, 0, st, a);   \
+        break
+    switch (dk) {
+        UP_KV_CASE(64);
+        UP_KV_CASE(128);
+        UP_KV_CASE(256);
+        default: return UP_ERR_SHAPE;
+    }
+#undef UP_KV_CASE
+    if (e != cudaSuccess) return UP_ERR_CUDA;
+    count_launch();
+    return check_launch();
+}
+
+}  // namespace kv
+}  // namespace up
+
+using namespace up;
+
+extern "C" int up_kv_scale_row(int B) { return kv::scale_row(B); }
+
+extern "C" up_status up_kv_write(const up_kv_cache* cache, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                 int64_t v_stride, const int64_t* slots, int64_t T, const int32_t* num_tokens,
+                                 int32_t* dev_status, void* stream) {
+    kv::Args a{};
+    if (!dev_status || T < 0) return UP_ERR_ARG;
+    const up_status s = kv::check(cache, &a.c);
+    if (s != UP_OK) return s;
+    if (T == 0 || (!k && !v)) return UP_OK;
+    if (!slots) return UP_ERR_ARG;
+    const int64_t row = static_cast<int64_t>(cache->Hkv) * cache->dk;
+    if ((k && (!aligned16(k) || k_stride % 8)) || (v && (!aligned16(v) || v_stride % 8))) return UP_ERR_SHAPE;
+    if (T > 1 && ((k && k_stride < row) || (v && v_stride < row))) return UP_ERR_SHAPE;
+    a.side[0] = {reinterpret_cast<const uint8_t*>(k), static_cast<uint8_t*>(cache->k), cache->k_scale, k_stride * 2};
+    a.side[1] = {reinterpret_cast<const uint8_t*>(v), static_cast<uint8_t*>(cache->v), cache->v_scale, v_stride * 2};
+    a.by_b = kv::fast_div(cache->B);
+    a.by_heads = kv::fast_div(cache->Hkv);
+    a.slots = slots;
+    a.T = T;
+    a.num_tokens = num_tokens;
+    a.status = dev_status;
+    return kv::launch<true>(a, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" up_status up_kv_read(const up_kv_cache* cache, const int64_t* slots, int64_t T, const int32_t* num_tokens,
+                                uint16_t* k, uint16_t* v, int32_t* dev_status, void* stream) {
+    kv::Args a{};
+    if (!dev_status || T < 0) return UP_ERR_ARG;
+    const up_status s = kv::check(cache, &a.c);
+    if (s != UP_OK) return s;
+    if (T == 0 || (!k && !v)) return UP_OK;
+    if (!slots) return UP_ERR_ARG;
+    if (!aligned16(k) || !aligned16(v)) return UP_ERR_SHAPE;
+    a.side[0] = {static_cast<const uint8_t*>(cache->k), reinterpret_cast<uint8_t*>(k), cache->k_scale, 0};
+    a.side[1] = {static_cast<const uint8_t*>(cache->v), reinterpret_cast<uint8_t*>(v), cache->v_scale, 0};
+    a.by_b = kv::fast_div(cache->B);
+    a.by_heads = kv::fast_div(cache->Hkv);
+    a.slots = slots;
+    a.T = T;
+    a.num_tokens = num_tokens;
+    a.status = dev_status;
+    return kv::launch<false>(a, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
+}

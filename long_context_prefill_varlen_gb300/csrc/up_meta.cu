@@ -137,6 +137,9 @@ extern "C" const char* up_status_string(int code, int device) {
             case UP_DEV_BAD_POSITION: return "a position lies outside its block-table row";
             case UP_DEV_BAD_TOKEN_COUNT: return "num_actual_tokens lies outside [0, T_upper]";
             case UP_DEV_BOUNDS: return "an index lies outside its array (bounds-checked build)";
+            case UP_DEV_BAD_SLOT: return "a cache slot lies outside [-1, num_blocks * B)";
+            case UP_DEV_BAD_PAGE: return "a block-table entry in use lies outside [0, num_blocks)";
+            case UP_DEV_BAD_LENGTH: return "seqused lies outside [0, max_blocks * B]";
             default: return "unknown device status";
         }
     }
