@@ -2,14 +2,30 @@
 // lengths that the drop history leaves each layer (up_seqused, section 3.5, Eq. 17 of "UniPrefill:
 // Universal Long-Context Prefill Acceleration via Block-wise Dynamic Sparsification", arXiv 2605.06221).
 //
-// The positions [lo, len) of a request are cut into tiles of kTile rows (whole pages, or parts of one
-// page) and the tiles into chunks, by the request's own length alone.  Each (request, KV head, chunk) gives
-// for each query head of the group
+// The positions [lo, len) of a request are cut into tiles of up to kTile rows (whole pages, or parts of
+// one page) and the tiles into chunks, by the request's own length alone.  Each (request, KV head, chunk)
+// gives for each query head of the group
 //   lse2 = log2 sum_i 2^(s_i)   and   o = sum_i 2^(s_i - lse2) v_i,   s_i = q . k_i * sm_scale * log2 e
 // and the join adds the chunks in order: out = sum_c 2^(lse2_c - L) o_c, L = log2 sum_c 2^(lse2_c).
+//
+// A cached number is used once per query head of its group, so HBM bounds the call from the first
+// thousand positions on: 2 dk (dk + 1) bytes a row in bf16 (e4m3).  split_kernel keeps enough copies in flight
+// and the rest out of their way:
+//  * persistent CTAs take runs of (request, chunk, head) items of equal length in tiles; every CTA finds its
+//    run from seqused itself, so no launch plans and the host never waits for a length;
+//  * a producer warp walks the run and fills a ring of stages (the K and V tile of one head) by TMA, one
+//    box per page and 128 bytes of dk, swizzled so that ldmatrix reads it without bank conflicts; the ring
+//    runs across items, so a new item's first tiles are there when the last one's sums are written;
+//  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
+//    running maximum and sums, joined through the last stage when the item ends.
+// The products are m16n8k16 (rows: query heads; a group below 16 leaves rows empty, which the bf16 form uses
+// for the low halves of the weights).  A matrix unit with larger tiles has nothing to win here: 16 rows of
+// queries are all there is, and the copies take four times as long as these products.
 #include <stdint.h>
 
 #include <algorithm>
+#include <mutex>
+#include <type_traits>
 
 #include "up_kv.cuh"
 
@@ -17,44 +33,53 @@ namespace up {
 namespace decode {
 
 using kv::Cache;
+using kv::FastDiv;
 
 constexpr int kTile = 64;            // rows of a tile
+constexpr int kWarps = 4;            // consumer warps, 16 rows of a tile each
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMinTiles = 4;         // a chunk holds at least this many tiles, if the request has them
+constexpr int kMaxTiles = 16;        // about as many tiles as a chunk holds, up to kMaxSplits chunks
+constexpr int kMaxSplits = 320;
+constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or values) in a stage
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;        // a running maximum moves once a score passes it by this much (log2)
 
 // How the positions of a request fall into segments (a page, or up to kTile rows of one), tiles of spt
 // segments, and chunks of tiles.
 struct Cut {
-    int B, seg, spp, spt;      // page; rows of a segment; segments of a page; segments of a tile
-    int window, s0;            // s0: chunks that spread one request's heads evenly over the grid
+    int B, seg, segp, spp, spt;      // page; rows of a segment, and of its place in a tile; segments of a
+                                     // page, of a tile
+    int window, s0;                  // s0: chunks that spread one request's heads evenly over the grid
     int max_splits;
+    FastDiv by_b, by_spt, by_spp, by_segp;
 };
 
 struct Range {
-    int len, lo;               // positions [lo, len)
-    int seg0, tiles, splits;   // first segment; tiles from there; chunks
+    int len, lo;                     // positions [lo, len)
+    int seg0, seg1, tiles, splits;   // first and last segment; tiles from the first; chunks
 };
 
 __host__ __device__ inline int splits_of(int tiles, int s0) {
-    const int by_min = (tiles + kMinTiles - 1) / kMinTiles;
-    return by_min < s0 ? by_min : s0;
+    const int fine = (tiles + kMinTiles - 1) / kMinTiles;
+    if (fine <= s0) return fine;
+    const int waves = (tiles + s0 * kMaxTiles - 1) / (s0 * kMaxTiles), most = kMaxSplits / s0;
+    return s0 * (waves < most ? waves : most);
 }
 
 __device__ __forceinline__ Range range_of(const Cut& c, int len, int64_t cap) {
     Range r;
     r.len = len < 0 || len > cap ? 0 : len;
     r.lo = c.window > 0 && r.len > c.window ? r.len - c.window : 0;
-    const int p0 = r.lo / c.B, p1 = r.len > 0 ? (r.len - 1) / c.B : 0;
-    r.seg0 = p0 * c.spp + (r.lo - p0 * c.B) / c.seg;
-    const int seg1 = p1 * c.spp + (r.len > 0 ? (r.len - 1 - p1 * c.B) / c.seg : 0);
-    r.tiles = r.len > r.lo ? (seg1 - r.seg0) / c.spt + 1 : 0;
+    const int last = r.len > 0 ? r.len - 1 : 0;
+    const int p0 = div_of(r.lo, c.by_b), p1 = div_of(last, c.by_b);
+    r.seg0 = p0 * c.spp + (r.lo - p0 * c.B) / kTile;
+    r.seg1 = p1 * c.spp + (last - p1 * c.B) / kTile;
+    r.tiles = r.len > 0 ? div_of(r.seg1 - r.seg0, c.by_spt) + 1 : 0;
     r.splits = splits_of(r.tiles, c.s0);
     return r;
 }
-
-// 2^(x - m), and 0 for x = -inf whatever m is (m is the largest of a set that x belongs to; NaN stays)
-__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : exp2f(x - m); }
 
 struct Args {
     const uint8_t* q;
@@ -62,99 +87,681 @@ struct Args {
     Cache c;
     const int32_t* table;
     const int32_t* seqused;
-    int R, max_blocks, Hq, group;
+    int R, max_blocks, Hq, group, head_tiles;
     float scale2;              // sm_scale * log2 e
     Cut cut;
     float* part_lse;           // [R, Hq, max_splits]
     float* part_o;             // [R, Hq, max_splits, dk]
+    int64_t parts;             // R * Hq * max_splits
     uint16_t* out;
     float* lse;
     int32_t* status;
 };
 
+// 2^(x - m), and 0 for x = -inf whatever m is (m is the largest of a set that x belongs to; NaN stays)
+__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : ex2(x - m); }
+
+__device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
+
 // ------------------------------------------------------------------------------------------------
-// one CTA per (chunk, KV head, request): a warp per row, lanes over dk
+// the walk over a CTA's run of items.  Item order: request, chunk, KV head, head tile.
+
+struct Walk {
+    int r, ch, unit;           // unit: KV head * head_tiles + head tile
+    Range g;
+    int q, rem;                // tiles of a chunk: q + 1 for the first rem chunks, q after
+    int64_t start, end;        // tiles before the item, and where the run ends
+    int next_len;
+
+    __device__ __forceinline__ int units(const Args& a) const { return a.c.Hkv * a.head_tiles; }
+    __device__ __forceinline__ int tile0() const { return ch * q + min(ch, rem); }
+    __device__ __forceinline__ int tiles() const { return q + (ch < rem ? 1 : 0); }
+    __device__ __forceinline__ bool live(const Args& a) const { return r < a.R && start < end; }
+
+    __device__ __forceinline__ void enter(const Args& a, int len) {
+        g = range_of(a.cut, len, (int64_t)a.max_blocks * a.cut.B);
+        q = g.splits ? g.tiles / g.splits : 0;
+        rem = g.tiles - q * g.splits;
+        ch = unit = 0;
+        next_len = r + 1 < a.R ? length_of(a, r + 1) : 0;
+    }
+    __device__ __forceinline__ void next(const Args& a) {
+        start += tiles();
+        if (++unit < units(a)) return;
+        unit = 0;
+        if (++ch < g.splits) return;
+        do {
+            if (++r >= a.R) return;
+            enter(a, next_len);
+        } while (g.splits == 0);
+    }
+};
+
+// Every warp finds its CTA's run: first the tiles of all requests, then the first item that starts at or
+// after its share.  Items stay whole, so a run is off by at most one item.
+__device__ __forceinline__ void find_run(const Args& a, Walk& w) {
+    const int lane = threadIdx.x & 31;
+    const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
+    const int units = w.units(a);
+    int64_t total = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 128) {
+        int len[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) len[i] = r0 + 32 * i + lane < a.R ? length_of(a, r0 + 32 * i + lane) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            total += range_of(a.cut, len[i], cap).tiles;
+            if ((len[i] < 0 || len[i] > cap) && blockIdx.x == 0 && threadIdx.x < 32) set_status(a.status, UP_DEV_BAD_LENGTH);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= units;
+    // neighbours in the order of runs are half a grid apart: a short list of items leaves no SM with two
+    // before every SM has one
+    const int n = gridDim.x, half = (n + 1) / 2, b = blockIdx.x;
+    const int64_t at = b < half ? 2 * b : 2 * (b - half) + 1;
+    w.end = total * (at + 1) / n;
+    const int64_t want = total * at / n;
+    w.start = 0;
+    w.r = a.R;
+    if (want >= w.end) return;
+    int64_t before = 0;        // tiles of the requests before
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
+        const int t = r0 + lane < a.R ? range_of(a.cut, length_of(a, r0 + lane), cap).tiles : 0;
+        int64_t s = (int64_t)t * units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + s > want);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            w.r = r0 + l;
+            before += __shfl_sync(0xffffffffu, s - (int64_t)t * units, l);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, s, 31);
+    }
+    w.enter(a, length_of(a, w.r));
+    const int64_t local = want - before;
+    const int u = static_cast<int>(local / units), wide = w.rem * (w.q + 1);
+    w.ch = u < wide ? u / (w.q + 1) : w.rem + (u - wide) / w.q;
+    w.start = before + (int64_t)units * w.tile0();
+    w.unit = static_cast<int>((want - w.start + w.tiles() - 1) / w.tiles());
+    w.start += (int64_t)w.unit * w.tiles();
+    if (w.unit >= units) {     // the last item of the chunk starts before the share: begin with the next chunk
+        w.unit = units - 1;
+        w.start -= w.tiles();
+        w.next(a);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// tiles in shared memory
 
 template <int DK, bool E4M3>
-__global__ void __launch_bounds__(128) chunk_kernel(const __grid_constant__ Args a) {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int E = DK / 32;
-    const int r = blockIdx.z, h = blockIdx.y, ch = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
-    const int len_in = a.seqused[r];
-    if ((len_in < 0 || len_in > cap) && threadIdx.x == 0) set_status(a.status, UP_DEV_BAD_LENGTH);
-    const Range g = range_of(a.cut, len_in, cap);
-    if (ch >= g.splits) return;
-    const int t0 = (int)((int64_t)ch * g.tiles / g.splits), t1 = (int)((int64_t)(ch + 1) * g.tiles / g.splits);
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][DK];
-    for (int j = 0; j < a.group; ++j) {
-        const int hq = h * a.group + j;
-        float q[E], o[E];
-        for (int e = 0; e < E; ++e) {
-            const uint16_t bits = reinterpret_cast<const uint16_t*>(a.q + r * a.q_stride)[hq * DK + lane * E + e];
-            q[e] = __uint_as_float((uint32_t)bits << 16);
-            o[e] = 0.f;
+struct Shape {
+    static constexpr int kRowBytes = DK * (E4M3 ? 1 : 2);
+    static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;      // a tile is panels of rows
+    static constexpr int kPanels = kRowBytes / kPanelBytes;
+    static constexpr int kTileBytes = kTile * kRowBytes;
+    static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
+    // two CTAs on an SM where three stages each fit (228 KB an SM, 1 KB of it per CTA reserved)
+    static constexpr int kCtas = 3 * kStage <= 112 * 1024 ? 2 : 1;
+    static constexpr int kFit = (kCtas == 2 ? 112 * 1024 : 224 * 1024) / kStage;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+};
+
+// byte offset of 16-byte column `c` of row `row` in a tile whose base is 1024-byte aligned, as the TMA
+// swizzle of kPanelBytes-wide rows lays it out
+template <int PANEL>
+__device__ __forceinline__ uint32_t swizzled(int row, int c) {
+    if constexpr (PANEL == 128)
+        return (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    else
+        return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// d += a b: a 16 x 16, b 16 x 8, bf16 or f16 in, fp32 sums
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float low_of(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
+__device__ __forceinline__ float high_of(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------------------------------------------
+// shared memory of a CTA: the stages, then this
+
+template <int DK, int HT, int NS>
+struct Control {
+    alignas(16) uint16_t q[2][HT * DK];        // the item's queries, double-buffered
+    float m[kWarps][16], f[kWarps][16], l[kWarps][16];
+    uint64_t full[NS], empty[NS], qfull[2], qempty[2];
+    int abort;
+};
+
+template <int DK, bool E4M3, int HT>
+struct Sizes {
+    using S = Shape<DK, E4M3>;
+    static constexpr int kSmem = S::kStages * S::kStage + static_cast<int>(sizeof(Control<DK, HT, S::kStages>)) + 1024;
+};
+
+// ------------------------------------------------------------------------------------------------
+
+template <int DK, bool E4M3, int HT>
+__device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
+                        Control<DK, HT, Shape<DK, E4M3>::kStages>& sh, Walk w) {
+    using S = Shape<DK, E4M3>;
+    const int lane = threadIdx.x & 31;
+    const Cut& c = a.cut;
+    int slot = 0, qslot = 0;
+    uint32_t phase = 0, qphase = 0;
+    int64_t issued = 0;
+    bool dead = false;
+    const int per = (32 / c.spt) * c.spt, tiles_per = 32 / c.spt;      // table entries and tiles of a batch
+    const int scs = (c.seg + 15) & ~15;
+    // the table entries of the run's segments, 32 (or the most that make whole tiles) at a time, one batch ahead
+    Walk nw = w;
+    int ntile = 0;                                                      // next batch: its item and first tile
+    auto fetch = [&](const Walk& x, int tile) {
+        const int s = x.g.seg0 + (x.tile0() + tile) * c.spt + lane;
+        int page = -1;
+        if (x.live(a) && lane < per && s <= x.g.seg1) {
+            const int64_t e = (int64_t)x.r * a.max_blocks + div_of(s, c.by_spp);
+            page = UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
         }
-        float m = -INFINITY, l = 0.f;
-        for (int row = t0 * a.cut.spt * a.cut.seg + w; row < t1 * a.cut.spt * a.cut.seg; row += 4) {
-            const int s = g.seg0 + row / a.cut.seg, off = row % a.cut.seg;
-            const int page_i = s / a.cut.spp, tok = (s % a.cut.spp) * a.cut.seg + off;
-            const int64_t pos = (int64_t)page_i * a.cut.B + tok;
-            if (tok >= a.cut.B || pos < g.lo || pos >= g.len) continue;
-            const int page = a.table[(int64_t)r * a.max_blocks + page_i];
-            const bool ok = page >= 0 && page < a.c.num_blocks;
-            if (!ok && lane == 0) set_status(a.status, UP_DEV_BAD_PAGE);
-            float k[E], v[E];
-            for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-            if (ok) {
-                const int64_t at = (int64_t)page * a.c.sb + h * a.c.sh + (int64_t)tok * a.c.st;
-                if constexpr (E4M3) {
-                    const int64_t sc = ((int64_t)page * a.c.Hkv + h) * a.c.Bp + tok;
-                    const float fk = exp2f((float)a.c.ks[sc] - 127.f), fv = exp2f((float)a.c.vs[sc] - 127.f);
-                    for (int e = 0; e < E; ++e) {
-                        const uint32_t ck = kv::e4m3x2_to_f16x2(a.c.k[at + lane * E + e]);
-                        const uint32_t cv = kv::e4m3x2_to_f16x2(a.c.v[at + lane * E + e]);
-                        float x, y;
-                        asm("{\n\t.reg .f16 p, q;\n\tmov.b32 {p, q}, %1;\n\tcvt.f32.f16 %0, p;\n\t}" : "=f"(x) : "r"(ck));
-                        asm("{\n\t.reg .f16 p, q;\n\tmov.b32 {p, q}, %1;\n\tcvt.f32.f16 %0, p;\n\t}" : "=f"(y) : "r"(cv));
-                        k[e] = x * fk;
-                        v[e] = y * fv;
+        return page;
+    };
+    auto step = [&]() {
+        ntile += tiles_per;
+        if (ntile >= nw.tiles()) {
+            nw.next(a);
+            ntile = 0;
+        }
+    };
+    int pages_next = fetch(nw, 0);
+    for (; w.live(a) && !dead; w.next(a)) {
+        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
+        const int heads = min(HT, a.group - h0);
+        if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
+        if (lane == 0) {
+            const uint32_t bar = smem_u32(&sh.qfull[qslot]);
+            mbar_arrive_expect_tx(bar, heads * DK * 2);
+            bulk_load(smem_u32(sh.q[qslot]), a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2, heads * DK * 2, bar);
+        }
+        if (++qslot == 2) qslot = 0, qphase ^= 1;
+        const int n = w.tiles(), t0 = w.tile0();
+        int pages = -1;
+        for (int i = 0, j = tiles_per; i < n; ++i, ++j) {
+            if (j == tiles_per) {                                       // a new batch
+                j = 0;
+                pages = pages_next;
+                step();
+                pages_next = fetch(nw, ntile);
+            }
+            if (!mbar_wait(smem_u32(&sh.empty[slot]), phase ^ 1, &sh.abort)) {
+                dead = true;
+                break;
+            }
+            const int page = __shfl_sync(0xffffffffu, pages, (j * c.spt + lane) & 31);
+            const int s = w.g.seg0 + (t0 + i) * c.spt + lane;
+            const bool mine = lane < c.spt && s <= w.g.seg1;
+            const bool good = mine && page >= 0 && page < a.c.num_blocks;
+            const int part = s - div_of(s, c.by_spp) * c.spp;           // which segment of its page
+            const uint32_t stage = ring + slot * S::kStage, bar = smem_u32(&sh.full[slot]);
+            const uint32_t sc = stage + 2 * S::kTileBytes + lane * scs;
+            const int scale_bytes = E4M3 ? min(scs, a.c.Bp - part * kTile) : 0;
+            if (mine && !good) {
+                set_status(a.status, UP_DEV_BAD_PAGE);
+                if constexpr (E4M3)                                     // codes of zero (out of the map's bounds), scale 1
+                    for (int b = 0; b < scs; b += 4) {
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + b), "r"(0x7f7f7f7fu) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + kScaleBytes + b), "r"(0x7f7f7f7fu) : "memory");
                     }
-                } else {
-                    for (int e = 0; e < E; ++e) {
-                        k[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.c.k + at)[lane * E + e] << 16);
-                        v[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.c.v + at)[lane * E + e] << 16);
+            }
+            const uint32_t bytes = __reduce_add_sync(0xffffffffu, (mine ? 2 * c.seg * S::kRowBytes : 0) + (good ? 2 * scale_bytes : 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (mine) {
+                const int at = good ? page : static_cast<int>(a.c.num_blocks);
+                const uint32_t dst = stage + lane * c.segp * S::kPanelBytes;
+#pragma unroll
+                for (int p = 0; p < S::kPanels; ++p) {
+                    tma_load_4d(dst + p * kTile * 128, kmap, bar, p * (E4M3 ? 128 : 64), part * kTile, head, at);
+                    tma_load_4d(dst + S::kTileBytes + p * kTile * 128, vmap, bar, p * (E4M3 ? 128 : 64), part * kTile, head, at);
+                }
+                if constexpr (E4M3) {
+                    const int64_t src = ((int64_t)page * a.c.Hkv + head) * a.c.Bp + part * kTile;
+                    if (good && UP_IN(src, a.c.scale_limit - scale_bytes + 1, a.status)) {
+                        bulk_load(sc, a.c.ks + src, scale_bytes, bar);
+                        bulk_load(sc + kScaleBytes, a.c.vs + src, scale_bytes, bar);
                     }
                 }
             }
-            float d = 0.f;
-            for (int e = 0; e < E; ++e) d += q[e] * k[e];
-            for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-            d *= a.scale2;
-            const float mn = fmaxf(m, d), c0 = weight(m, mn), p = weight(d, mn);
-            l = l * c0 + p;
-            for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + p * v[e];
-            m = mn;
-        }
-        __syncthreads();
-        if (lane == 0) {
-            sm_m[w] = m;
-            sm_l[w] = l;
-        }
-        for (int e = 0; e < E; ++e) sm_o[w][lane * E + e] = o[e];
-        __syncthreads();
-        const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-        float L = 0.f;
-        for (int i = 0; i < 4; ++i) L += weight(sm_m[i], M) * sm_l[i];
-        const int64_t part = ((int64_t)r * a.Hq + hq) * a.cut.max_splits + ch;
-        if (threadIdx.x == 0) a.part_lse[part] = M == -INFINITY && L == 0.f ? -INFINITY : M + log2f(L);
-        for (int d = threadIdx.x; d < DK; d += 128) {
-            float x = 0.f;
-            for (int i = 0; i < 4; ++i) x += weight(sm_m[i], M) * sm_o[i][d];
-            a.part_o[part * DK + d] = M == -INFINITY && L == 0.f ? 0.f : x / L;
+            ++issued;
+            if (++slot == S::kStages) slot = 0, phase ^= 1;
         }
     }
+    if (dead || sh.abort) {
+        // let the copies in flight land before the CTA goes (they write its shared memory)
+        const uint64_t t0 = globaltimer_ns();
+        const int64_t last = issued < S::kStages ? issued : S::kStages;
+        for (int64_t k = issued - last; k < issued; ++k)
+            while (!mbar_try_wait(smem_u32(&sh.full[k % S::kStages]), (k / S::kStages) & 1))
+                if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+    }
+}
+
+template <int DK, bool E4M3, int HT>
+__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3>::kStages>& sh,
+                        Walk w) {
+    using S = Shape<DK, E4M3>;
+    constexpr int KS = DK / 16, NT = DK / 8, QR = HT == 16 ? 4 : 2;
+    constexpr int PB = S::kPanelBytes;
+    constexpr int ROWS = HT / 8;                       // query heads of a thread: g, and g + 8
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const Cut& c = a.cut;
+    int slot = 0, qslot = 0;
+    uint32_t phase = 0, qphase = 0;
+    bool dead = false;
+
+    // the four keys whose scores this thread holds: tile rows 16 warp + {2t, 2t+1, 2t+8, 2t+9}, each in a
+    // segment of the tile at a token of it
+    int key_seg[4], key_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 16 * warp + 2 * t + (i & 1) + (i >> 1) * 8;
+        key_seg[i] = div_of(row, c.by_segp);
+        key_off[i] = row - key_seg[i] * c.segp;
+    }
+    const bool whole = c.spt * c.segp == kTile && c.segp == c.seg && (c.spp == 1 || c.B % kTile == 0);
+    const int scs = (c.seg + 15) & ~15;
+
+    for (; w.live(a); w.next(a)) {
+        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
+        const int heads = min(HT, a.group - h0);
+        // queries to registers: row g (and g + 8), the columns of the products' fragments
+        uint32_t qa[KS][QR];
+        float qf[ROWS];                                // factor of a row's scores
+        if (!dead && !mbar_wait(smem_u32(&sh.qfull[qslot]), qphase, &sh.abort)) dead = true;
+        const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            const uint32_t* row = qs + (g + 8 * h) * (DK / 2);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                // bf16: columns 16k + 2t, 16k + 2t + 8.  e4m3: 16k + 4t, 16k + 4t + 2 (the order of the key bytes)
+                qa[k][h] = E4M3 ? row[8 * k + 2 * t] : row[8 * k + t];
+                qa[k][h + ROWS] = E4M3 ? row[8 * k + 2 * t + 1] : row[8 * k + t + 4];
+            }
+            qf[h] = a.scale2;
+            if constexpr (E4M3) {
+                // e4m3 codes are exact in f16, and so are the queries once their largest is in [2^14, 2^15) (numbers
+                // 2^-29 and less of it lose bits far below an fp32 sum's)
+                uint32_t m = 0;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) m = __vmaxu2(m, __vmaxu2(qa[k][h] & 0x7fff7fffu, qa[k][h + ROWS] & 0x7fff7fffu));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);      // exponent field of the row's largest
+                const int up = min(268 - e, 253);                                    // 2^(up - 127) scales it
+                const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                qf[h] *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    qa[k][h] = f16x2(low_of(qa[k][h]) * f, high_of(qa[k][h]) * f);
+                    qa[k][h + ROWS] = f16x2(low_of(qa[k][h + ROWS]) * f, high_of(qa[k][h + ROWS]) * f);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.qempty[qslot]));
+        if (++qslot == 2) qslot = 0, qphase ^= 1;
+
+        float o[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        // running maximum of the scores (of the sums l) and, with scaled values, of score + the value's exponent
+        // (of the sums o): a token may have nearly all the weight and values 2^-100 of another's
+        float ms[ROWS], mt[ROWS], l[ROWS];
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            ms[h] = mt[h] = -INFINITY;
+            l[h] = 0.f;
+        }
+
+        const int n = w.tiles(), t0 = w.tile0();
+        int last_slot = 0;
+        for (int i = 0; i < n; ++i) {
+            if (!dead && !mbar_wait(smem_u32(&sh.full[slot]), phase, &sh.abort)) dead = true;
+            last_slot = slot;
+            if (!dead) {
+                const uint32_t kb = ring + slot * S::kStage, vb = kb + S::kTileBytes, sb = vb + S::kTileBytes;
+                // which of the four keys count
+                bool ok[4] = {true, true, true, true};
+                const bool masked = !whole || t0 + i == 0 || t0 + i == w.g.tiles - 1;
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int s = w.g.seg0 + (t0 + i) * c.spt + key_seg[j];
+                        const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + key_off[j];
+                        const int64_t pos = (int64_t)page * c.B + tok;
+                        ok[j] = key_seg[j] < c.spt && key_off[j] < c.seg && tok < c.B && pos >= w.g.lo && pos < w.g.len;
+                    }
+                }
+                // scores: 16 keys as two column tiles of 8
+                float s[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+                    const int row = 16 * warp + 8 * j + (lane & 7);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int k = 0; k < KS; k += 4) {
+                            uint32_t b[4];
+                            ldsm4(b, kb + swizzled<PB>(row, k + (lane >> 3)));
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                mma<true>(s[j], qa[k + x][0], HT == 16 ? qa[k + x][1] : 0u, qa[k + x][ROWS],
+                                          HT == 16 ? qa[k + x][QR - 1] : 0u, kv::e4m3x2_to_f16x2(b[x]),
+                                          kv::e4m3x2_to_f16x2(b[x] >> 16));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < KS; k += 2) {
+                            uint32_t b[4];
+                            ldsm4(b, kb + swizzled<PB>(row, 2 * k + (lane >> 3)));
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                mma<false>(s[j], qa[k + x][0], HT == 16 ? qa[k + x][1] : 0u, qa[k + x][ROWS],
+                                           HT == 16 ? qa[k + x][QR - 1] : 0u, b[2 * x], b[2 * x + 1]);
+                        }
+                    }
+                }
+                // p[h][key] = scores of row h in units of log2, te[key] the values' exponents
+                float p[ROWS][4], te[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float kf = 1.f;
+                    te[j] = 0.f;
+                    if constexpr (E4M3) {
+                        const uint32_t at = min(key_seg[j] * scs + key_off[j], kScaleBytes - 1);
+                        kf = __uint_as_float(max(lds_u8(sb + at) << 23, 0x00400000u));             // 2^(b - 127)
+                        te[j] = __uint_as_float(0x4b000000u | lds_u8(sb + kScaleBytes + at)) - 8388608.f - 127.f;
+                    }
+#pragma unroll
+                    for (int h = 0; h < ROWS; ++h) {
+                        const float x = s[j >> 1][2 * h + (j & 1)];
+                        p[h][j] = ok[j] ? (E4M3 ? x * kf * qf[h] : x * qf[h]) : -INFINITY;
+                    }
+                }
+                // move the references if a score passes them (all rows of the warp at once)
+                bool over = false;
+#pragma unroll
+                for (int h = 0; h < ROWS; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        over |= p[h][j] > ms[h] + kSlack;
+                        if constexpr (E4M3) over |= p[h][j] + te[j] > mt[h] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int h = 0; h < ROWS; ++h) {
+                        float x = fmaxf(fmaxf(p[h][0], p[h][1]), fmaxf(p[h][2], p[h][3]));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        const float ns = fmaxf(ms[h], x);
+                        l[h] *= weight(ms[h], ns);
+                        float f = weight(ms[h], ns);
+                        ms[h] = ns;
+                        if constexpr (E4M3) {
+                            float y = fmaxf(fmaxf(p[h][0] + te[0], p[h][1] + te[1]), fmaxf(p[h][2] + te[2], p[h][3] + te[3]));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                            const float nt = fmaxf(mt[h], y);
+                            f = weight(mt[h], nt);
+                            mt[h] = nt;
+                        }
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) {
+                            o[k][2 * h] *= f;
+                            o[k][2 * h + 1] *= f;
+                            if constexpr (!E4M3 && HT == 8) {
+                                o[k][2] *= f;
+                                o[k][3] *= f;
+                            }
+                        }
+                    }
+                }
+                // weights; a row without a score so far has the reference -inf: 0 stands in for it
+                uint32_t pa[4], lo[4];
+#pragma unroll
+                for (int h = 0; h < ROWS; ++h) {
+                    const float rs = ms[h] == -INFINITY ? 0.f : ms[h];
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[j] = ex2(p[h][j] - rs);
+                        l[h] += x[j];
+                    }
+                    if constexpr (E4M3) {
+                        const float rt = mt[h] == -INFINITY ? 0.f : mt[h];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = ex2(p[h][j] + te[j] - rt);
+                        // 11 bits of a weight: its one rounding before the sum
+                        pa[h] = f16x2(x[0], x[1]);
+                        pa[h + 2] = f16x2(x[2], x[3]);
+                    } else {
+                        // bf16 values want bf16 weights: high and low part, 16 bits together
+                        pa[h] = bf16x2(x[0], x[1]);
+                        pa[h + 2] = bf16x2(x[2], x[3]);
+                        lo[h] = bf16x2(x[0] - low_of(pa[h]), x[1] - high_of(pa[h]));
+                        lo[h + 2] = bf16x2(x[2] - low_of(pa[h + 2]), x[3] - high_of(pa[h + 2]));
+                    }
+                }
+                if constexpr (HT == 8) {
+                    pa[1] = E4M3 ? 0u : lo[0];
+                    pa[3] = E4M3 ? 0u : lo[2];
+                }
+                // values; a key that does not count is zero, whatever its row holds
+                const uint32_t z0 = (ok[0] ? 0xffffu : 0u) | (ok[1] ? 0xffff0000u : 0u);
+                const uint32_t z1 = (ok[2] ? 0xffffu : 0u) | (ok[3] ? 0xffff0000u : 0u);
+                const int vrow = 16 * warp + (lane & 15);
+                auto values = [&](auto with_mask) {
+                    constexpr bool M = decltype(with_mask)::value;
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int k = 0; k < DK / 16; k += 2) {
+                            uint32_t b[4];
+                            ldsm4t(b, vb + swizzled<PB>(vrow, k + (lane >> 4)));
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
+                                uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
+                                uint32_t e0 = kv::e4m3x2_to_f16x2(b0), e1 = kv::e4m3x2_to_f16x2(b1);
+                                uint32_t d0 = kv::e4m3x2_to_f16x2(b0 >> 16), d1 = kv::e4m3x2_to_f16x2(b1 >> 16);
+                                if constexpr (M) e0 &= z0, d0 &= z0, e1 &= z1, d1 &= z1;
+                                mma<true>(o[2 * (k + x)], pa[0], pa[1], pa[2], pa[3], e0, e1);
+                                mma<true>(o[2 * (k + x) + 1], pa[0], pa[1], pa[2], pa[3], d0, d1);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < NT; k += 2) {
+                            uint32_t b[4];
+                            ldsm4t(b, vb + swizzled<PB>(vrow, k + (lane >> 4)));
+                            if constexpr (M) b[0] &= z0, b[1] &= z1, b[2] &= z0, b[3] &= z1;
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                mma<false>(o[k + x], pa[0], pa[1], pa[2], pa[3], b[2 * x], b[2 * x + 1]);
+                                if constexpr (HT == 16) mma<false>(o[k + x], lo[0], lo[1], lo[2], lo[3], b[2 * x], b[2 * x + 1]);
+                            }
+                        }
+                    }
+                };
+                if (masked) values(std::true_type{}); else values(std::false_type{});
+            }
+            if (i + 1 < n) {                           // the last stage is kept for the join of the warps
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+            }
+            if (++slot == S::kStages) slot = 0, phase ^= 1;
+        }
+
+        // join the four warps: references and sums, then the outputs through the stage
+        constexpr int LD = DK + 8;                     // floats of a row: rows 32 bytes apart in the banks
+        float* scratch = reinterpret_cast<float*>(ring_ptr + last_slot * S::kStage);
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+        named_bar_sync(1, 32 * kWarps);                // every warp is done with the stage, and with sh.m of the last item
+        if (t == 0) {
+#pragma unroll
+            for (int h = 0; h < ROWS; ++h) {
+                sh.m[warp][g + 8 * h] = ms[h];
+                sh.f[warp][g + 8 * h] = E4M3 ? mt[h] : ms[h];
+                sh.l[warp][g + 8 * h] = l[h];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) {
+            if (h) named_bar_sync(1, 32 * kWarps);
+            float* row = scratch + (warp * 8 + g) * LD;
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    *reinterpret_cast<float4*>(row + 16 * k + 4 * t) =
+                        make_float4(o[2 * k][2 * h], o[2 * k + 1][2 * h], o[2 * k][2 * h + 1], o[2 * k + 1][2 * h + 1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    float x = o[k][2 * h], y = o[k][2 * h + 1];
+                    if constexpr (HT == 8) x += o[k][2], y += o[k][3];
+                    *reinterpret_cast<float2*>(row + 8 * k + 2 * t) = make_float2(x, y);
+                }
+            }
+            named_bar_sync(1, 32 * kWarps);
+            // 16 threads a head
+            const int hh = threadIdx.x >> 4, x = threadIdx.x & 15, hr = 8 * h + hh;
+            if (hr < heads) {
+                float M = sh.m[0][hr];
+#pragma unroll
+                for (int i = 1; i < kWarps; ++i) M = fmaxf(M, sh.m[i][hr]);
+                float L = 0.f, f[kWarps];
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    L += sh.l[i][hr] * weight(sh.m[i][hr], M);
+                    f[i] = weight(sh.f[i][hr], M);
+                }
+                // L = 0: no score above -inf.  NaN goes through.
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const int hq = head * a.group + h0 + hr;
+                const int64_t part = ((int64_t)w.r * a.Hq + hq) * c.max_splits + w.ch;
+                if (UP_IN(part, a.parts, a.status) && !dead) {
+                    if (x == 0) a.part_lse[part] = L == 0.f ? -INFINITY : M + log2f(L);
+#pragma unroll
+                    for (int d = 4 * x; d < DK; d += 64) {
+                        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < kWarps; ++i) {
+                            const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * LD + d);
+                            s.x += f[i] * y.x, s.y += f[i] * y.y, s.z += f[i] * y.z, s.w += f[i] * y.w;
+                        }
+                        *reinterpret_cast<float4*>(a.part_o + part * DK + d) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+                    }
+                }
+            }
+        }
+        fence_proxy_async_smem();                      // the stage's next content comes by the async proxy
+        __syncwarp();
+        if (lane == 0 && n > 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
+    }
+    if (dead && threadIdx.x == 0) set_status(a.status, UP_DEV_WAIT_TIMEOUT);
+}
+
+template <int DK, bool E4M3, int HT>
+__global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3>::kCtas))
+split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+             const __grid_constant__ Args a) {
+    using S = Shape<DK, E4M3>;
+    using C = Control<DK, HT, S::kStages>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    C& sh = *reinterpret_cast<C*>(base + S::kStages * S::kStage);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), kWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.qfull[i]), 1);
+            mbar_init(smem_u32(&sh.qempty[i]), kWarps);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    // rows of a head tile that no query fills
+    for (int i = threadIdx.x; i < HT * DK; i += kThreads) reinterpret_cast<uint32_t*>(sh.q)[i] = 0;
+    fence_proxy_async_smem();
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    Walk w;
+    find_run(a, w);
+    if (warp == kWarps)
+        produce<DK, E4M3, HT>(a, &kmap, &vmap, smem_u32(base), sh, w);
+    else
+        consume<DK, E4M3, HT>(a, smem_u32(base), base, sh, w);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -166,7 +773,8 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     pdl_trigger();
     const int hq = blockIdx.x, r = blockIdx.y;
     const int64_t row = (int64_t)r * a.Hq + hq;
-    const Range g = range_of(a.cut, a.seqused[r], (int64_t)a.max_blocks * a.cut.B);
+    const Range g = range_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B);
+    if (!UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
     const float* pl = a.part_lse + row * a.cut.max_splits;
     const float* po = a.part_o + row * a.cut.max_splits * DK;
     float m = -INFINITY;
@@ -177,9 +785,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
         float x = 0.f;
         for (int i = 0; i < g.splits; ++i) x += weight(pl[i], m) * po[(int64_t)i * DK + d];
         x = l == 0.f ? 0.f : x / l;
-        uint32_t b;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(0.f), "f"(x));
-        a.out[row * DK + d] = static_cast<uint16_t>(b);
+        a.out[row * DK + d] = static_cast<uint16_t>(bf16x2(x, 0.f) & 0xffffu);
     }
     if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -195,16 +801,67 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
     if ((int64_t)max_blocks * B > 0x7fffffff - 2 * kTile) return 0;
     c->B = B;
     c->seg = B < kTile ? B : kTile;
+    c->segp = (c->seg + 1) & ~1;               // 64-byte rows: a segment starts on a 128-byte boundary
     c->spp = static_cast<int>(cdiv(B, kTile));
-    c->spt = kTile / c->seg;
+    c->spt = kTile / c->segp;
     c->window = window;
-    int s0 = num_sms();
-    for (int h = Hkv; s0 % 2 == 0 && h % 2 == 0; h /= 2) s0 /= 2;
-    c->s0 = s0;
+    c->by_b = kv::fast_div(B);
+    c->by_spt = kv::fast_div(c->spt);
+    c->by_spp = kv::fast_div(c->spp);
+    c->by_segp = kv::fast_div(c->segp);
+    // the least number of chunks that makes one request's items a multiple of two CTAs on every SM
+    const int group = Hq / Hkv, units = Hkv * (group <= 8 ? 1 : static_cast<int>(cdiv(group, 16)));
+    int x = 2 * num_sms(), y = units;
+    while (y) {
+        const int z = x % y;
+        x = y;
+        y = z;
+    }
+    c->s0 = std::min(2 * num_sms() / x, kMaxSplits);
     int64_t segs = (int64_t)max_blocks * c->spp;
     if (window > 0) segs = std::min<int64_t>(segs, (cdiv(window, B) + 1) * (int64_t)c->spp);
-    c->max_splits = splits_of(static_cast<int>(cdiv(segs, c->spt)), s0);
+    const int tiles = static_cast<int>(cdiv(segs, c->spt));
+    c->max_splits = splits_of(tiles, c->s0);       // splits_of never falls as the tiles grow
     return 1;
+}
+
+static bool make_map(CUtensorMap* m, const uint8_t* ptr, const Cache& c, const Cut& cut, int dk, bool e4m3) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const int e = e4m3 ? 1 : 2, inner = std::min(dk, 128 / e);
+    cuuint64_t dims[4] = {(cuuint64_t)dk, (cuuint64_t)c.B, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks};
+    cuuint64_t strides[3] = {(cuuint64_t)c.st, (cuuint64_t)c.sh, (cuuint64_t)c.sb};
+    cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(ptr),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, bool E4M3, int HT>
+static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
+    constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    static_assert(Shape<DK, E4M3>::kStage >= 32 * (DK + 8) * 4, "the join of the warps fits a stage");
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (attr != cudaSuccess) return attr;
+    return launch_pdl(split_kernel<DK, E4M3, HT>, dim3(Shape<DK, E4M3>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
+}
+
+template <int DK>
+static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, bool e4m3, cudaStream_t st) {
+    cudaError_t e;
+    if (a.group <= 8)
+        e = e4m3 ? launch_split<DK, true, 8>(k, v, a, st) : launch_split<DK, false, 8>(k, v, a, st);
+    else
+        e = e4m3 ? launch_split<DK, true, 16>(k, v, a, st) : launch_split<DK, false, 16>(k, v, a, st);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(join_kernel<DK>, dim3(a.Hq, a.R), dim3(128), 0, st, a);
 }
 
 }  // namespace decode
@@ -231,10 +888,10 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     if (R <= 0 || max_blocks <= 0 || Hq <= 0 || window < 0 || !(sm_scale > -INFINITY && sm_scale < INFINITY)) return UP_ERR_ARG;
     if (!make_cut(R, Hq, cache->Hkv, cache->dk, cache->B, max_blocks, window, &a.cut)) return UP_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(out) || q_stride % 8 || (R > 1 && q_stride < (int64_t)Hq * cache->dk)) return UP_ERR_SHAPE;
-    if (ws_bytes < up_paged_decode_workspace_bytes(R, Hq, cache->Hkv, cache->dk, cache->B, max_blocks, window) ||
-        !aligned16(ws))
-        return UP_ERR_WORKSPACE;
     const size_t parts = static_cast<size_t>(R) * Hq * a.cut.max_splits;
+    const size_t lse_bytes = align_up(parts * sizeof(float), 256);
+    if (ws_bytes < lse_bytes + parts * cache->dk * sizeof(float) || !aligned16(ws)) return UP_ERR_WORKSPACE;
+    const bool e4m3 = cache->format == UP_KV_E4M3;
     a.q = reinterpret_cast<const uint8_t*>(q);
     a.q_stride = q_stride * 2;
     a.table = block_table;
@@ -243,28 +900,26 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     a.max_blocks = max_blocks;
     a.Hq = Hq;
     a.group = Hq / cache->Hkv;
+    a.head_tiles = a.group <= 8 ? 1 : static_cast<int>(cdiv(a.group, 16));
     a.scale2 = sm_scale * kLog2e;
     a.part_lse = static_cast<float*>(ws);
-    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(parts * sizeof(float), 256));
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + lse_bytes);
+    a.parts = static_cast<int64_t>(parts);
     a.out = out;
     a.lse = lse;
     a.status = dev_status;
+    CUtensorMap km, vm;
+    if (!encode_tiled_fn()) return UP_ERR_CUDA;
+    if (!make_map(&km, a.c.k, a.c, a.cut, cache->dk, e4m3) || !make_map(&vm, a.c.v, a.c, a.cut, cache->dk, e4m3))
+        return UP_ERR_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 g(a.cut.max_splits, cache->Hkv, R), gj(Hq, R), b(128);
-    const bool f8 = cache->format == UP_KV_E4M3;
     cudaError_t e = cudaErrorInvalidValue;
-#define UP_DECODE_CASE(DK)                                                                                   \
-    case DK:                                                                                                 \
-        e = f8 ? launch_pdl(chunk_kernel<DK, true>, g, b, 0, st, a) : launch_pdl(chunk_kernel<DK, false>, g, b, 0, st, a); \
-        if (e == cudaSuccess) e = launch_pdl(join_kernel<DK>, gj, b, 0, st, a);                              \
-        break
     switch (cache->dk) {
-        UP_DECODE_CASE(64);
-        UP_DECODE_CASE(128);
-        UP_DECODE_CASE(256);
+        case 64: e = launch<64>(km, vm, a, e4m3, st); break;
+        case 128: e = launch<128>(km, vm, a, e4m3, st); break;
+        case 256: e = launch<256>(km, vm, a, e4m3, st); break;
         default: return UP_ERR_SHAPE;
     }
-#undef UP_DECODE_CASE
     if (e != cudaSuccess) return UP_ERR_CUDA;
     count_launch(2);
     return check_launch();

@@ -50,8 +50,11 @@ inline up_status check(const up_kv_cache* c, Cache* out) {
     if (c->dk != 64 && c->dk != 128 && c->dk != 256) return UP_ERR_SHAPE;
     const int e = element_bytes(c->format);
     if (!aligned16(c->k) || !aligned16(c->v)) return UP_ERR_SHAPE;
-    if (c->stride_block < 0 || c->stride_head < 0 || c->stride_token < 0) return UP_ERR_SHAPE;
-    if (c->stride_block * e % 16 || c->stride_head * e % 16 || c->stride_token * e % 16) return UP_ERR_SHAPE;
+    // the stride of an axis of one entry is never used
+    const int64_t stride[3] = {c->num_blocks > 1 ? c->stride_block : 16, c->Hkv > 1 ? c->stride_head : 16,
+                               c->B > 1 ? c->stride_token : 16};
+    for (int64_t s : stride)
+        if (s <= 0 || s * e % 16) return UP_ERR_SHAPE;
     if (c->format == UP_KV_E4M3) {
         if (!c->k_scale || !c->v_scale) return UP_ERR_ARG;
         if (!aligned16(c->k_scale) || !aligned16(c->v_scale)) return UP_ERR_SHAPE;
@@ -61,9 +64,9 @@ inline up_status check(const up_kv_cache* c, Cache* out) {
     out->ks = c->k_scale;
     out->vs = c->v_scale;
     out->num_blocks = c->num_blocks;
-    out->sb = c->stride_block * e;
-    out->sh = c->stride_head * e;
-    out->st = c->stride_token * e;
+    out->sb = stride[0] * e;
+    out->sh = stride[1] * e;
+    out->st = stride[2] * e;
     out->Hkv = c->Hkv;
     out->B = c->B;
     out->Bp = scale_row(c->B);
