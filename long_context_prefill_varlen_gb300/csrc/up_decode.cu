@@ -18,9 +18,11 @@
 //    runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
 //    running maximum and sums, joined through the last stage when the item ends.
-// The products are m16n8k16 (rows: query heads; a group below 16 leaves rows empty, which the bf16 form uses
-// for the low halves of the weights).  A matrix unit with larger tiles has nothing to win here: 16 rows of
-// queries are all there is, and the copies take four times as long as these products.
+// The products are m16n8k16 with the long side of each in the 16 rows: scores = keys x queries (16 keys, 8
+// heads), outputs = values transposed x weights transposed (16 columns, 8 heads), so that a group of up to 8
+// heads, and a second tile of 8 above that, leaves little of them empty.  The scores' own layout, transposed
+// in the registers, is the weights' operand.  A matrix unit with larger tiles has nothing to win here: 8 or
+// 16 queries are all there is to multiply with.
 #include <stdint.h>
 
 #include <algorithm>
@@ -201,15 +203,16 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
 // ------------------------------------------------------------------------------------------------
 // tiles in shared memory
 
-template <int DK, bool E4M3>
+template <int DK, bool E4M3, int HT>
 struct Shape {
     static constexpr int kRowBytes = DK * (E4M3 ? 1 : 2);
     static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;      // a tile is panels of rows
     static constexpr int kPanels = kRowBytes / kPanelBytes;
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
-    // two CTAs on an SM where three stages each fit (228 KB an SM, 1 KB of it per CTA reserved)
-    static constexpr int kCtas = 3 * kStage <= 112 * 1024 ? 2 : 1;
+    // two CTAs on an SM where three stages each fit (228 KB an SM, 1 KB of it per CTA reserved) and the sums
+    // of 16 heads leave registers for it
+    static constexpr int kCtas = 3 * kStage <= 112 * 1024 && !(DK == 256 && HT == 16) ? 2 : 1;
     static constexpr int kFit = (kCtas == 2 ? 112 * 1024 : 224 * 1024) / kStage;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
 };
@@ -268,10 +271,11 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+// an 8 x 8 matrix of halves, a row per four lanes, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -285,9 +289,12 @@ struct Control {
     int abort;
 };
 
+template <int DK>
+constexpr int kLd = DK + 4;      // floats of a row in the join of the warps: heads 2t, 2t + 1 of four lanes fall 8 banks apart
+
 template <int DK, bool E4M3, int HT>
 struct Sizes {
-    using S = Shape<DK, E4M3>;
+    using S = Shape<DK, E4M3, HT>;
     static constexpr int kSmem = S::kStages * S::kStage + static_cast<int>(sizeof(Control<DK, HT, S::kStages>)) + 1024;
 };
 
@@ -295,8 +302,8 @@ struct Sizes {
 
 template <int DK, bool E4M3, int HT>
 __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
-                        Control<DK, HT, Shape<DK, E4M3>::kStages>& sh, Walk w) {
-    using S = Shape<DK, E4M3>;
+                        Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh, Walk w) {
+    using S = Shape<DK, E4M3, HT>;
     const int lane = threadIdx.x & 31;
     const Cut& c = a.cut;
     int slot = 0, qslot = 0;
@@ -398,64 +405,66 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
 }
 
 template <int DK, bool E4M3, int HT>
-__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3>::kStages>& sh,
+__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh,
                         Walk w) {
-    using S = Shape<DK, E4M3>;
-    constexpr int KS = DK / 16, NT = DK / 8, QR = HT == 16 ? 4 : 2;
+    using S = Shape<DK, E4M3, HT>;
+    constexpr int KS = DK / 16, NH = HT / 8;           // steps of 16 columns; tiles of 8 query heads
     constexpr int PB = S::kPanelBytes;
-    constexpr int ROWS = HT / 8;                       // query heads of a thread: g, and g + 8
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const Cut& c = a.cut;
     int slot = 0, qslot = 0;
     uint32_t phase = 0, qphase = 0;
     bool dead = false;
 
-    // the four keys whose scores this thread holds: tile rows 16 warp + {2t, 2t+1, 2t+8, 2t+9}, each in a
-    // segment of the tile at a token of it
-    int key_seg[4], key_off[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 16 * warp + 2 * t + (i & 1) + (i >> 1) * 8;
-        key_seg[i] = div_of(row, c.by_segp);
-        key_off[i] = row - key_seg[i] * c.segp;
-    }
+    // tile row 16 warp + (lane & 15): its segment of the tile and its token there
+    const int my_row = 16 * warp + (lane & 15);
+    const int my_seg = div_of(my_row, c.by_segp), my_off = my_row - my_seg * c.segp;
     const bool whole = c.spt * c.segp == kTile && c.segp == c.seg && (c.spp == 1 || c.B % kTile == 0);
     const int scs = (c.seg + 15) & ~15;
+    // scale bytes of the keys g and g + 8 of the warp
+    uint32_t sc_at[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int row = 16 * warp + g + 8 * j, s = div_of(row, c.by_segp);
+        sc_at[j] = min(s * scs + row - s * c.segp, kScaleBytes - 1);
+    }
 
     for (; w.live(a); w.next(a)) {
         const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
         const int heads = min(HT, a.group - h0);
-        // queries to registers: row g (and g + 8), the columns of the products' fragments
-        uint32_t qa[KS][QR];
-        float qf[ROWS];                                // factor of a row's scores
+        // queries to registers, as the products' second operand: head g (of each tile of 8), columns
+        // 16k + {2t, 2t+1, 2t+8, 2t+9}; for e4m3 16k + 4t .. 4t+3, the order that the key bytes come in
+        uint32_t qb[NH][KS][2];
+        float qf[NH][2];                               // factors of the scores of heads 2t, 2t + 1
         if (!dead && !mbar_wait(smem_u32(&sh.qfull[qslot]), qphase, &sh.abort)) dead = true;
         const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
 #pragma unroll
-        for (int h = 0; h < ROWS; ++h) {
+        for (int h = 0; h < NH; ++h) {
             const uint32_t* row = qs + (g + 8 * h) * (DK / 2);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                // bf16: columns 16k + 2t, 16k + 2t + 8.  e4m3: 16k + 4t, 16k + 4t + 2 (the order of the key bytes)
-                qa[k][h] = E4M3 ? row[8 * k + 2 * t] : row[8 * k + t];
-                qa[k][h + ROWS] = E4M3 ? row[8 * k + 2 * t + 1] : row[8 * k + t + 4];
+                qb[h][k][0] = E4M3 ? row[8 * k + 2 * t] : row[8 * k + t];
+                qb[h][k][1] = E4M3 ? row[8 * k + 2 * t + 1] : row[8 * k + t + 4];
             }
-            qf[h] = a.scale2;
+            qf[h][0] = qf[h][1] = a.scale2;
             if constexpr (E4M3) {
                 // e4m3 codes are exact in f16, and so are the queries once their largest is in [2^14, 2^15) (numbers
                 // 2^-29 and less of it lose bits far below an fp32 sum's)
                 uint32_t m = 0;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) m = __vmaxu2(m, __vmaxu2(qa[k][h] & 0x7fff7fffu, qa[k][h + ROWS] & 0x7fff7fffu));
+                for (int k = 0; k < KS; ++k) m = __vmaxu2(m, __vmaxu2(qb[h][k][0] & 0x7fff7fffu, qb[h][k][1] & 0x7fff7fffu));
                 m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);      // exponent field of the row's largest
+                const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);      // exponent field of the head's largest
                 const int up = min(268 - e, 253);                                    // 2^(up - 127) scales it
                 const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
-                qf[h] *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+                const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+                qf[h][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
+                qf[h][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    qa[k][h] = f16x2(low_of(qa[k][h]) * f, high_of(qa[k][h]) * f);
-                    qa[k][h + ROWS] = f16x2(low_of(qa[k][h + ROWS]) * f, high_of(qa[k][h + ROWS]) * f);
+                    qb[h][k][0] = f16x2(low_of(qb[h][k][0]) * f, high_of(qb[h][k][0]) * f);
+                    qb[h][k][1] = f16x2(low_of(qb[h][k][1]) * f, high_of(qb[h][k][1]) * f);
                 }
             }
         }
@@ -463,16 +472,21 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         if (lane == 0) mbar_arrive(smem_u32(&sh.qempty[qslot]));
         if (++qslot == 2) qslot = 0, qphase ^= 1;
 
-        float o[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
+        // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
+        float o[NH][KS][4];
         // running maximum of the scores (of the sums l) and, with scaled values, of score + the value's exponent
         // (of the sums o): a token may have nearly all the weight and values 2^-100 of another's
-        float ms[ROWS], mt[ROWS], l[ROWS];
+        float ms[NH][2], mt[NH][2], l[NH][2];
 #pragma unroll
-        for (int h = 0; h < ROWS; ++h) {
-            ms[h] = mt[h] = -INFINITY;
-            l[h] = 0.f;
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) o[h][k][0] = o[h][k][1] = o[h][k][2] = o[h][k][3] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ms[h][x] = mt[h][x] = -INFINITY;
+                l[h][x] = 0.f;
+            }
         }
 
         const int n = w.tiles(), t0 = w.tile0();
@@ -482,164 +496,159 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             last_slot = slot;
             if (!dead) {
                 const uint32_t kb = ring + slot * S::kStage, vb = kb + S::kTileBytes, sb = vb + S::kTileBytes;
-                // which of the four keys count
-                bool ok[4] = {true, true, true, true};
+                // bit i: the warp's i-th key counts
+                uint32_t counts = 0xffffu;
                 const bool masked = !whole || t0 + i == 0 || t0 + i == w.g.tiles - 1;
                 if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int s = w.g.seg0 + (t0 + i) * c.spt + key_seg[j];
-                        const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + key_off[j];
-                        const int64_t pos = (int64_t)page * c.B + tok;
-                        ok[j] = key_seg[j] < c.spt && key_off[j] < c.seg && tok < c.B && pos >= w.g.lo && pos < w.g.len;
-                    }
+                    const int s = w.g.seg0 + (t0 + i) * c.spt + my_seg;
+                    const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + my_off;
+                    const int64_t pos = (int64_t)page * c.B + tok;
+                    counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= w.g.lo &&
+                                                            pos < w.g.len);
                 }
-                // scores: 16 keys as two column tiles of 8
-                float s[2][4];
+                // scores, keys in the rows: s[h] = (key g: heads 2t, 2t + 1; key g + 8: the same), in two parts so
+                // that a product need not wait for the one before
+                float s[NH][2][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-                    const int row = 16 * warp + 8 * j + (lane & 7);
-                    if constexpr (E4M3) {
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                        for (int k = 0; k < KS; k += 4) {
-                            uint32_t b[4];
-                            ldsm4(b, kb + swizzled<PB>(row, k + (lane >> 3)));
+                    for (int x = 0; x < 4; ++x) s[h][0][x] = s[h][1][x] = 0.f;
+                const int arow = 16 * warp + (lane & 15);
+                if constexpr (E4M3) {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                mma<true>(s[j], qa[k + x][0], HT == 16 ? qa[k + x][1] : 0u, qa[k + x][ROWS],
-                                          HT == 16 ? qa[k + x][QR - 1] : 0u, kv::e4m3x2_to_f16x2(b[x]),
-                                          kv::e4m3x2_to_f16x2(b[x] >> 16));
-                        }
-                    } else {
+                    for (int k = 0; k < KS; k += 2) {
+                        uint32_t b[4];                 // (keys 0-7, 8-15) of 16 bytes, then of the next 16
+                        ldsm4(b, kb + swizzled<PB>(arow, k + (lane >> 4)));
 #pragma unroll
-                        for (int k = 0; k < KS; k += 2) {
-                            uint32_t b[4];
-                            ldsm4(b, kb + swizzled<PB>(row, 2 * k + (lane >> 3)));
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t a0 = kv::e4m3x2_to_f16x2(b[2 * x]), a2 = kv::e4m3x2_to_f16x2(b[2 * x] >> 16);
+                            const uint32_t a1 = kv::e4m3x2_to_f16x2(b[2 * x + 1]), a3 = kv::e4m3x2_to_f16x2(b[2 * x + 1] >> 16);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                mma<false>(s[j], qa[k + x][0], HT == 16 ? qa[k + x][1] : 0u, qa[k + x][ROWS],
-                                           HT == 16 ? qa[k + x][QR - 1] : 0u, b[2 * x], b[2 * x + 1]);
+                            for (int h = 0; h < NH; ++h) mma<true>(s[h][x], a0, a1, a2, a3, qb[h][k + x][0], qb[h][k + x][1]);
                         }
                     }
-                }
-                // p[h][key] = scores of row h in units of log2, te[key] the values' exponents
-                float p[ROWS][4], te[4];
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float kf = 1.f;
-                    te[j] = 0.f;
-                    if constexpr (E4M3) {
-                        const uint32_t at = min(key_seg[j] * scs + key_off[j], kScaleBytes - 1);
-                        kf = __uint_as_float(max(lds_u8(sb + at) << 23, 0x00400000u));             // 2^(b - 127)
-                        te[j] = __uint_as_float(0x4b000000u | lds_u8(sb + kScaleBytes + at)) - 8388608.f - 127.f;
-                    }
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t b[4];                 // (keys 0-7, 8-15) of 8 columns, then of the next 8
+                        ldsm4(b, kb + swizzled<PB>(arow, 2 * k + (lane >> 4)));
 #pragma unroll
-                    for (int h = 0; h < ROWS; ++h) {
-                        const float x = s[j >> 1][2 * h + (j & 1)];
-                        p[h][j] = ok[j] ? (E4M3 ? x * kf * qf[h] : x * qf[h]) : -INFINITY;
+                        for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
                     }
                 }
-                // move the references if a score passes them (all rows of the warp at once)
+                float kf[2] = {1.f, 1.f}, te[2] = {0.f, 0.f};      // of keys g, g + 8: scale of the keys, exponent of the values
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        kf[j] = __uint_as_float(max(lds_u8(sb + sc_at[j]) << 23, 0x00400000u));    // 2^(b - 127)
+                        te[j] = __uint_as_float(0x4b000000u | lds_u8(sb + kScaleBytes + sc_at[j])) - 8388608.f - 127.f;
+                    }
+                }
+                const bool ok[2] = {((counts >> g) & 1) != 0, ((counts >> (g + 8)) & 1) != 0};
+                // p[h][j][x]: log2-score of key g + 8j and head 2t + x
+                float p[NH][2][2];
                 bool over = false;
 #pragma unroll
-                for (int h = 0; h < ROWS; ++h)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        over |= p[h][j] > ms[h] + kSlack;
-                        if constexpr (E4M3) over |= p[h][j] + te[j] > mt[h] + kSlack;
-                    }
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float y = s[h][0][2 * j + x] + s[h][1][2 * j + x];
+                            p[h][j][x] = ok[j] ? (E4M3 ? y * kf[j] * qf[h][x] : y * qf[h][x]) : -INFINITY;
+                            over |= p[h][j][x] > ms[h][x] + kSlack;
+                            if constexpr (E4M3) over |= p[h][j][x] + te[j] > mt[h][x] + kSlack;
+                        }
+                // move the references if a score passes them (all of the warp at once)
                 if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-                    for (int h = 0; h < ROWS; ++h) {
-                        float x = fmaxf(fmaxf(p[h][0], p[h][1]), fmaxf(p[h][2], p[h][3]));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        const float ns = fmaxf(ms[h], x);
-                        l[h] *= weight(ms[h], ns);
-                        float f = weight(ms[h], ns);
-                        ms[h] = ns;
-                        if constexpr (E4M3) {
-                            float y = fmaxf(fmaxf(p[h][0] + te[0], p[h][1] + te[1]), fmaxf(p[h][2] + te[2], p[h][3] + te[3]));
-                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-                            const float nt = fmaxf(mt[h], y);
-                            f = weight(mt[h], nt);
-                            mt[h] = nt;
-                        }
+                    for (int h = 0; h < NH; ++h)
 #pragma unroll
-                        for (int k = 0; k < NT; ++k) {
-                            o[k][2 * h] *= f;
-                            o[k][2 * h + 1] *= f;
-                            if constexpr (!E4M3 && HT == 8) {
-                                o[k][2] *= f;
-                                o[k][3] *= f;
+                        for (int x = 0; x < 2; ++x) {
+                            float y = fmaxf(p[h][0][x], p[h][1][x]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                            const float ns = fmaxf(ms[h][x], y);
+                            float f = weight(ms[h][x], ns);
+                            l[h][x] *= f;
+                            ms[h][x] = ns;
+                            if constexpr (E4M3) {
+                                y = fmaxf(p[h][0][x] + te[0], p[h][1][x] + te[1]);
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                                const float nt = fmaxf(mt[h][x], y);
+                                f = weight(mt[h][x], nt);
+                                mt[h][x] = nt;
+                            }
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) {
+                                o[h][k][x] *= f;
+                                o[h][k][2 + x] *= f;
                             }
                         }
+                }
+                // weights, transposed to the second operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of head g); a head without
+                // a score so far has the reference -inf: 0 stands in for it
+                uint32_t pb[NH][2], lo[NH][2];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    float y[2][2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float rs = ms[h][x] == -INFINITY ? 0.f : ms[h][x];
+                        y[0][x] = ex2(p[h][0][x] - rs);
+                        y[1][x] = ex2(p[h][1][x] - rs);
+                        l[h][x] += y[0][x] + y[1][x];
+                        if constexpr (E4M3) {
+                            const float rt = mt[h][x] == -INFINITY ? 0.f : mt[h][x];
+                            y[0][x] = ex2(p[h][0][x] + te[0] - rt);
+                            y[1][x] = ex2(p[h][1][x] + te[1] - rt);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if constexpr (E4M3) {
+                            pb[h][j] = transposed(f16x2(y[j][0], y[j][1]));        // 11 bits: a weight's one rounding
+                        } else {
+                            // bf16 values want bf16 weights: high and low part, 16 bits together
+                            const uint32_t hi = bf16x2(y[j][0], y[j][1]);
+                            pb[h][j] = transposed(hi);
+                            lo[h][j] = transposed(bf16x2(y[j][0] - low_of(hi), y[j][1] - high_of(hi)));
+                        }
                     }
                 }
-                // weights; a row without a score so far has the reference -inf: 0 stands in for it
-                uint32_t pa[4], lo[4];
-#pragma unroll
-                for (int h = 0; h < ROWS; ++h) {
-                    const float rs = ms[h] == -INFINITY ? 0.f : ms[h];
-                    float x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[j] = ex2(p[h][j] - rs);
-                        l[h] += x[j];
-                    }
-                    if constexpr (E4M3) {
-                        const float rt = mt[h] == -INFINITY ? 0.f : mt[h];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = ex2(p[h][j] + te[j] - rt);
-                        // 11 bits of a weight: its one rounding before the sum
-                        pa[h] = f16x2(x[0], x[1]);
-                        pa[h + 2] = f16x2(x[2], x[3]);
-                    } else {
-                        // bf16 values want bf16 weights: high and low part, 16 bits together
-                        pa[h] = bf16x2(x[0], x[1]);
-                        pa[h + 2] = bf16x2(x[2], x[3]);
-                        lo[h] = bf16x2(x[0] - low_of(pa[h]), x[1] - high_of(pa[h]));
-                        lo[h + 2] = bf16x2(x[2] - low_of(pa[h + 2]), x[3] - high_of(pa[h + 2]));
-                    }
-                }
-                if constexpr (HT == 8) {
-                    pa[1] = E4M3 ? 0u : lo[0];
-                    pa[3] = E4M3 ? 0u : lo[2];
-                }
-                // values; a key that does not count is zero, whatever its row holds
-                const uint32_t z0 = (ok[0] ? 0xffffu : 0u) | (ok[1] ? 0xffff0000u : 0u);
-                const uint32_t z1 = (ok[2] ? 0xffffu : 0u) | (ok[3] ? 0xffff0000u : 0u);
-                const int vrow = 16 * warp + (lane & 15);
+                // values, columns in the rows; a key that does not count is zero, whatever its row holds
+                const uint32_t c0 = counts >> (2 * t), c1 = counts >> (2 * t + 8);
+                const uint32_t z0 = (c0 & 1 ? 0xffffu : 0u) | (c0 & 2 ? 0xffff0000u : 0u);
+                const uint32_t z1 = (c1 & 1 ? 0xffffu : 0u) | (c1 & 2 ? 0xffff0000u : 0u);
                 auto values = [&](auto with_mask) {
                     constexpr bool M = decltype(with_mask)::value;
                     if constexpr (E4M3) {
 #pragma unroll
-                        for (int k = 0; k < DK / 16; k += 2) {
-                            uint32_t b[4];
-                            ldsm4t(b, vb + swizzled<PB>(vrow, k + (lane >> 4)));
+                        for (int k = 0; k < KS; k += 2) {
+                            uint32_t b[4];             // (keys 0-7, 8-15) of 16 bytes, then of the next 16
+                            ldsm4t(b, vb + swizzled<PB>(16 * warp + (lane & 15), k + (lane >> 4)));
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
-                                uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
+                                const uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
                                 uint32_t e0 = kv::e4m3x2_to_f16x2(b0), e1 = kv::e4m3x2_to_f16x2(b1);
                                 uint32_t d0 = kv::e4m3x2_to_f16x2(b0 >> 16), d1 = kv::e4m3x2_to_f16x2(b1 >> 16);
                                 if constexpr (M) e0 &= z0, d0 &= z0, e1 &= z1, d1 &= z1;
-                                mma<true>(o[2 * (k + x)], pa[0], pa[1], pa[2], pa[3], e0, e1);
-                                mma<true>(o[2 * (k + x) + 1], pa[0], pa[1], pa[2], pa[3], d0, d1);
+#pragma unroll
+                                for (int h = 0; h < NH; ++h) mma<true>(o[h][k + x], e0, d0, e1, d1, pb[h][0], pb[h][1]);
                             }
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < NT; k += 2) {
-                            uint32_t b[4];
-                            ldsm4t(b, vb + swizzled<PB>(vrow, k + (lane >> 4)));
-                            if constexpr (M) b[0] &= z0, b[1] &= z1, b[2] &= z0, b[3] &= z1;
+                        for (int k = 0; k < KS; ++k) {
+                            uint32_t b[4];             // keys 0-7 of 8 columns and the next 8, then keys 8-15
+                            ldsm4t(b, vb + swizzled<PB>(16 * warp + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                            if constexpr (M) b[0] &= z0, b[1] &= z0, b[2] &= z1, b[3] &= z1;
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                mma<false>(o[k + x], pa[0], pa[1], pa[2], pa[3], b[2 * x], b[2 * x + 1]);
-                                if constexpr (HT == 16) mma<false>(o[k + x], lo[0], lo[1], lo[2], lo[3], b[2 * x], b[2 * x + 1]);
+                            for (int h = 0; h < NH; ++h) {
+                                mma<false>(o[h][k], b[0], b[1], b[2], b[3], pb[h][0], pb[h][1]);
+                                mma<false>(o[h][k], b[0], b[1], b[2], b[3], lo[h][0], lo[h][1]);
                             }
                         }
                     }
@@ -654,37 +663,38 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         }
 
         // join the four warps: references and sums, then the outputs through the stage
-        constexpr int LD = DK + 8;                     // floats of a row: rows 32 bytes apart in the banks
         float* scratch = reinterpret_cast<float*>(ring_ptr + last_slot * S::kStage);
 #pragma unroll
-        for (int h = 0; h < ROWS; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[h][x] += __shfl_xor_sync(0xffffffffu, l[h][x], d);
         named_bar_sync(1, 32 * kWarps);                // every warp is done with the stage, and with sh.m of the last item
-        if (t == 0) {
+        if (g == 0) {
 #pragma unroll
-            for (int h = 0; h < ROWS; ++h) {
-                sh.m[warp][g + 8 * h] = ms[h];
-                sh.f[warp][g + 8 * h] = E4M3 ? mt[h] : ms[h];
-                sh.l[warp][g + 8 * h] = l[h];
-            }
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    sh.m[warp][8 * h + 2 * t + x] = ms[h][x];
+                    sh.f[warp][8 * h + 2 * t + x] = E4M3 ? mt[h][x] : ms[h][x];
+                    sh.l[warp][8 * h + 2 * t + x] = l[h][x];
+                }
         }
 #pragma unroll
-        for (int h = 0; h < ROWS; ++h) {
+        for (int h = 0; h < NH; ++h) {
             if (h) named_bar_sync(1, 32 * kWarps);
-            float* row = scratch + (warp * 8 + g) * LD;
-            if constexpr (E4M3) {
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    *reinterpret_cast<float4*>(row + 16 * k + 4 * t) =
-                        make_float4(o[2 * k][2 * h], o[2 * k + 1][2 * h], o[2 * k][2 * h + 1], o[2 * k + 1][2 * h + 1]);
-            } else {
+            for (int x = 0; x < 2; ++x) {
+                float* row = scratch + (warp * 8 + 2 * t + x) * kLd<DK>;
 #pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    float x = o[k][2 * h], y = o[k][2 * h + 1];
-                    if constexpr (HT == 8) x += o[k][2], y += o[k][3];
-                    *reinterpret_cast<float2*>(row + 8 * k + 2 * t) = make_float2(x, y);
+                for (int k = 0; k < KS; ++k) {
+                    if constexpr (E4M3) {
+                        *reinterpret_cast<float2*>(row + 16 * k + 2 * g) = make_float2(o[h][k][x], o[h][k][2 + x]);
+                    } else {
+                        row[16 * k + g] = o[h][k][x];
+                        row[16 * k + g + 8] = o[h][k][2 + x];
+                    }
                 }
             }
             named_bar_sync(1, 32 * kWarps);
@@ -711,7 +721,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int i = 0; i < kWarps; ++i) {
-                            const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * LD + d);
+                            const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * kLd<DK> + d);
                             s.x += f[i] * y.x, s.y += f[i] * y.y, s.z += f[i] * y.z, s.w += f[i] * y.w;
                         }
                         *reinterpret_cast<float4*>(a.part_o + part * DK + d) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
@@ -727,10 +737,10 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 }
 
 template <int DK, bool E4M3, int HT>
-__global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3>::kCtas))
+__global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, HT>::kCtas))
 split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
              const __grid_constant__ Args a) {
-    using S = Shape<DK, E4M3>;
+    using S = Shape<DK, E4M3, HT>;
     using C = Control<DK, HT, S::kStages>;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -843,14 +853,14 @@ template <int DK, bool E4M3, int HT>
 static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
     constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    static_assert(Shape<DK, E4M3>::kStage >= 32 * (DK + 8) * 4, "the join of the warps fits a stage");
+    static_assert(Shape<DK, E4M3, HT>::kStage >= 32 * kLd<DK> * 4, "the join of the warps fits a stage");
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
         attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (attr != cudaSuccess) return attr;
-    return launch_pdl(split_kernel<DK, E4M3, HT>, dim3(Shape<DK, E4M3>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
+    return launch_pdl(split_kernel<DK, E4M3, HT>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
 }
 
 template <int DK>
