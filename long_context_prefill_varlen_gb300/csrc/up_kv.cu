@@ -10,8 +10,10 @@
 // round on both sides and take four bytes instead of one.
 //
 // Both kernels only move bytes (write: 2 dk in, dk + 1 or 2 dk out per row; read: the reverse): HBM-bound.  A
-// row belongs to dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that a row's maximum is a few
-// shuffles and every access is a whole run; each lane has kUnroll rows in flight.
+// warp takes units of kChunk tokens of one head: one coalesced load brings their slots, each lane places one
+// token, and the tokens' scale bytes, neighbours in a page, leave (or come) in one access.  A row belongs to
+// dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that its maximum is a few shuffles; the warps of a CTA
+// take the heads of the same tokens, so that they read or write whole tokens of the stream together.
 #include <stdint.h>
 
 #include <algorithm>
@@ -22,7 +24,9 @@ namespace up {
 namespace kv {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kChunk = 32;           // tokens of a warp's unit
+constexpr int kGridPerSm = 16;      // CTAs of a side
+constexpr int kUnroll = 8;           // rows (or groups of rows) in flight
 
 struct Side {              // keys or values of a call
     const uint8_t* src;    // write: the stream; read: the cache
@@ -93,70 +97,86 @@ __device__ __forceinline__ uint32_t finite_or(uint32_t w, uint32_t other) {
     return lo | hi;
 }
 
+// The tokens of a unit: lane i holds where token i's row lies (element bytes and scale byte of head 0), -1 for none.
+struct Place {
+    int64_t row, scale;
+};
+
+__device__ __forceinline__ Place place_of(const Args& a, int64_t t, int64_t n) {
+    Place p{-1, -1};
+    int64_t page;
+    int tok;
+    if (t < n && UP_IN(t, a.T, a.status) && place(a, a.slots[t], &page, &tok)) {
+        p.row = page * a.c.sb + tok * a.c.st;
+        p.scale = page * a.c.Hkv * a.c.Bp + tok;
+    }
+    return p;
+}
+
 template <int DK, bool E4M3>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Args a) {
-    constexpr int LPR = DK / 8;
+    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = kChunk / RPI;      // lanes of a row, rows at a time, times
+    constexpr int U = IT < kUnroll ? IT : kUnroll;
     pdl_wait();
     pdl_trigger();
     const int64_t n = token_count(a);
+    if (n <= 0) return;
     const Side s = a.side[blockIdx.y];
-    if (!s.src || n <= 0) return;
-    const int64_t rows = n * a.c.Hkv;
-    const int lane = threadIdx.x % LPR;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / LPR);
-    // every lane of a warp takes the same number of rounds (the shuffles name all 32)
-    const int64_t first = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    const int64_t rounds = (rows + step * kUnroll - 1) / (step * kUnroll);
-    for (int64_t i = 0; i < rounds; ++i) {
-        uint4 x[kUnroll];
-        int64_t page[kUnroll];
-        int tok[kUnroll], head[kUnroll];
-        bool live[kUnroll];
+    if (!s.src) return;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
+    const int64_t units = (n + kChunk - 1) / kChunk * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
+        const int64_t chunk = unit < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(unit), a.by_heads) : unit / a.c.Hkv;
+        const int head = static_cast<int>(unit - chunk * a.c.Hkv);
+        const int64_t t0 = chunk * kChunk;
+        const Place pl = place_of(a, t0 + lane, n);
+        const uint8_t* src = s.src + t0 * s.stride + (head * DK + sub * 8) * 2;
+        int scale = 0;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t row = first + (i * kUnroll + u) * step;
-            live[u] = row < rows;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (live[u]) {
-                const int64_t t = row < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(row), a.by_heads) : row / a.c.Hkv;
-                head[u] = static_cast<int>(row - t * a.c.Hkv);
-                live[u] = UP_IN(t, a.T, a.status) && place(a, a.slots[t], &page[u], &tok[u]);
-                if (live[u])
-                    x[u] = *reinterpret_cast<const uint4*>(s.src + t * s.stride + (head[u] * DK + lane * 8) * 2);
+        for (int i0 = 0; i0 < IT; i0 += U) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = (i0 + u) * RPI + grp;
+                x[u] = t0 + j < n ? *reinterpret_cast<const uint4*>(src + j * s.stride) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = __shfl_sync(0xffffffffu, pl.row, (i0 + u) * RPI + grp);
+                const int64_t at = row + head * a.c.sh + sub * (E4M3 ? 8 : 16);
+                if constexpr (!E4M3) {
+                    if (row >= 0 && UP_IN(at, a.c.row_limit, a.status)) *reinterpret_cast<uint4*>(s.dst + at) = x[u];
+                } else {
+                    uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                           max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                    m = row_max<LPR>(m);
+                    if (__any_sync(0xffffffffu, m >= 0x7f80u)) {      // a row with infinities or NaN
+                        uint32_t f = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            f = max_u16x2(f, finite_or(w[j], 0) & 0x7fff7fffu);
+                            w[j] = finite_or(w[j], 0x7fff7fffu);
+                        }
+                        m = row_max<LPR>(f);
+                    }
+                    int b = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0);
+                    b = m == 0 ? 127 : max(b, 1);
+                    const float inv = f_of(static_cast<uint32_t>(254 - b) << 23);      // 2^(127 - b)
+                    uint32_t c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[j] = to_e4m3x2(f_of(w[j] << 16) * inv, f_of(w[j] & 0xffff0000u) * inv);
+                    if (row >= 0 && UP_IN(at, a.c.row_limit, a.status))
+                        *reinterpret_cast<uint2*>(s.dst + at) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    // to the lane of the row's token
+                    const int v = __shfl_sync(0xffffffffu, b, (lane % RPI) * LPR);
+                    if (lane / RPI == i0 + u) scale = v;
+                }
             }
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t at = live[u] ? page[u] * a.c.sb + head[u] * a.c.sh + tok[u] * a.c.st : 0;
-            if constexpr (!E4M3) {
-                if (live[u] && UP_IN(at + lane * 16, a.c.row_limit, a.status))
-                    *reinterpret_cast<uint4*>(s.dst + at + lane * 16) = x[u];
-            } else {
-                uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                       max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-                m = row_max<LPR>(m);
-                if (__any_sync(0xffffffffu, m >= 0x7f80u)) {      // a row with infinities or NaN
-                    uint32_t f = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        f = max_u16x2(f, finite_or(w[j], 0) & 0x7fff7fffu);
-                        w[j] = finite_or(w[j], 0x7fff7fffu);
-                    }
-                    m = row_max<LPR>(f);
-                }
-                int b = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0);
-                b = m == 0 ? 127 : max(b, 1);
-                const float inv = f_of(static_cast<uint32_t>(254 - b) << 23);      // 2^(127 - b)
-                uint32_t c[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = to_e4m3x2(f_of(w[j] << 16) * inv, f_of(w[j] & 0xffff0000u) * inv);
-                if (live[u] && UP_IN(at + lane * 8, a.c.row_limit, a.status)) {
-                    *reinterpret_cast<uint2*>(s.dst + at + lane * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-                    const int64_t sc = (page[u] * a.c.Hkv + head[u]) * a.c.Bp + tok[u];
-                    if (lane == 0 && UP_IN(sc, a.c.scale_limit, a.status)) s.scale[sc] = static_cast<uint8_t>(b);
-                }
-            }
+        if constexpr (E4M3) {          // neighbouring tokens of a page: one run of bytes
+            const int64_t at = pl.scale + head * a.c.Bp;
+            if (lane < kChunk && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status)) s.scale[at] = static_cast<uint8_t>(scale);
         }
     }
 }
@@ -172,65 +192,66 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
 
 template <int DK, bool E4M3>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Args a) {
-    constexpr int LPR = DK / 8;
+    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = kChunk / RPI;
+    constexpr int U = IT < kUnroll ? IT : kUnroll;
     pdl_wait();
     pdl_trigger();
     const int64_t n = token_count(a);
+    if (n <= 0) return;
     const Side s = a.side[blockIdx.y];
-    if (!s.dst || n <= 0) return;
-    const int64_t rows = n * a.c.Hkv;
-    const int lane = threadIdx.x % LPR;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / LPR);
-    for (int64_t row0 = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; row0 < rows; row0 += step * kUnroll) {
-        uint4 x[kUnroll];
-        int b[kUnroll];
+    if (!s.dst) return;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
+    const int64_t units = (n + kChunk - 1) / kChunk * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
+    for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
+        const int64_t chunk = unit < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(unit), a.by_heads) : unit / a.c.Hkv;
+        const int head = static_cast<int>(unit - chunk * a.c.Hkv);
+        const int64_t t0 = chunk * kChunk;
+        const Place pl = place_of(a, t0 + lane, n);
+        float factor = 0.f;            // 2^(b - 127) of the lane's token
+        if constexpr (E4M3) {
+            const int64_t at = pl.scale + head * a.c.Bp;
+            if (lane < kChunk && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status))
+                factor = f_of(max(static_cast<uint32_t>(s.scale[at]) << 23, 0x00400000u));
+        }
+        const int64_t dst = (t0 * a.c.Hkv + head) * DK + sub * 8;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t row = row0 + u * step;
-            x[u] = make_uint4(0, 0, 0, 0);
-            b[u] = 127;
-            if (row < rows) {
-                const int64_t t = row < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(row), a.by_heads) : row / a.c.Hkv;
-                const int head = static_cast<int>(row - t * a.c.Hkv);
-                int64_t page = 0;
-                int tok = 0;
-                if (UP_IN(t, a.T, a.status) && place(a, a.slots[t], &page, &tok)) {
-                    const int64_t at = page * a.c.sb + head * a.c.sh + tok * a.c.st + lane * (E4M3 ? 8 : 16);
-                    if (UP_IN(at, a.c.row_limit, a.status)) {
-                        if constexpr (E4M3) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(s.src + at);
-                            x[u].x = v.x;
-                            x[u].y = v.y;
-                            const int64_t sc = (page * a.c.Hkv + head) * a.c.Bp + tok;
-                            b[u] = UP_IN(sc, a.c.scale_limit, a.status) ? s.scale[sc] : 0;
-                        } else {
-                            x[u] = *reinterpret_cast<const uint4*>(s.src + at);
-                        }
+        for (int i0 = 0; i0 < IT; i0 += U) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = __shfl_sync(0xffffffffu, pl.row, (i0 + u) * RPI + grp);
+                const int64_t at = row + head * a.c.sh + sub * (E4M3 ? 8 : 16);
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (row >= 0 && UP_IN(at, a.c.row_limit, a.status)) {
+                    if constexpr (E4M3) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(s.src + at);
+                        x[u].x = v.x;
+                        x[u].y = v.y;
+                    } else {
+                        x[u] = *reinterpret_cast<const uint4*>(s.src + at);
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t row = row0 + u * step;
-            if (row >= rows) break;
-            if constexpr (E4M3) {
-                const float f = b[u] ? f_of(static_cast<uint32_t>(b[u]) << 23) : f_of(0x00400000u);   // 2^(b - 127)
-                const uint2 v = make_uint2(x[u].x, x[u].y);
-                x[u] = make_uint4(scaled_bf16x2(e4m3x2_to_f16x2(v.x), f), scaled_bf16x2(e4m3x2_to_f16x2(v.x >> 16), f),
-                                  scaled_bf16x2(e4m3x2_to_f16x2(v.y), f), scaled_bf16x2(e4m3x2_to_f16x2(v.y >> 16), f));
+            for (int u = 0; u < U; ++u) {
+                const int j = (i0 + u) * RPI + grp;
+                const int64_t at = dst + (int64_t)j * a.c.Hkv * DK;
+                if constexpr (E4M3) {
+                    const float f = __shfl_sync(0xffffffffu, factor, j);
+                    const uint2 v = make_uint2(x[u].x, x[u].y);
+                    x[u] = make_uint4(scaled_bf16x2(e4m3x2_to_f16x2(v.x), f), scaled_bf16x2(e4m3x2_to_f16x2(v.x >> 16), f),
+                                      scaled_bf16x2(e4m3x2_to_f16x2(v.y), f), scaled_bf16x2(e4m3x2_to_f16x2(v.y >> 16), f));
+                }
+                if (t0 + j < n && UP_IN(at, a.T * a.c.Hkv * DK, a.status)) *reinterpret_cast<uint4*>(s.dst + at * 2) = x[u];
             }
-            if (UP_IN(row * DK + lane * 8, a.T * a.c.Hkv * DK, a.status))
-                *reinterpret_cast<uint4*>(s.dst + (row * DK + lane * 8) * 2) = x[u];
         }
     }
 }
 
 template <bool WRITE>
 static up_status launch(const Args& a, int dk, int format, cudaStream_t st) {
-    const int64_t rows = a.T * a.c.Hkv;
-    const int64_t per = kThreads / (dk / 8);
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, per), 4 * num_sms())));
+    const int64_t units = cdiv(a.T, kChunk) * a.c.Hkv;
+    const int grid = static_cast<int>(std::min<int64_t>(cdiv(units, kThreads / 32), kGridPerSm * num_sms()));
     const dim3 g(grid, 2), b(kThreads);
     const bool f8 = format == UP_KV_E4M3;
     cudaError_t e;
