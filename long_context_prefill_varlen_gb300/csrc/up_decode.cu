@@ -47,6 +47,7 @@ constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or va
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // a running maximum moves once a score passes it by this much (log2)
+constexpr float kTop = 256.f;        // 2^kSlack
 
 // How the positions of a request fall into segments (a page, or up to kTile rows of one), tiles of spt
 // segments, and chunks of tiles.
@@ -106,32 +107,39 @@ __device__ __forceinline__ float weight(float x, float m) { return x == -INFINIT
 __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
 
 // ------------------------------------------------------------------------------------------------
-// the walk over a CTA's run of items.  Item order: request, chunk, KV head, head tile.
+// the walk over a CTA's run of items.  Item order: request, unit (KV head, head tile), chunk.
 
 struct Walk {
-    int r, ch, unit;           // unit: KV head * head_tiles + head tile
+    int r, unit, ch;           // unit: KV head * head_tiles + head tile
     Range g;
-    int q, rem;                // tiles of a chunk: q + 1 for the first rem chunks, q after
+    int q, rem;                // tiles = q * splits + rem: chunk ch starts at tile ch q + floor(ch rem / splits)
+    int t0, n;                 // the item's first tile of the request, and its tiles
     int64_t start, end;        // tiles before the item, and where the run ends
     int next_len;
 
     __device__ __forceinline__ int units(const Args& a) const { return a.c.Hkv * a.head_tiles; }
-    __device__ __forceinline__ int tile0() const { return ch * q + min(ch, rem); }
-    __device__ __forceinline__ int tiles() const { return q + (ch < rem ? 1 : 0); }
-    __device__ __forceinline__ bool live(const Args& a) const { return r < a.R && start < end; }
+    __device__ __forceinline__ int tile0(int i) const { return i * q + static_cast<int>(static_cast<unsigned>(i * rem) / static_cast<unsigned>(g.splits)); }
+    // an item belongs to the run that its middle falls into
+    __device__ __forceinline__ bool live(const Args& a) const { return r < a.R && 2 * start + n < 2 * end; }
 
     __device__ __forceinline__ void enter(const Args& a, int len) {
         g = range_of(a.cut, len, (int64_t)a.max_blocks * a.cut.B);
         q = g.splits ? g.tiles / g.splits : 0;
         rem = g.tiles - q * g.splits;
-        ch = unit = 0;
+        unit = ch = t0 = 0;
+        n = g.splits ? tile0(1) : 0;
         next_len = r + 1 < a.R ? length_of(a, r + 1) : 0;
     }
     __device__ __forceinline__ void next(const Args& a) {
-        start += tiles();
+        start += n;
+        if (++ch < g.splits) {
+            t0 += n;
+            n = tile0(ch + 1) - t0;
+            return;
+        }
+        ch = t0 = 0;
+        n = tile0(1);
         if (++unit < units(a)) return;
-        unit = 0;
-        if (++ch < g.splits) return;
         do {
             if (++r >= a.R) return;
             enter(a, next_len);
@@ -139,15 +147,16 @@ struct Walk {
     }
 };
 
-// Every warp finds its CTA's run: first the tiles of all requests, then the first item that starts at or
-// after its share.  Items stay whole, so a run is off by at most one item.
+// Every warp finds its CTA's run: first the tiles of all requests, then the first item whose middle lies in
+// its share.  Items stay whole, so a run is off by at most one item, and equal items as many as CTAs (or a
+// multiple) fall one (or that many) to each.
 __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     const int lane = threadIdx.x & 31;
     const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
     const int units = w.units(a);
     int64_t total = 0;
+    int len[4];                // of requests 32 i + lane of the last 128
     for (int r0 = 0; r0 < a.R; r0 += 128) {
-        int len[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) len[i] = r0 + 32 * i + lane < a.R ? length_of(a, r0 + 32 * i + lane) : 0;
 #pragma unroll
@@ -169,8 +178,13 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     w.r = a.R;
     if (want >= w.end) return;
     int64_t before = 0;        // tiles of the requests before
+    int mine = 0;
     for (int r0 = 0; r0 < a.R; r0 += 32) {
-        const int t = r0 + lane < a.R ? range_of(a.cut, length_of(a, r0 + lane), cap).tiles : 0;
+        if (a.R <= 128)
+            mine = r0 == 0 ? len[0] : r0 == 32 ? len[1] : r0 == 64 ? len[2] : len[3];
+        else
+            mine = r0 + lane < a.R ? length_of(a, r0 + lane) : 0;
+        const int t = range_of(a.cut, mine, cap).tiles;
         int64_t s = (int64_t)t * units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -182,22 +196,20 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
             const int l = __ffs(hit) - 1;
             w.r = r0 + l;
             before += __shfl_sync(0xffffffffu, s - (int64_t)t * units, l);
+            mine = __shfl_sync(0xffffffffu, mine, l);
             break;
         }
         before += __shfl_sync(0xffffffffu, s, 31);
     }
-    w.enter(a, length_of(a, w.r));
+    w.enter(a, mine);
     const int64_t local = want - before;
-    const int u = static_cast<int>(local / units), wide = w.rem * (w.q + 1);
-    w.ch = u < wide ? u / (w.q + 1) : w.rem + (u - wide) / w.q;
-    w.start = before + (int64_t)units * w.tile0();
-    w.unit = static_cast<int>((want - w.start + w.tiles() - 1) / w.tiles());
-    w.start += (int64_t)w.unit * w.tiles();
-    if (w.unit >= units) {     // the last item of the chunk starts before the share: begin with the next chunk
-        w.unit = units - 1;
-        w.start -= w.tiles();
-        w.next(a);
-    }
+    w.unit = static_cast<int>(local / w.g.tiles);
+    const int u = static_cast<int>(local - (int64_t)w.unit * w.g.tiles);
+    w.ch = max(0, static_cast<int>((int64_t)u * w.g.splits / w.g.tiles) - 1);
+    w.t0 = w.tile0(w.ch);
+    w.n = w.tile0(w.ch + 1) - w.t0;
+    w.start = before + (int64_t)w.unit * w.g.tiles + w.t0;
+    while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -210,11 +222,12 @@ struct Shape {
     static constexpr int kPanels = kRowBytes / kPanelBytes;
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
-    // two CTAs on an SM where three stages each fit (228 KB an SM, 1 KB of it per CTA reserved) and the sums
-    // of 16 heads leave registers for it
-    static constexpr int kCtas = 3 * kStage <= 112 * 1024 && !(DK == 256 && HT == 16) ? 2 : 1;
-    static constexpr int kFit = (kCtas == 2 ? 112 * 1024 : 224 * 1024) / kStage;
-    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    // As many CTAs on an SM as leave each a few stages (228 KB of shared memory, 1 KB of it per CTA reserved) and the
+    // registers that its sums need: 15 warps have 128 a thread, 10 have 168, 5 have 255.
+    static constexpr int kControl = 4 * HT * DK + 1024 + 1024;         // queries, barriers and the join's; alignment
+    static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 1024 - kControl) / kStage; }
+    static constexpr int kCtas = DK <= 128 && HT == 8 && fit(3) >= 4 ? 3 : !(DK == 256 && HT == 16) && fit(2) >= 3 ? 2 : 1;
+    static constexpr int kStages = fit(kCtas) < 8 ? fit(kCtas) : 8;
 };
 
 // byte offset of 16-byte column `c` of row `row` in a tile whose base is 1024-byte aligned, as the TMA
@@ -296,6 +309,7 @@ template <int DK, bool E4M3, int HT>
 struct Sizes {
     using S = Shape<DK, E4M3, HT>;
     static constexpr int kSmem = S::kStages * S::kStage + static_cast<int>(sizeof(Control<DK, HT, S::kStages>)) + 1024;
+    static_assert(sizeof(Control<DK, HT, S::kStages>) + 1024 <= S::kControl, "room of the control block");
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -316,7 +330,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     Walk nw = w;
     int ntile = 0;                                                      // next batch: its item and first tile
     auto fetch = [&](const Walk& x, int tile) {
-        const int s = x.g.seg0 + (x.tile0() + tile) * c.spt + lane;
+        const int s = x.g.seg0 + (x.t0 + tile) * c.spt + lane;
         int page = -1;
         if (x.live(a) && lane < per && s <= x.g.seg1) {
             const int64_t e = (int64_t)x.r * a.max_blocks + div_of(s, c.by_spp);
@@ -326,7 +340,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     };
     auto step = [&]() {
         ntile += tiles_per;
-        if (ntile >= nw.tiles()) {
+        if (ntile >= nw.n) {
             nw.next(a);
             ntile = 0;
         }
@@ -342,7 +356,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
             bulk_load(smem_u32(sh.q[qslot]), a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2, heads * DK * 2, bar);
         }
         if (++qslot == 2) qslot = 0, qphase ^= 1;
-        const int n = w.tiles(), t0 = w.tile0();
+        const int n = w.n, t0 = w.t0;
         int pages = -1;
         for (int i = 0, j = tiles_per; i < n; ++i, ++j) {
             if (j == tiles_per) {                                       // a new batch
@@ -475,21 +489,23 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
         float o[NH][KS][4];
-        // running maximum of the scores (of the sums l) and, with scaled values, of score + the value's exponent
-        // (of the sums o): a token may have nearly all the weight and values 2^-100 of another's
-        float ms[NH][2], mt[NH][2], l[NH][2];
+        // References: rs near the running maximum of the scores (of the sums l) and, with scaled values, rt near that of
+        // score + the value's exponent (of the sums o): a token may have nearly all the weight and values 2^-100 of
+        // another's.  -inf before the first score.  rf = 2^(rs - rt).
+        float rs[NH][2], rt[NH][2], rf[NH][2], l[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[h][k][0] = o[h][k][1] = o[h][k][2] = o[h][k][3] = 0.f;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                ms[h][x] = mt[h][x] = -INFINITY;
+                rs[h][x] = rt[h][x] = -INFINITY;
+                rf[h][x] = 1.f;
                 l[h][x] = 0.f;
             }
         }
 
-        const int n = w.tiles(), t0 = w.tile0();
+        const int n = w.n, t0 = w.t0;
         int last_slot = 0;
         for (int i = 0; i < n; ++i) {
             if (!dead && !mbar_wait(smem_u32(&sh.full[slot]), phase, &sh.abort)) dead = true;
@@ -536,84 +552,101 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                         for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
                     }
                 }
-                float kf[2] = {1.f, 1.f}, te[2] = {0.f, 0.f};      // of keys g, g + 8: scale of the keys, exponent of the values
+                float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f};      // scales of the keys' and values' rows g, g + 8
                 if constexpr (E4M3) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         kf[j] = __uint_as_float(max(lds_u8(sb + sc_at[j]) << 23, 0x00400000u));    // 2^(b - 127)
-                        te[j] = __uint_as_float(0x4b000000u | lds_u8(sb + kScaleBytes + sc_at[j])) - 8388608.f - 127.f;
+                        vf[j] = __uint_as_float(max(lds_u8(sb + kScaleBytes + sc_at[j]) << 23, 0x00400000u));
                     }
                 }
                 const bool ok[2] = {((counts >> g) & 1) != 0, ((counts >> (g + 8)) & 1) != 0};
-                // p[h][j][x]: log2-score of key g + 8j and head 2t + x
-                float p[NH][2][2];
-                bool over = false;
+                if (E4M3 && masked) {                  // bytes that nobody wrote may stand for infinity
+                    vf[0] = ok[0] ? vf[0] : 0.f;
+                    vf[1] = ok[1] ? vf[1] : 0.f;
+                }
+                // Of key g + 8j and head 2t + x: y[h][j][x] = 2^(score - rs), and pw the same times the value's scale over
+                // 2^(rt - rs).  The references stay while no weight passes 2^kSlack: a weight that does, or is NaN (also
+                // before the first score), has all the warp's moved.
+                float y[NH][2][2], pw[NH][2][2];
+                auto weigh = [&]() {
+                    bool good = true;
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
+                    for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float y = s[h][0][2 * j + x] + s[h][1][2 * j + x];
-                            p[h][j][x] = ok[j] ? (E4M3 ? y * kf[j] * qf[h][x] : y * qf[h][x]) : -INFINITY;
-                            over |= p[h][j][x] > ms[h][x] + kSlack;
-                            if constexpr (E4M3) over |= p[h][j][x] + te[j] > mt[h][x] + kSlack;
-                        }
-                // move the references if a score passes them (all of the warp at once)
-                if (__any_sync(0xffffffffu, over)) {
+                            for (int x = 0; x < 2; ++x) {
+                                const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
+                                float d = (s[h][0][2 * j + x] + s[h][1][2 * j + x]) * f - rs[h][x];
+                                if (masked && !ok[j]) d = -INFINITY;
+                                good &= d <= kSlack;
+                                y[h][j][x] = ex2(d);
+                                pw[h][j][x] = y[h][j][x];
+                                if constexpr (E4M3) {
+                                    pw[h][j][x] = y[h][j][x] * vf[j] * rf[h][x];
+                                    good &= pw[h][j][x] <= kTop;
+                                }
+                            }
+                    return good;
+                };
+                if (!__all_sync(0xffffffffu, weigh())) {
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            float y = fmaxf(p[h][0][x], p[h][1][x]);
+                            float p[2], top = -INFINITY, topv = -INFINITY;
 #pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                            const float ns = fmaxf(ms[h][x], y);
-                            float f = weight(ms[h][x], ns);
+                            for (int j = 0; j < 2; ++j) {
+                                const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
+                                p[j] = masked && !ok[j] ? -INFINITY : (s[h][0][2 * j + x] + s[h][1][2 * j + x]) * f;
+                                top = fmaxf(top, p[j]);
+                                if constexpr (E4M3) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
+                            }
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            const float ns = fmaxf(rs[h][x], top);
+                            float f = weight(rs[h][x], ns);
                             l[h][x] *= f;
-                            ms[h][x] = ns;
+                            rs[h][x] = ns;
+                            const float us = ns == -INFINITY ? 0.f : ns;       // 0 stands in for a reference of -inf
+                            float ut = 0.f;
                             if constexpr (E4M3) {
-                                y = fmaxf(p[h][0][x] + te[0], p[h][1][x] + te[1]);
 #pragma unroll
-                                for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                                const float nt = fmaxf(mt[h][x], y);
-                                f = weight(mt[h][x], nt);
-                                mt[h][x] = nt;
+                                for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
+                                const float nt = fmaxf(rt[h][x], topv);
+                                f = weight(rt[h][x], nt);
+                                rt[h][x] = nt;
+                                ut = nt == -INFINITY ? 0.f : nt;
+                                rf[h][x] = ex2(fminf(us - ut, 126.f));
                             }
 #pragma unroll
                             for (int k = 0; k < KS; ++k) {
                                 o[h][k][x] *= f;
                                 o[h][k][2 + x] *= f;
                             }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                y[h][j][x] = ex2(p[j] - us);
+                                pw[h][j][x] = E4M3 ? y[h][j][x] * vf[j] * rf[h][x] : y[h][j][x];
+                            }
                         }
                 }
-                // weights, transposed to the second operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of head g); a head without
-                // a score so far has the reference -inf: 0 stands in for it
+                // weights, transposed to the second operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of head g)
                 uint32_t pb[NH][2], lo[NH][2];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    float y[2][2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float rs = ms[h][x] == -INFINITY ? 0.f : ms[h][x];
-                        y[0][x] = ex2(p[h][0][x] - rs);
-                        y[1][x] = ex2(p[h][1][x] - rs);
-                        l[h][x] += y[0][x] + y[1][x];
-                        if constexpr (E4M3) {
-                            const float rt = mt[h][x] == -INFINITY ? 0.f : mt[h][x];
-                            y[0][x] = ex2(p[h][0][x] + te[0] - rt);
-                            y[1][x] = ex2(p[h][1][x] + te[1] - rt);
-                        }
-                    }
+                    for (int x = 0; x < 2; ++x) l[h][x] += y[h][0][x] + y[h][1][x];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         if constexpr (E4M3) {
-                            pb[h][j] = transposed(f16x2(y[j][0], y[j][1]));        // 11 bits: a weight's one rounding
+                            pb[h][j] = transposed(f16x2(pw[h][j][0], pw[h][j][1]));        // 11 bits: a weight's one rounding
                         } else {
                             // bf16 values want bf16 weights: high and low part, 16 bits together
-                            const uint32_t hi = bf16x2(y[j][0], y[j][1]);
+                            const uint32_t hi = bf16x2(pw[h][j][0], pw[h][j][1]);
                             pb[h][j] = transposed(hi);
-                            lo[h][j] = transposed(bf16x2(y[j][0] - low_of(hi), y[j][1] - high_of(hi)));
+                            lo[h][j] = transposed(bf16x2(pw[h][j][0] - low_of(hi), pw[h][j][1] - high_of(hi)));
                         }
                     }
                 }
@@ -676,8 +709,8 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    sh.m[warp][8 * h + 2 * t + x] = ms[h][x];
-                    sh.f[warp][8 * h + 2 * t + x] = E4M3 ? mt[h][x] : ms[h][x];
+                    sh.m[warp][8 * h + 2 * t + x] = rs[h][x];
+                    sh.f[warp][8 * h + 2 * t + x] = E4M3 ? rt[h][x] : rs[h][x];
                     sh.l[warp][8 * h + 2 * t + x] = l[h][x];
                 }
         }
@@ -775,27 +808,79 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------------------------------------
-// one CTA per (query head, request): the chunks of a row, in order
+// one CTA per (query head, request): the chunks of a row, in an order of its own.  Its weights first, a
+// thread a chunk; then a warp (or the half of one, dk = 64) takes every kJoin-th chunk's sums, several in
+// flight, and the warps' sums are added in order.
+
+constexpr int kJoinThreads = 256;
 
 template <int DK>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+    constexpr int LANES = DK / 4 < 32 ? DK / 4 : 32, VEC = DK / LANES / 4, GROUPS = kJoinThreads / LANES, U = 4;
+    __shared__ float wt[kMaxSplits], red[kJoinThreads / 32], sums[GROUPS][DK];
     pdl_wait();
     pdl_trigger();
-    const int hq = blockIdx.x, r = blockIdx.y;
+    const int hq = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)r * a.Hq + hq;
-    const Range g = range_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B);
+    const int n = range_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B).splits;
     if (!UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
     const float* pl = a.part_lse + row * a.cut.max_splits;
     const float* po = a.part_o + row * a.cut.max_splits * DK;
     float m = -INFINITY;
-    for (int i = 0; i < g.splits; ++i) m = fmaxf(m, pl[i]);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+        wt[i] = pl[i];
+        m = fmaxf(m, wt[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[i]);
+    __syncthreads();
     float l = 0.f;
-    for (int i = 0; i < g.splits; ++i) l += weight(pl[i], m);
-    for (int d = threadIdx.x; d < DK; d += 128) {
-        float x = 0.f;
-        for (int i = 0; i < g.splits; ++i) x += weight(pl[i], m) * po[(int64_t)i * DK + d];
-        x = l == 0.f ? 0.f : x / l;
-        a.out[row * DK + d] = static_cast<uint16_t>(bf16x2(x, 0.f) & 0xffffu);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+        wt[i] = weight(wt[i], m);
+        l += wt[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[i];
+    const int grp = threadIdx.x / LANES, at = (threadIdx.x % LANES) * 4;
+    float4 s[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) s[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = grp; i0 < n; i0 += U * GROUPS) {
+        float4 x[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (i0 + u * GROUPS < n)
+                    x[u][v] = *reinterpret_cast<const float4*>(po + (int64_t)(i0 + u * GROUPS) * DK + v * LANES * 4 + at);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * GROUPS >= n) break;
+            const float f = wt[i0 + u * GROUPS];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s[v].x += f * x[u][v].x, s[v].y += f * x[u][v].y, s[v].z += f * x[u][v].z, s[v].w += f * x[u][v].w;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) *reinterpret_cast<float4*>(&sums[grp][v * LANES * 4 + at]) = s[v];
+    __syncthreads();
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (threadIdx.x < DK / 2) {
+        float x = 0.f, y = 0.f;
+        for (int g = 0; g < min(GROUPS, n); ++g) {
+            const float2 z = *reinterpret_cast<const float2*>(&sums[g][2 * threadIdx.x]);
+            x += z.x, y += z.y;
+        }
+        reinterpret_cast<uint32_t*>(a.out)[row * (DK / 2) + threadIdx.x] = bf16x2(x * inv, y * inv);
     }
     if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -871,7 +956,7 @@ static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args
     else
         e = e4m3 ? launch_split<DK, true, 16>(k, v, a, st) : launch_split<DK, false, 16>(k, v, a, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<DK>, dim3(a.Hq, a.R), dim3(128), 0, st, a);
+    return launch_pdl(join_kernel<DK>, dim3(a.Hq, a.R), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace decode
