@@ -514,14 +514,15 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 const uint32_t kb = ring + slot * S::kStage, vb = kb + S::kTileBytes, sb = vb + S::kTileBytes;
                 // bit i: the warp's i-th key counts
                 uint32_t counts = 0xffffu;
-                const bool masked = !whole || t0 + i == 0 || t0 + i == w.g.tiles - 1;
-                if (masked) {
+                if (!whole || t0 + i == 0 || t0 + i == w.g.tiles - 1) {
                     const int s = w.g.seg0 + (t0 + i) * c.spt + my_seg;
                     const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + my_off;
                     const int64_t pos = (int64_t)page * c.B + tok;
                     counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= w.g.lo &&
                                                             pos < w.g.len);
                 }
+                const bool masked = counts != 0xffffu;
+                if (counts != 0) {                     // else nothing for this warp (rows that odd pages leave unused)
                 // scores, keys in the rows: s[h] = (key g: heads 2t, 2t + 1; key g + 8: the same), in two parts so
                 // that a product need not wait for the one before
                 float s[NH][2][4];
@@ -687,6 +688,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                     }
                 };
                 if (masked) values(std::true_type{}); else values(std::false_type{});
+                }
             }
             if (i + 1 < n) {                           // the last stage is kept for the join of the warps
                 __syncwarp();
