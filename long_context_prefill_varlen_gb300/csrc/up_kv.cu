@@ -10,7 +10,7 @@
 // round on both sides and take four bytes instead of one.
 //
 // Both kernels only move bytes (write: 2 dk in, dk + 1 or 2 dk out per row; read: the reverse): HBM-bound.  A
-// warp takes units of kChunk tokens of one head: one coalesced load brings their slots, each lane places one
+// warp takes units of 16 (or 4) tokens of one head: one coalesced load brings their slots, each lane places one
 // token, and the tokens' scale bytes, neighbours in a page, leave (or come) in one access.  A row belongs to
 // dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that its maximum is a few shuffles; the warps of a CTA
 // take the heads of the same tokens, so that they read or write whole tokens of the stream together.
@@ -23,10 +23,15 @@
 namespace up {
 namespace kv {
 
-constexpr int kThreads = 256;
-constexpr int kChunk = 32;           // tokens of a warp's unit
-constexpr int kGridPerSm = 16;      // CTAs of a side
-constexpr int kUnroll = 8;           // rows (or groups of rows) in flight
+// 128 threads, 64 registers: 1,024 threads on an SM with up to eight rows (or groups of rows) of 16 bytes in
+// flight each.  A unit of 16 tokens against 8 and 32: 35 / 38 / 41 us for a write of 32K tokens of 8 heads of 128 in
+// e4m3, 214 / 222 / 218 for a read of 462K of 2 heads of 256.  A call too small to give every SM four warps
+// that way takes units of 4: 2.1 against 3.0 us for 64 tokens.
+constexpr int kThreads = 128, kCtas = 8;
+constexpr int kChunk = 16, kSmallChunk = 4;      // tokens of a warp's unit
+constexpr int kSmallWarps = 4;                   // warps of an SM below which units are small
+constexpr int kGridPerSm = 32;                   // most CTAs of a side
+constexpr int kUnroll = 8;
 
 struct Side {              // keys or values of a call
     const uint8_t* src;    // write: the stream; read: the cache
@@ -113,9 +118,9 @@ __device__ __forceinline__ Place place_of(const Args& a, int64_t t, int64_t n) {
     return p;
 }
 
-template <int DK, bool E4M3>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Args a) {
-    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = kChunk / RPI;      // lanes of a row, rows at a time, times
+template <int DK, bool E4M3, int CHUNK>
+__global__ void __launch_bounds__(kThreads, kCtas) write_kernel(const __grid_constant__ Args a) {
+    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = CHUNK / RPI;      // lanes of a row, rows at a time, times
     constexpr int U = IT < kUnroll ? IT : kUnroll;
     pdl_wait();
     pdl_trigger();
@@ -124,12 +129,12 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
     const Side s = a.side[blockIdx.y];
     if (!s.src) return;
     const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
-    const int64_t units = (n + kChunk - 1) / kChunk * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t units = (n + CHUNK - 1) / CHUNK * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
         const int64_t chunk = unit < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(unit), a.by_heads) : unit / a.c.Hkv;
         const int head = static_cast<int>(unit - chunk * a.c.Hkv);
-        const int64_t t0 = chunk * kChunk;
-        const Place pl = place_of(a, t0 + lane, n);
+        const int64_t t0 = chunk * CHUNK;
+        const Place pl = place_of(a, lane < CHUNK ? t0 + lane : n, n);
         const uint8_t* src = s.src + t0 * s.stride + (head * DK + sub * 8) * 2;
         int scale = 0;
 #pragma unroll
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
         }
         if constexpr (E4M3) {          // neighbouring tokens of a page: one run of bytes
             const int64_t at = pl.scale + head * a.c.Bp;
-            if (lane < kChunk && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status)) s.scale[at] = static_cast<uint8_t>(scale);
+            if (lane < CHUNK && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status)) s.scale[at] = static_cast<uint8_t>(scale);
         }
     }
 }
@@ -190,9 +195,9 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
     return r;
 }
 
-template <int DK, bool E4M3>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Args a) {
-    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = kChunk / RPI;
+template <int DK, bool E4M3, int CHUNK>
+__global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const __grid_constant__ Args a) {
+    constexpr int LPR = DK / 8, RPI = 32 / LPR, IT = CHUNK / RPI;
     constexpr int U = IT < kUnroll ? IT : kUnroll;
     pdl_wait();
     pdl_trigger();
@@ -201,16 +206,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const Side s = a.side[blockIdx.y];
     if (!s.dst) return;
     const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
-    const int64_t units = (n + kChunk - 1) / kChunk * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t units = (n + CHUNK - 1) / CHUNK * a.c.Hkv, step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
         const int64_t chunk = unit < (int64_t{1} << 31) ? div_of(static_cast<uint32_t>(unit), a.by_heads) : unit / a.c.Hkv;
         const int head = static_cast<int>(unit - chunk * a.c.Hkv);
-        const int64_t t0 = chunk * kChunk;
-        const Place pl = place_of(a, t0 + lane, n);
+        const int64_t t0 = chunk * CHUNK;
+        const Place pl = place_of(a, lane < CHUNK ? t0 + lane : n, n);
         float factor = 0.f;            // 2^(b - 127) of the lane's token
         if constexpr (E4M3) {
             const int64_t at = pl.scale + head * a.c.Bp;
-            if (lane < kChunk && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status))
+            if (lane < CHUNK && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status))
                 factor = f_of(max(static_cast<uint32_t>(s.scale[at]) << 23, 0x00400000u));
         }
         const int64_t dst = (t0 * a.c.Hkv + head) * DK + sub * 8;
@@ -248,27 +253,25 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     }
 }
 
-template <bool WRITE>
-static up_status launch(const Args& a, int dk, int format, cudaStream_t st) {
-    const int64_t units = cdiv(a.T, kChunk) * a.c.Hkv;
-    const int grid = static_cast<int>(std::min<int64_t>(cdiv(units, kThreads / 32), kGridPerSm * num_sms()));
-    const dim3 g(grid, 2), b(kThreads);
-    const bool f8 = format == UP_KV_E4M3;
-    cudaError_t e;
-#define UP_KV_CASE(DK)                                                                                      \
-    case DK:                                                                                                \
-        if (WRITE)                                                                                          \
-            e = f8 ? launch_pdl(write_kernel<DK, true>, g, b, 0, st, a) : launch_pdl(write_kernel<DK, false>, g, b, 0, st, a); \
-        else                                                                                                \
-            e = f8 ? launch_pdl(read_kernel<DK, true>, g, b, 0, st, a) : launch_pdl(read_kernel<DK, false>, g, b, 0, st, a);   \
-        break
-    switch (dk) {
-        UP_KV_CASE(64);
-        UP_KV_CASE(128);
-        UP_KV_CASE(256);
-        default: return UP_ERR_SHAPE;
-    }
-#undef UP_KV_CASE
+template <int DK, bool E4M3, int CHUNK>
+static cudaError_t launch_one(const Args& a, bool write, cudaStream_t st) {
+    const int64_t units = cdiv(a.T, CHUNK) * a.c.Hkv;
+    const dim3 g(static_cast<unsigned>(std::min<int64_t>(cdiv(units, kThreads / 32), kGridPerSm * num_sms())), 2);
+    return write ? launch_pdl(write_kernel<DK, E4M3, CHUNK>, g, dim3(kThreads), 0, st, a)
+                 : launch_pdl(read_kernel<DK, E4M3, CHUNK>, g, dim3(kThreads), 0, st, a);
+}
+
+template <int DK>
+static cudaError_t launch_dk(const Args& a, bool write, bool e4m3, cudaStream_t st) {
+    const bool small = 2 * cdiv(a.T, kChunk) * a.c.Hkv < kSmallWarps * num_sms();
+    if (e4m3) return small ? launch_one<DK, true, kSmallChunk>(a, write, st) : launch_one<DK, true, kChunk>(a, write, st);
+    return small ? launch_one<DK, false, kSmallChunk>(a, write, st) : launch_one<DK, false, kChunk>(a, write, st);
+}
+
+static up_status launch(const Args& a, bool write, int dk, int format, cudaStream_t st) {
+    const bool e4m3 = format == UP_KV_E4M3;
+    const cudaError_t e = dk == 64 ? launch_dk<64>(a, write, e4m3, st) : dk == 128 ? launch_dk<128>(a, write, e4m3, st)
+                                                                                    : launch_dk<256>(a, write, e4m3, st);
     if (e != cudaSuccess) return UP_ERR_CUDA;
     count_launch();
     return check_launch();
@@ -301,7 +304,7 @@ extern "C" up_status up_kv_write(const up_kv_cache* cache, const uint16_t* k, in
     a.T = T;
     a.num_tokens = num_tokens;
     a.status = dev_status;
-    return kv::launch<true>(a, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
+    return kv::launch(a, true, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" up_status up_kv_read(const up_kv_cache* cache, const int64_t* slots, int64_t T, const int32_t* num_tokens,
@@ -321,5 +324,5 @@ extern "C" up_status up_kv_read(const up_kv_cache* cache, const int64_t* slots, 
     a.T = T;
     a.num_tokens = num_tokens;
     a.status = dev_status;
-    return kv::launch<false>(a, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
+    return kv::launch(a, false, cache->dk, cache->format, static_cast<cudaStream_t>(stream));
 }
