@@ -147,6 +147,12 @@ struct Walk {
     }
 };
 
+// x / y of numbers that mostly fit 32 bits (a 64-bit division takes a third of a microsecond, here in the way of
+// the first copy)
+__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
+    return x >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+
 // Every warp finds its CTA's run: first the tiles of all requests, then the first item whose middle lies in
 // its share.  Items stay whole, so a run is off by at most one item, and equal items as many as CTAs (or a
 // multiple) fall one (or that many) to each.
@@ -172,8 +178,8 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     // before every SM has one
     const int n = gridDim.x, half = (n + 1) / 2, b = blockIdx.x;
     const int64_t at = b < half ? 2 * b : 2 * (b - half) + 1;
-    w.end = total * (at + 1) / n;
-    const int64_t want = total * at / n;
+    w.end = quotient(total * (at + 1), n);
+    const int64_t want = quotient(total * at, n);
     w.start = 0;
     w.r = a.R;
     if (want >= w.end) return;
@@ -203,9 +209,9 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     }
     w.enter(a, mine);
     const int64_t local = want - before;
-    w.unit = static_cast<int>(local / w.g.tiles);
+    w.unit = static_cast<int>(quotient(local, w.g.tiles));
     const int u = static_cast<int>(local - (int64_t)w.unit * w.g.tiles);
-    w.ch = max(0, static_cast<int>((int64_t)u * w.g.splits / w.g.tiles) - 1);
+    w.ch = max(0, static_cast<int>(quotient((int64_t)u * w.g.splits, w.g.tiles)) - 1);
     w.t0 = w.tile0(w.ch);
     w.n = w.tile0(w.ch + 1) - w.t0;
     w.start = before + (int64_t)w.unit * w.g.tiles + w.t0;
@@ -346,24 +352,27 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
         }
     };
     int pages_next = fetch(nw, 0);
+    int q_r = -1, q_unit = -1;                                          // whose queries were sent last
     for (; w.live(a) && !dead; w.next(a)) {
         const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
-        const int heads = min(HT, a.group - h0);
-        if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
-        if (lane == 0) {
-            const uint32_t bar = smem_u32(&sh.qfull[qslot]);
-            mbar_arrive_expect_tx(bar, heads * DK * 2);
-            bulk_load(smem_u32(sh.q[qslot]), a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2, heads * DK * 2, bar);
+        if (w.r != q_r || w.unit != q_unit) {
+            q_r = w.r, q_unit = w.unit;
+            const int bytes = min(HT, a.group - h0) * DK * 2;
+            if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&sh.qfull[qslot]);
+                mbar_arrive_expect_tx(bar, bytes);
+                bulk_load(smem_u32(sh.q[qslot]), a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2, bytes, bar);
+            }
+            if (++qslot == 2) qslot = 0, qphase ^= 1;
         }
-        if (++qslot == 2) qslot = 0, qphase ^= 1;
         const int n = w.n, t0 = w.t0;
         int pages = -1;
         for (int i = 0, j = tiles_per; i < n; ++i, ++j) {
-            if (j == tiles_per) {                                       // a new batch
+            const bool fresh = j == tiles_per;                          // a new batch
+            if (fresh) {
                 j = 0;
                 pages = pages_next;
-                step();
-                pages_next = fetch(nw, ntile);
             }
             if (!mbar_wait(smem_u32(&sh.empty[slot]), phase ^ 1, &sh.abort)) {
                 dead = true;
@@ -406,6 +415,10 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
             }
             ++issued;
             if (++slot == S::kStages) slot = 0, phase ^= 1;
+            if (fresh) {
+                step();
+                pages_next = fetch(nw, ntile);
+            }
         }
     }
     if (dead || sh.abort) {
@@ -443,13 +456,11 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         sc_at[j] = min(s * scs + row - s * c.segp, kScaleBytes - 1);
     }
 
-    for (; w.live(a); w.next(a)) {
-        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
-        const int heads = min(HT, a.group - h0);
-        // queries to registers, as the products' second operand: head g (of each tile of 8), columns
-        // 16k + {2t, 2t+1, 2t+8, 2t+9}; for e4m3 16k + 4t .. 4t+3, the order that the key bytes come in
-        uint32_t qb[NH][KS][2];
-        float qf[NH][2];                               // factors of the scores of heads 2t, 2t + 1
+    uint32_t qb[NH][KS][2];
+    float qf[NH][2];                                   // factors of the scores of heads 2t, 2t + 1
+    // queries to registers, as the products' second operand: head g (of each tile of 8), columns
+    // 16k + {2t, 2t+1, 2t+8, 2t+9}; for e4m3 16k + 4t .. 4t+3, the order that the key bytes come in
+    auto load_queries = [&]() {
         if (!dead && !mbar_wait(smem_u32(&sh.qfull[qslot]), qphase, &sh.abort)) dead = true;
         const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
 #pragma unroll
@@ -485,7 +496,16 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.qempty[qslot]));
         if (++qslot == 2) qslot = 0, qphase ^= 1;
+    };
 
+    int q_r = -1, q_unit = -1;                         // whose queries the registers hold
+    for (; w.live(a); w.next(a)) {
+        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
+        const int heads = min(HT, a.group - h0);
+        if (w.r != q_r || w.unit != q_unit) {
+            q_r = w.r, q_unit = w.unit;
+            load_queries();
+        }
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
         float o[NH][KS][4];
@@ -538,8 +558,9 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                         ldsm4(b, kb + swizzled<PB>(arow, k + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t a0 = kv::e4m3x2_to_f16x2(b[2 * x]), a2 = kv::e4m3x2_to_f16x2(b[2 * x] >> 16);
-                            const uint32_t a1 = kv::e4m3x2_to_f16x2(b[2 * x + 1]), a3 = kv::e4m3x2_to_f16x2(b[2 * x + 1] >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            kv::e4m3x4_to_f16x4(b[2 * x], a0, a2);
+                            kv::e4m3x4_to_f16x4(b[2 * x + 1], a1, a3);
 #pragma unroll
                             for (int h = 0; h < NH; ++h) mma<true>(s[h][x], a0, a1, a2, a3, qb[h][k + x][0], qb[h][k + x][1]);
                         }
@@ -666,8 +687,9 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                             for (int x = 0; x < 2; ++x) {
                                 // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
                                 const uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
-                                uint32_t e0 = kv::e4m3x2_to_f16x2(b0), e1 = kv::e4m3x2_to_f16x2(b1);
-                                uint32_t d0 = kv::e4m3x2_to_f16x2(b0 >> 16), d1 = kv::e4m3x2_to_f16x2(b1 >> 16);
+                                uint32_t e0, e1, d0, d1;
+                                kv::e4m3x4_to_f16x4(b0, e0, d0);
+                                kv::e4m3x4_to_f16x4(b1, e1, d1);
                                 if constexpr (M) e0 &= z0, d0 &= z0, e1 &= z1, d1 &= z1;
 #pragma unroll
                                 for (int h = 0; h < NH; ++h) mma<true>(o[h][k + x], e0, d0, e1, d1, pb[h][0], pb[h][1]);
@@ -810,16 +832,19 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------------------------------------
-// one CTA per (query head, request): the chunks of a row, in an order of its own.  Its weights first, a
-// thread a chunk; then a warp (or the half of one, dk = 64) takes every kJoin-th chunk's sums, several in
-// flight, and the warps' sums are added in order.
+// One CTA per (query head, request).  Every warp finds the row's largest lse2 and the sum of its chunks'
+// weights; then the chunks i = g mod 16 are group g's, whose sums are added in the order of g.  A CTA has 16
+// warps with a group each, eight chunks in flight, where rows are few (4 requests of 128K: 152 chunks a row), and
+// 4 warps with four groups each where they are many: the order of the additions is the same.
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = 16;
 
-template <int DK>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
-    constexpr int LANES = DK / 4 < 32 ? DK / 4 : 32, VEC = DK / LANES / 4, GROUPS = kJoinThreads / LANES, U = 4;
-    __shared__ float wt[kMaxSplits], red[kJoinThreads / 32], sums[GROUPS][DK];
+template <int DK, int W>
+__global__ void __launch_bounds__(32 * W) join_kernel(const __grid_constant__ Args a) {
+    constexpr int GPW = kJoinGroups / W, E = DK / 32, U = (W == 16 ? 8 : 2) / (E == 8 ? 2 : 1);
+    constexpr int VE = E < 4 ? E : 4, V = E / VE;      // a lane's columns: V vectors of VE floats
+    using Vec = typename std::conditional<VE == 2, float2, float4>::type;
+    __shared__ alignas(16) float sums[kJoinGroups][DK];
     pdl_wait();
     pdl_trigger();
     const int hq = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -827,58 +852,60 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int n = range_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B).splits;
     if (!UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
     const float* pl = a.part_lse + row * a.cut.max_splits;
-    const float* po = a.part_o + row * a.cut.max_splits * DK;
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-        wt[i] = pl[i];
-        m = fmaxf(m, wt[i]);
-    }
+    const float* po = a.part_o + row * a.cut.max_splits * DK + lane * VE;
+    float s[GPW][E], l = 0.f, m = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
+    for (int i = 0; i < GPW; ++i)
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[i]);
-    __syncthreads();
-    float l = 0.f;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-        wt[i] = weight(wt[i], m);
-        l += wt[i];
-    }
+        for (int e = 0; e < E; ++e) s[i][e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += kJoinGroups * U) {
+        float x[GPW][U][E], f[GPW][U];                 // on their way while the weights are found
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) red[warp] = l;
-    __syncthreads();
-    l = 0.f;
+        for (int i = 0; i < GPW; ++i)
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[i];
-    const int grp = threadIdx.x / LANES, at = (threadIdx.x % LANES) * 4;
-    float4 s[VEC];
+            for (int u = 0; u < U; ++u) {
+                const int at = i0 + u * kJoinGroups + warp + i * W;
+                f[i][u] = at < n ? pl[at] : -INFINITY;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) s[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = grp; i0 < n; i0 += U * GROUPS) {
-        float4 x[U][VEC];
+                for (int v = 0; v < V; ++v)
+                    if (at < n) {
+                        const Vec y = *reinterpret_cast<const Vec*>(po + (int64_t)at * DK + v * 32 * VE);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+                        for (int e = 0; e < VE; ++e) x[i][u][v * VE + e] = reinterpret_cast<const float*>(&y)[e];
+                    }
+            }
+        if (i0 == 0) {
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, pl[i]);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (i0 + u * GROUPS < n)
-                    x[u][v] = *reinterpret_cast<const float4*>(po + (int64_t)(i0 + u * GROUPS) * DK + v * LANES * 4 + at);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = lane; i < n; i += 32) l += weight(pl[i], m);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * GROUPS >= n) break;
-            const float f = wt[i0 + u * GROUPS];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v].x += f * x[u][v].x, s[v].y += f * x[u][v].y, s[v].z += f * x[u][v].z, s[v].w += f * x[u][v].w;
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         }
+#pragma unroll
+        for (int i = 0; i < GPW; ++i)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * kJoinGroups + warp + i * W < n) {
+                    const float w = weight(f[i][u], m);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) s[i][e] += w * x[i][u][e];
+                }
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) *reinterpret_cast<float4*>(&sums[grp][v * LANES * 4 + at]) = s[v];
+    for (int i = 0; i < GPW; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Vec y;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) reinterpret_cast<float*>(&y)[e] = s[i][v * VE + e];
+            *reinterpret_cast<Vec*>(&sums[warp + i * W][v * 32 * VE + lane * VE]) = y;
+        }
     __syncthreads();
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / l;        // l = 0: no score above -inf.  NaN goes through.
     if (threadIdx.x < DK / 2) {
         float x = 0.f, y = 0.f;
-        for (int g = 0; g < min(GROUPS, n); ++g) {
+        for (int g = 0; g < min(kJoinGroups, n); ++g) {
             const float2 z = *reinterpret_cast<const float2*>(&sums[g][2 * threadIdx.x]);
             x += z.x, y += z.y;
         }
@@ -958,7 +985,9 @@ static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args
     else
         e = e4m3 ? launch_split<DK, true, 16>(k, v, a, st) : launch_split<DK, false, 16>(k, v, a, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<DK>, dim3(a.Hq, a.R), dim3(kJoinThreads), 0, st, a);
+    const bool few = (int64_t)a.Hq * a.R <= 4 * num_sms();
+    return few ? launch_pdl(join_kernel<DK, 16>, dim3(a.Hq, a.R), dim3(512), 0, st, a)
+               : launch_pdl(join_kernel<DK, 4>, dim3(a.Hq, a.R), dim3(128), 0, st, a);
 }
 
 }  // namespace decode
