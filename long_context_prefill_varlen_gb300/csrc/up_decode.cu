@@ -14,7 +14,7 @@
 //  * persistent CTAs take runs of (request, chunk, head) items of equal length in tiles; every CTA finds its
 //    run from seqused itself, so no launch plans and the host never waits for a length;
 //  * a producer warp walks the run and fills a ring of stages (the K and V tile of one head) by TMA, one
-//    box per page and 128 bytes of dk, swizzled so that ldmatrix reads it without bank conflicts; the ring
+//    box per page, swizzled so that ldmatrix reads it without bank conflicts; the ring
 //    runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
 //    running maximum and sums, joined through the last stage when the item ends.
@@ -54,9 +54,10 @@ constexpr float kTop = 256.f;        // 2^kSlack
 struct Cut {
     int B, seg, segp, spp, spt;      // page; rows of a segment, and of its place in a tile; segments of a
                                      // page, of a tile
-    int window, s0;                  // s0: chunks that spread one request's heads evenly over the grid
+    int window, s0, most;            // s0: chunks that spread one request's heads evenly over the grid; at most
+                                     // `most` times as many
     int max_splits;
-    FastDiv by_b, by_spt, by_spp, by_segp;
+    FastDiv by_b, by_spt, by_spp, by_segp, by_wave;    // by_wave: s0 * kMaxTiles
 };
 
 struct Range {
@@ -64,11 +65,20 @@ struct Range {
     int seg0, seg1, tiles, splits;   // first and last segment; tiles from the first; chunks
 };
 
-__host__ __device__ inline int splits_of(int tiles, int s0) {
+// floor(x / f.d) on either side
+__host__ __device__ __forceinline__ int divided(int x, const FastDiv& f) {
+#ifdef __CUDA_ARCH__
+    return static_cast<int>(div_of(static_cast<uint32_t>(x), f));
+#else
+    return x / static_cast<int>(f.d);
+#endif
+}
+
+__host__ __device__ __forceinline__ int splits_of(int tiles, const Cut& c) {
     const int fine = (tiles + kMinTiles - 1) / kMinTiles;
-    if (fine <= s0) return fine;
-    const int waves = (tiles + s0 * kMaxTiles - 1) / (s0 * kMaxTiles), most = kMaxSplits / s0;
-    return s0 * (waves < most ? waves : most);
+    if (fine <= c.s0) return fine;
+    const int waves = divided(tiles + c.s0 * kMaxTiles - 1, c.by_wave);
+    return c.s0 * (waves < c.most ? waves : c.most);
 }
 
 __device__ __forceinline__ Range range_of(const Cut& c, int len, int64_t cap) {
@@ -76,13 +86,18 @@ __device__ __forceinline__ Range range_of(const Cut& c, int len, int64_t cap) {
     r.len = len < 0 || len > cap ? 0 : len;
     r.lo = c.window > 0 && r.len > c.window ? r.len - c.window : 0;
     const int last = r.len > 0 ? r.len - 1 : 0;
-    const int p0 = div_of(r.lo, c.by_b), p1 = div_of(last, c.by_b);
+    const int p0 = r.lo ? divided(r.lo, c.by_b) : 0, p1 = divided(last, c.by_b);
     r.seg0 = p0 * c.spp + (r.lo - p0 * c.B) / kTile;
     r.seg1 = p1 * c.spp + (last - p1 * c.B) / kTile;
-    r.tiles = r.len > 0 ? div_of(r.seg1 - r.seg0, c.by_spt) + 1 : 0;
-    r.splits = splits_of(r.tiles, c.s0);
+    r.tiles = r.len > 0 ? divided(r.seg1 - r.seg0, c.by_spt) + 1 : 0;
+    r.splits = 0;
     return r;
 }
+
+__device__ __forceinline__ int splits_of(const Cut& c, int len, int64_t cap) { return splits_of(range_of(c, len, cap).tiles, c); }
+
+// 2^(x - m), and 0 for x = -inf whatever m is (m is the largest of a set that x belongs to; NaN stays)
+__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : ex2(x - m); }
 
 struct Args {
     const uint8_t* q;
@@ -101,9 +116,6 @@ struct Args {
     int32_t* status;
 };
 
-// 2^(x - m), and 0 for x = -inf whatever m is (m is the largest of a set that x belongs to; NaN stays)
-__device__ __forceinline__ float weight(float x, float m) { return x == -INFINITY ? 0.f : ex2(x - m); }
-
 __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
 
 // ------------------------------------------------------------------------------------------------
@@ -112,33 +124,42 @@ __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r,
 struct Walk {
     int r, unit, ch;           // unit: KV head * head_tiles + head tile
     Range g;
-    int q, rem;                // tiles = q * splits + rem: chunk ch starts at tile ch q + floor(ch rem / splits)
+    int q, rem, err;           // tiles = q * splits + rem: chunk ch starts at tile ch q + floor(ch rem / splits);
+                               // err = ch rem mod splits
     int t0, n;                 // the item's first tile of the request, and its tiles
     int64_t start, end;        // tiles before the item, and where the run ends
     int next_len;
 
     __device__ __forceinline__ int units(const Args& a) const { return a.c.Hkv * a.head_tiles; }
-    __device__ __forceinline__ int tile0(int i) const { return i * q + static_cast<int>(static_cast<unsigned>(i * rem) / static_cast<unsigned>(g.splits)); }
     // an item belongs to the run that its middle falls into
     __device__ __forceinline__ bool live(const Args& a) const { return r < a.R && 2 * start + n < 2 * end; }
 
+    // chunk i, its rem i / splits and remainder given
+    __device__ __forceinline__ void chunk(int i, int whole, int left) {
+        ch = i;
+        t0 = i * q + whole;
+        err = left;
+        n = q + (err + rem >= g.splits ? 1 : 0);
+    }
     __device__ __forceinline__ void enter(const Args& a, int len) {
         g = range_of(a.cut, len, (int64_t)a.max_blocks * a.cut.B);
-        q = g.splits ? g.tiles / g.splits : 0;
+        g.splits = splits_of(g.tiles, a.cut);
+        q = g.splits ? static_cast<int>(static_cast<unsigned>(g.tiles) / static_cast<unsigned>(g.splits)) : 0;
         rem = g.tiles - q * g.splits;
-        unit = ch = t0 = 0;
-        n = g.splits ? tile0(1) : 0;
+        unit = 0;
+        chunk(0, 0, 0);
         next_len = r + 1 < a.R ? length_of(a, r + 1) : 0;
     }
     __device__ __forceinline__ void next(const Args& a) {
         start += n;
         if (++ch < g.splits) {
             t0 += n;
-            n = tile0(ch + 1) - t0;
+            err += rem;
+            if (err >= g.splits) err -= g.splits;
+            n = q + (err + rem >= g.splits ? 1 : 0);
             return;
         }
-        ch = t0 = 0;
-        n = tile0(1);
+        chunk(0, 0, 0);
         if (++unit < units(a)) return;
         do {
             if (++r >= a.R) return;
@@ -153,26 +174,30 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int y) {
     return x >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
 
-// Every warp finds its CTA's run: first the tiles of all requests, then the first item whose middle lies in
-// its share.  Items stay whole, so a run is off by at most one item, and equal items as many as CTAs (or a
+// Every warp finds its CTA's run: the tiles of all requests, then the first item whose middle lies in its
+// share.  Items stay whole, so a run is off by at most one item, and equal items as many as CTAs (or a
 // multiple) fall one (or that many) to each.
 __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     const int lane = threadIdx.x & 31;
     const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
     const int units = w.units(a);
-    int64_t total = 0;
-    int len[4];                // of requests 32 i + lane of the last 128
-    for (int r0 = 0; r0 < a.R; r0 += 128) {
+    // 32 requests at a time: a lane's length, its tiles and the tiles up to it.  Up to 32 requests are read once.
+    int len = 0, mine = 0, upto = 0;
+    auto scan = [&](int r0) {
+        len = r0 + lane < a.R ? length_of(a, r0 + lane) : 0;
+        upto = mine = range_of(a.cut, len, cap).tiles;         // at most 2^25 a request
 #pragma unroll
-        for (int i = 0; i < 4; ++i) len[i] = r0 + 32 * i + lane < a.R ? length_of(a, r0 + 32 * i + lane) : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            total += range_of(a.cut, len[i], cap).tiles;
-            if ((len[i] < 0 || len[i] > cap) && blockIdx.x == 0 && threadIdx.x < 32) set_status(a.status, UP_DEV_BAD_LENGTH);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
+    };
+    int64_t total = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
+        scan(r0);
+        total += __shfl_sync(0xffffffffu, upto, 31);
+        if ((len < 0 || len > cap) && blockIdx.x == 0 && threadIdx.x < 32) set_status(a.status, UP_DEV_BAD_LENGTH);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= units;
     // neighbours in the order of runs are half a grid apart: a short list of items leaves no SM with two
     // before every SM has one
@@ -184,36 +209,26 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     w.r = a.R;
     if (want >= w.end) return;
     int64_t before = 0;        // tiles of the requests before
-    int mine = 0;
+    int found = 0;
     for (int r0 = 0; r0 < a.R; r0 += 32) {
-        if (a.R <= 128)
-            mine = r0 == 0 ? len[0] : r0 == 32 ? len[1] : r0 == 64 ? len[2] : len[3];
-        else
-            mine = r0 + lane < a.R ? length_of(a, r0 + lane) : 0;
-        const int t = range_of(a.cut, mine, cap).tiles;
-        int64_t s = (int64_t)t * units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, before + s > want);
+        if (a.R > 32) scan(r0);
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + (int64_t)upto * units > want);
         if (hit) {
             const int l = __ffs(hit) - 1;
             w.r = r0 + l;
-            before += __shfl_sync(0xffffffffu, s - (int64_t)t * units, l);
-            mine = __shfl_sync(0xffffffffu, mine, l);
+            before += (int64_t)__shfl_sync(0xffffffffu, upto - mine, l) * units;
+            found = __shfl_sync(0xffffffffu, len, l);
             break;
         }
-        before += __shfl_sync(0xffffffffu, s, 31);
+        before += (int64_t)__shfl_sync(0xffffffffu, upto, 31) * units;
     }
-    w.enter(a, mine);
+    w.enter(a, found);
     const int64_t local = want - before;
     w.unit = static_cast<int>(quotient(local, w.g.tiles));
     const int u = static_cast<int>(local - (int64_t)w.unit * w.g.tiles);
-    w.ch = max(0, static_cast<int>(quotient((int64_t)u * w.g.splits, w.g.tiles)) - 1);
-    w.t0 = w.tile0(w.ch);
-    w.n = w.tile0(w.ch + 1) - w.t0;
+    const int i = max(0, static_cast<int>(quotient((int64_t)u * w.g.splits, w.g.tiles)) - 1);
+    const int whole = static_cast<int>(static_cast<unsigned>(i * w.rem) / static_cast<unsigned>(w.g.splits));
+    w.chunk(i, whole, i * w.rem - whole * w.g.splits);
     w.start = before + (int64_t)w.unit * w.g.tiles + w.t0;
     while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
 }
@@ -224,7 +239,7 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
 template <int DK, bool E4M3, int HT>
 struct Shape {
     static constexpr int kRowBytes = DK * (E4M3 ? 1 : 2);
-    static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;      // a tile is panels of rows
+    static constexpr int kPanelBytes = kRowBytes < 128 ? kRowBytes : 128;      // a segment is panels of rows
     static constexpr int kPanels = kRowBytes / kPanelBytes;
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
@@ -236,14 +251,14 @@ struct Shape {
     static constexpr int kStages = fit(kCtas) < 8 ? fit(kCtas) : 8;
 };
 
-// byte offset of 16-byte column `c` of row `row` in a tile whose base is 1024-byte aligned, as the TMA
-// swizzle of kPanelBytes-wide rows lays it out
+// Byte offset of 16-byte column c of a panel's row that starts at byte `row` of a tile (the tile 1024-byte aligned):
+// the TMA swizzle takes the address bits above the row into the column.
 template <int PANEL>
-__device__ __forceinline__ uint32_t swizzled(int row, int c) {
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, int c) {
     if constexpr (PANEL == 128)
-        return (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        return row + (((c & 7) ^ ((row >> 7) & 7)) << 4);
     else
-        return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+        return row + ((c ^ ((row >> 7) & 3)) << 4);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -285,6 +300,13 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float low_of(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
 __device__ __forceinline__ float high_of(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
+// 16 bytes to shared memory, and one arrival of this thread at `bar` once its copies so far have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -331,7 +353,8 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     int64_t issued = 0;
     bool dead = false;
     const int per = (32 / c.spt) * c.spt, tiles_per = 32 / c.spt;      // table entries and tiles of a batch
-    const int scs = (c.seg + 15) & ~15;
+    // the 16 scale bytes that this lane copies: of which segment of the tile, and from which byte of its part of a page
+    const int per_seg = (c.seg + 15) / 16, sc_seg = lane / per_seg, sc_part = (lane - sc_seg * per_seg) * 16;
     // the table entries of the run's segments, 32 (or the most that make whole tiles) at a time, one batch ahead
     Walk nw = w;
     int ntile = 0;                                                      // next batch: its item and first tile
@@ -378,40 +401,45 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                 dead = true;
                 break;
             }
-            const int page = __shfl_sync(0xffffffffu, pages, (j * c.spt + lane) & 31);
-            const int s = w.g.seg0 + (t0 + i) * c.spt + lane;
-            const bool mine = lane < c.spt && s <= w.g.seg1;
-            const bool good = mine && page >= 0 && page < a.c.num_blocks;
-            const int part = s - div_of(s, c.by_spp) * c.spp;           // which segment of its page
+            // segments s0 .. s0 + ns - 1 of the request (in a page of several segments one: part of its page)
+            const int s0 = w.g.seg0 + (t0 + i) * c.spt, ns = min(c.spt, w.g.seg1 - s0 + 1);
+            const int part = c.spp == 1 ? 0 : s0 - div_of(s0, c.by_spp) * c.spp;
             const uint32_t stage = ring + slot * S::kStage, bar = smem_u32(&sh.full[slot]);
-            const uint32_t sc = stage + 2 * S::kTileBytes + lane * scs;
-            const int scale_bytes = E4M3 ? min(scs, a.c.Bp - part * kTile) : 0;
-            if (mine && !good) {
-                set_status(a.status, UP_DEV_BAD_PAGE);
-                if constexpr (E4M3)                                     // codes of zero (out of the map's bounds), scale 1
-                    for (int b = 0; b < scs; b += 4) {
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + b), "r"(0x7f7f7f7fu) : "memory");
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + kScaleBytes + b), "r"(0x7f7f7f7fu) : "memory");
-                    }
+            const uint32_t sc = stage + 2 * S::kTileBytes + 16 * lane;
+            int sc_page = -1;
+            bool sc_mine = false;
+            if constexpr (E4M3) {
+                sc_page = __shfl_sync(0xffffffffu, pages, (j * c.spt + sc_seg) & 31);
+                sc_mine = sc_seg < ns && part * kTile + sc_part < a.c.Bp;
+                if (sc_mine && (sc_page < 0 || sc_page >= a.c.num_blocks)) {       // codes of zero, scale 1
+                    const uint32_t one = 0x7f7f7f7fu;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sc), "r"(one) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sc + kScaleBytes), "r"(one) : "memory");
+                    sc_mine = false;
+                }
+                __syncwarp();
             }
-            const uint32_t bytes = __reduce_add_sync(0xffffffffu, (mine ? 2 * c.seg * S::kRowBytes : 0) + (good ? 2 * scale_bytes : 0));
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * ns * c.seg * S::kRowBytes);
             __syncwarp();
-            if (mine) {
-                const int at = good ? page : static_cast<int>(a.c.num_blocks);
-                const uint32_t dst = stage + lane * c.segp * S::kPanelBytes;
-#pragma unroll
-                for (int p = 0; p < S::kPanels; ++p) {
-                    tma_load_4d(dst + p * kTile * 128, kmap, bar, p * (E4M3 ? 128 : 64), part * kTile, head, at);
-                    tma_load_4d(dst + S::kTileBytes + p * kTile * 128, vmap, bar, p * (E4M3 ? 128 : 64), part * kTile, head, at);
+            // a lane a segment: side by side they issue in 85 cycles each, one after another from one lane in 120
+            int at = __shfl_sync(0xffffffffu, pages, (j * c.spt + lane) & 31);
+            if (lane < ns) {
+                if (at < 0 || at >= a.c.num_blocks) {
+                    set_status(a.status, UP_DEV_BAD_PAGE);
+                    at = static_cast<int>(a.c.num_blocks);              // out of the map's bounds: zeros
                 }
-                if constexpr (E4M3) {
-                    const int64_t src = ((int64_t)page * a.c.Hkv + head) * a.c.Bp + part * kTile;
-                    if (good && UP_IN(src, a.c.scale_limit - scale_bytes + 1, a.status)) {
-                        bulk_load(sc, a.c.ks + src, scale_bytes, bar);
-                        bulk_load(sc + kScaleBytes, a.c.vs + src, scale_bytes, bar);
-                    }
+                const uint32_t dst = stage + lane * c.segp * S::kRowBytes;
+                tma_load_5d(dst, kmap, bar, 0, part * kTile, 0, head, at);
+                tma_load_5d(dst + S::kTileBytes, vmap, bar, 0, part * kTile, 0, head, at);
+            }
+            __syncwarp();
+            if constexpr (E4M3) {
+                const int64_t src = ((int64_t)sc_page * a.c.Hkv + head) * a.c.Bp + part * kTile + sc_part;
+                if (sc_mine && UP_IN(src, a.c.scale_limit - 15, a.status)) {
+                    copy16(sc, a.c.ks + src);
+                    copy16(sc + kScaleBytes, a.c.vs + src);
                 }
+                arrive_after_copies(bar);
             }
             ++issued;
             if (++slot == S::kStages) slot = 0, phase ^= 1;
@@ -446,6 +474,13 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     // tile row 16 warp + (lane & 15): its segment of the tile and its token there
     const int my_row = 16 * warp + (lane & 15);
     const int my_seg = div_of(my_row, c.by_segp), my_off = my_row - my_seg * c.segp;
+    // where the rows that this lane addresses for ldmatrix start: a segment is all panels of its rows, one after another
+    auto row_at = [&](int row) {
+        const int j = div_of(row, c.by_segp);
+        return static_cast<uint32_t>((j * c.segp * S::kPanels + row - j * c.segp) * PB);
+    };
+    const uint32_t krow = row_at(my_row), vrow = E4M3 ? krow : row_at(16 * warp + (lane & 7) + ((lane >> 4) << 3));
+    const uint32_t panel = c.seg * PB;
     const bool whole = c.spt * c.segp == kTile && c.segp == c.seg && (c.spp == 1 || c.B % kTile == 0);
     const int scs = (c.seg + 15) & ~15;
     // scale bytes of the keys g and g + 8 of the warp
@@ -550,12 +585,11 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) s[h][0][x] = s[h][1][x] = 0.f;
-                const int arow = 16 * warp + (lane & 15);
                 if constexpr (E4M3) {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
                         uint32_t b[4];                 // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                        ldsm4(b, kb + swizzled<PB>(arow, k + (lane >> 4)));
+                        ldsm4(b, kb + swizzled<PB>(krow + (k >> 3) * panel, k + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint32_t a0, a1, a2, a3;
@@ -569,7 +603,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         uint32_t b[4];                 // (keys 0-7, 8-15) of 8 columns, then of the next 8
-                        ldsm4(b, kb + swizzled<PB>(arow, 2 * k + (lane >> 4)));
+                        ldsm4(b, kb + swizzled<PB>(krow + (k >> 2) * panel, 2 * k + (lane >> 4)));
 #pragma unroll
                         for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
                     }
@@ -682,7 +716,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                         for (int k = 0; k < KS; k += 2) {
                             uint32_t b[4];             // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                            ldsm4t(b, vb + swizzled<PB>(16 * warp + (lane & 15), k + (lane >> 4)));
+                            ldsm4t(b, vb + swizzled<PB>(vrow + (k >> 3) * panel, k + (lane >> 4)));
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
@@ -699,7 +733,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             uint32_t b[4];             // keys 0-7 of 8 columns and the next 8, then keys 8-15
-                            ldsm4t(b, vb + swizzled<PB>(16 * warp + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                            ldsm4t(b, vb + swizzled<PB>(vrow + (k >> 2) * panel, 2 * k + ((lane >> 3) & 1)));
                             if constexpr (M) b[0] &= z0, b[1] &= z0, b[2] &= z1, b[3] &= z1;
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
@@ -805,7 +839,7 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.full[i]), E4M3 ? 33 : 1);       // the bulk copies; each lane's scale bytes
             mbar_init(smem_u32(&sh.empty[i]), kWarps);
         }
         for (int i = 0; i < 2; ++i) {
@@ -849,7 +883,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const __grid_constant__ Ar
     pdl_trigger();
     const int hq = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)r * a.Hq + hq;
-    const int n = range_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B).splits;
+    const int n = splits_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B);
     if (!UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
     const float* pl = a.part_lse + row * a.cut.max_splits;
     const float* po = a.part_o + row * a.cut.max_splits * DK + lane * VE;
@@ -942,10 +976,12 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
         y = z;
     }
     c->s0 = std::min(2 * num_sms() / x, kMaxSplits);
+    c->most = kMaxSplits / c->s0;
+    c->by_wave = kv::fast_div(c->s0 * kMaxTiles);
     int64_t segs = (int64_t)max_blocks * c->spp;
     if (window > 0) segs = std::min<int64_t>(segs, (cdiv(window, B) + 1) * (int64_t)c->spp);
     const int tiles = static_cast<int>(cdiv(segs, c->spt));
-    c->max_splits = splits_of(tiles, c->s0);       // splits_of never falls as the tiles grow
+    c->max_splits = splits_of(tiles, *c);      // splits_of never falls as the tiles grow
     return 1;
 }
 
@@ -953,11 +989,12 @@ static bool make_map(CUtensorMap* m, const uint8_t* ptr, const Cache& c, const C
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     const int e = e4m3 ? 1 : 2, inner = std::min(dk, 128 / e);
-    cuuint64_t dims[4] = {(cuuint64_t)dk, (cuuint64_t)c.B, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks};
-    cuuint64_t strides[3] = {(cuuint64_t)c.st, (cuuint64_t)c.sh, (cuuint64_t)c.sb};
-    cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, 1, 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(ptr),
+    // (columns of a panel, tokens, panels, heads, pages): a box is every panel of a segment's rows
+    cuuint64_t dims[5] = {(cuuint64_t)inner, (cuuint64_t)c.B, (cuuint64_t)(dk / inner), (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks};
+    cuuint64_t strides[4] = {(cuuint64_t)c.st, (cuuint64_t)(inner * e), (cuuint64_t)c.sh, (cuuint64_t)c.sb};
+    cuuint32_t box[5] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, (cuuint32_t)(dk / inner), 1, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(ptr),
               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
