@@ -40,9 +40,11 @@ using kv::FastDiv;
 constexpr int kTile = 64;            // rows of a tile
 constexpr int kWarps = 4;            // consumer warps, 16 rows of a tile each
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMinTiles = 4;         // a chunk holds at least this many tiles, if the request has them
+constexpr int kMinTiles = 4;         // a chunk holds at least this many tiles, if the request has them, and twice
+constexpr int kFewSplits = 16;       // as many beyond this many chunks
 constexpr int kMaxTiles = 16;        // about as many tiles as a chunk holds, up to kMaxSplits chunks
-constexpr int kMaxSplits = 320;
+constexpr int kMaxSplits = 640;
+constexpr int kSpread = 2;           // items of one request on an SM
 constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or values) in a stage
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -75,8 +77,9 @@ __host__ __device__ __forceinline__ int divided(int x, const FastDiv& f) {
 }
 
 __host__ __device__ __forceinline__ int splits_of(int tiles, const Cut& c) {
-    const int fine = (tiles + kMinTiles - 1) / kMinTiles;
-    if (fine <= c.s0) return fine;
+    const int few = (tiles + kMinTiles - 1) / kMinTiles, fine = (tiles + 2 * kMinTiles - 1) / (2 * kMinTiles);
+    const int want = few <= kFewSplits ? few : fine > kFewSplits ? fine : kFewSplits;
+    if (want <= c.s0) return want;
     const int waves = divided(tiles + c.s0 * kMaxTiles - 1, c.by_wave);
     return c.s0 * (waves < c.most ? waves : c.most);
 }
@@ -244,10 +247,12 @@ struct Shape {
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
     // As many CTAs on an SM as leave each a few stages (228 KB of shared memory, 1 KB of it per CTA reserved) and the
-    // registers that its sums need: 15 warps have 128 a thread, 10 have 168, 5 have 255.
+    // registers that its sums need: 16 warps have 128 a thread, 12 have 168, 8 have 255.
     static constexpr int kControl = 4 * HT * DK + 1024 + 1024;         // queries, barriers and the join's; alignment
+    static constexpr int kWarpsFit = DK == 256 && (HT == 16 || !E4M3) ? 8 : DK == 256 || HT == 16 || (DK == 128 && !E4M3) ? 12 : 16;
     static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 1024 - kControl) / kStage; }
-    static constexpr int kCtas = DK <= 128 && HT == 8 && fit(3) >= 4 ? 3 : !(DK == 256 && HT == 16) && fit(2) >= 3 ? 2 : 1;
+    static constexpr int ctas(int c) { return c == 1 || (c * (kWarps + 1) <= kWarpsFit && fit(c) >= 3) ? c : ctas(c - 1); }
+    static constexpr int kCtas = ctas(6);
     static constexpr int kStages = fit(kCtas) < 8 ? fit(kCtas) : 8;
 };
 
@@ -753,7 +758,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             if (++slot == S::kStages) slot = 0, phase ^= 1;
         }
 
-        // join the four warps: references and sums, then the outputs through the stage
+        // join the warps: references and sums, then the outputs through the stage
         float* scratch = reinterpret_cast<float*>(ring_ptr + last_slot * S::kStage);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -789,40 +794,43 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 }
             }
             named_bar_sync(1, 32 * kWarps);
-            // 16 threads a head
-            const int hh = threadIdx.x >> 4, x = threadIdx.x & 15, hr = 8 * h + hh;
-            if (hr < heads) {
-                float M = sh.m[0][hr];
+            constexpr int TPH = 4 * kWarps;            // threads of a head
+            const int hh = threadIdx.x / TPH, x = threadIdx.x % TPH, hr = 8 * h + hh;
+            float M = sh.m[0][hr];
 #pragma unroll
-                for (int i = 1; i < kWarps; ++i) M = fmaxf(M, sh.m[i][hr]);
-                float L = 0.f, f[kWarps];
+            for (int i = 1; i < kWarps; ++i) M = fmaxf(M, sh.m[i][hr]);
+            float L = 0.f, f[kWarps];
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                L += sh.l[i][hr] * weight(sh.m[i][hr], M);
+                f[i] = weight(sh.f[i][hr], M);
+            }
+            float4 s[DK / (4 * TPH)];
+#pragma unroll
+            for (int k = 0; k < DK / (4 * TPH); ++k) {
+                s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
-                    L += sh.l[i][hr] * weight(sh.m[i][hr], M);
-                    f[i] = weight(sh.f[i][hr], M);
-                }
-                // L = 0: no score above -inf.  NaN goes through.
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                const int hq = head * a.group + h0 + hr;
-                const int64_t part = ((int64_t)w.r * a.Hq + hq) * c.max_splits + w.ch;
-                if (UP_IN(part, a.parts, a.status) && !dead) {
-                    if (x == 0) a.part_lse[part] = L == 0.f ? -INFINITY : M + log2f(L);
-#pragma unroll
-                    for (int d = 4 * x; d < DK; d += 64) {
-                        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int i = 0; i < kWarps; ++i) {
-                            const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * kLd<DK> + d);
-                            s.x += f[i] * y.x, s.y += f[i] * y.y, s.z += f[i] * y.z, s.w += f[i] * y.w;
-                        }
-                        *reinterpret_cast<float4*>(a.part_o + part * DK + d) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
-                    }
+                    const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * kLd<DK> + 4 * (x + k * TPH));
+                    s[k].x += f[i] * y.x, s[k].y += f[i] * y.y, s[k].z += f[i] * y.z, s[k].w += f[i] * y.w;
                 }
             }
+            if (h == NH - 1) {                         // the stage goes back before the sums leave
+                fence_proxy_async_smem();              // its next content comes by the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
+            }
+            const int64_t part = ((int64_t)w.r * a.Hq + head * a.group + h0 + hr) * c.max_splits + w.ch;
+            if (hr < heads && !dead && UP_IN(part, a.parts, a.status)) {
+                // L = 0: no score above -inf.  NaN goes through.
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                for (int k = 0; k < DK / (4 * TPH); ++k)
+                    *reinterpret_cast<float4*>(a.part_o + part * DK + 4 * (x + k * TPH)) =
+                        make_float4(s[k].x * inv, s[k].y * inv, s[k].z * inv, s[k].w * inv);
+                if (x == 0) a.part_lse[part] = L == 0.f ? -INFINITY : M + log2f(L);
+            }
         }
-        fence_proxy_async_smem();                      // the stage's next content comes by the async proxy
-        __syncwarp();
-        if (lane == 0 && n > 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
     }
     if (dead && threadIdx.x == 0) set_status(a.status, UP_DEV_WAIT_TIMEOUT);
 }
@@ -866,47 +874,78 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------------------------------------
-// One CTA per (query head, request).  Every warp finds the row's largest lse2 and the sum of its chunks'
-// weights; then the chunks i = g mod 16 are group g's, whose sums are added in the order of g.  A CTA has 16
-// warps with a group each, eight chunks in flight, where rows are few (4 requests of 128K: 152 chunks a row), and
-// 4 warps with four groups each where they are many: the order of the additions is the same.
+// The largest lse2 m of a row and the sum l of its chunks' weights, by every warp for itself; then the chunks
+// i = g mod 16 are group g's, whose sums are added in the order of g.  A row has W warps: 16, a group each and
+// eight chunks in flight, where rows are few (4 requests of 128K: 152 chunks a row); 4, with four groups each,
+// where they are many; 1 where no row can have more than 8 chunks (256 requests of 1K: 128 -> 112 us for the
+// whole call).  The order of the additions, and so the result, is the same.
 
-constexpr int kJoinGroups = 16;
+constexpr int kJoinGroups = 16, kJoinAlone = 8;
+static_assert(kJoinAlone <= kJoinGroups, "a group's sum is one chunk's where a warp adds them one after another");
+
+template <int DK>
+struct Row {
+    static constexpr int E = DK / 32, VE = E < 4 ? E : 4, V = E / VE;      // a lane's columns: V vectors of VE floats
+    using Vec = typename std::conditional<VE == 2, float2, float4>::type;
+    float x[E];
+    __device__ __forceinline__ void load(const float* row, int lane) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Vec y = *reinterpret_cast<const Vec*>(row + v * 32 * VE + lane * VE);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) x[v * VE + e] = reinterpret_cast<const float*>(&y)[e];
+        }
+    }
+    __device__ __forceinline__ void store(float* row, int lane) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Vec y;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) reinterpret_cast<float*>(&y)[e] = x[v * VE + e];
+            *reinterpret_cast<Vec*>(row + v * 32 * VE + lane * VE) = y;
+        }
+    }
+    // the result row; l = 0: no score above -inf.  NaN goes through.
+    __device__ __forceinline__ void put(const Args& a, int64_t row, int lane, float m, float l) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + (row * DK + v * 32 * VE + lane * VE) / 2;
+#pragma unroll
+            for (int e = 0; e < VE; e += 2) out[e / 2] = bf16x2(x[v * VE + e] * inv, x[v * VE + e + 1] * inv);
+        }
+        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+};
 
 template <int DK, int W>
-__global__ void __launch_bounds__(32 * W) join_kernel(const __grid_constant__ Args a) {
-    constexpr int GPW = kJoinGroups / W, E = DK / 32, U = (W == 16 ? 8 : 2) / (E == 8 ? 2 : 1);
-    constexpr int VE = E < 4 ? E : 4, V = E / VE;      // a lane's columns: V vectors of VE floats
-    using Vec = typename std::conditional<VE == 2, float2, float4>::type;
-    __shared__ alignas(16) float sums[kJoinGroups][DK];
+__global__ void __launch_bounds__(W == 16 ? 512 : 128) join_kernel(const __grid_constant__ Args a) {
+    constexpr int GPW = W > 1 ? kJoinGroups / W : 1;                   // groups of a warp
+    constexpr int U = (W == 16 ? 8 : W == 4 ? 2 : 8) / (DK == 256 ? 2 : 1);
+    __shared__ alignas(16) float sums[W > 1 ? kJoinGroups : 1][DK];
     pdl_wait();
     pdl_trigger();
-    const int hq = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)r * a.Hq + hq;
-    const int n = splits_of(a.cut, length_of(a, r), (int64_t)a.max_blocks * a.cut.B);
-    if (!UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
+    const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
+    const int64_t row = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.R * a.Hq || !UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
+    const int n = splits_of(a.cut, length_of(a, static_cast<int>(row / a.Hq)), (int64_t)a.max_blocks * a.cut.B);
     const float* pl = a.part_lse + row * a.cut.max_splits;
-    const float* po = a.part_o + row * a.cut.max_splits * DK + lane * VE;
-    float s[GPW][E], l = 0.f, m = -INFINITY;
+    const float* po = a.part_o + row * a.cut.max_splits * DK;
+    float m = -INFINITY, l = 0.f;
+    Row<DK> s[GPW];
 #pragma unroll
     for (int i = 0; i < GPW; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[i][e] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += kJoinGroups * U) {
-        float x[GPW][U][E], f[GPW][U];                 // on their way while the weights are found
+        for (int e = 0; e < Row<DK>::E; ++e) s[i].x[e] = 0.f;
+    constexpr int STEP = W > 1 ? kJoinGroups : 1;
+    for (int i0 = 0; i0 < n; i0 += STEP * U) {
+        Row<DK> x[GPW][U];                             // on their way while the weights are found
 #pragma unroll
         for (int i = 0; i < GPW; ++i)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int at = i0 + u * kJoinGroups + warp + i * W;
-                f[i][u] = at < n ? pl[at] : -INFINITY;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (at < n) {
-                        const Vec y = *reinterpret_cast<const Vec*>(po + (int64_t)at * DK + v * 32 * VE);
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) x[i][u][v * VE + e] = reinterpret_cast<const float*>(&y)[e];
-                    }
+                const int at = i0 + u * STEP + warp + i * W;
+                if (at < n) x[i][u].load(po + (int64_t)at * DK, lane);
             }
         if (i0 == 0) {
             for (int i = lane; i < n; i += 32) m = fmaxf(m, pl[i]);
@@ -919,33 +958,31 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const __grid_constant__ Ar
 #pragma unroll
         for (int i = 0; i < GPW; ++i)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * kJoinGroups + warp + i * W < n) {
-                    const float w = weight(f[i][u], m);
+            for (int u = 0; u < U; ++u) {
+                const int at = i0 + u * STEP + warp + i * W;
+                if (at < n) {
+                    const float f = weight(pl[at], m);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) s[i][e] += w * x[i][u][e];
+                    for (int e = 0; e < Row<DK>::E; ++e)       // alone: a group's sum is one product, added as the others are
+                        s[i].x[e] = W > 1 ? __fmaf_rn(f, x[i][u].x[e], s[i].x[e]) : __fadd_rn(s[i].x[e], __fmul_rn(f, x[i][u].x[e]));
                 }
+            }
     }
+    if constexpr (W > 1) {
 #pragma unroll
-    for (int i = 0; i < GPW; ++i)
+        for (int i = 0; i < GPW; ++i) s[i].store(sums[warp + i * W], lane);
+        __syncthreads();
+        if (warp != 0) return;
+        Row<DK> y;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            Vec y;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) reinterpret_cast<float*>(&y)[e] = s[i][v * VE + e];
-            *reinterpret_cast<Vec*>(&sums[warp + i * W][v * 32 * VE + lane * VE]) = y;
-        }
-    __syncthreads();
-    const float inv = l == 0.f ? 0.f : 1.f / l;        // l = 0: no score above -inf.  NaN goes through.
-    if (threadIdx.x < DK / 2) {
-        float x = 0.f, y = 0.f;
+        for (int e = 0; e < Row<DK>::E; ++e) s[0].x[e] = 0.f;
         for (int g = 0; g < min(kJoinGroups, n); ++g) {
-            const float2 z = *reinterpret_cast<const float2*>(&sums[g][2 * threadIdx.x]);
-            x += z.x, y += z.y;
+            y.load(sums[g], lane);
+#pragma unroll
+            for (int e = 0; e < Row<DK>::E; ++e) s[0].x[e] = __fadd_rn(s[0].x[e], y.x[e]);
         }
-        reinterpret_cast<uint32_t*>(a.out)[row * (DK / 2) + threadIdx.x] = bf16x2(x * inv, y * inv);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    s[0].put(a, row, lane, m, l);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -969,13 +1006,13 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
     c->by_segp = kv::fast_div(c->segp);
     // the least number of chunks that makes one request's items a multiple of two CTAs on every SM
     const int group = Hq / Hkv, units = Hkv * (group <= 8 ? 1 : static_cast<int>(cdiv(group, 16)));
-    int x = 2 * num_sms(), y = units;
+    int x = kSpread * num_sms(), y = units;
     while (y) {
         const int z = x % y;
         x = y;
         y = z;
     }
-    c->s0 = std::min(2 * num_sms() / x, kMaxSplits);
+    c->s0 = std::min(kSpread * num_sms() / x, kMaxSplits);
     c->most = kMaxSplits / c->s0;
     c->by_wave = kv::fast_div(c->s0 * kMaxTiles);
     int64_t segs = (int64_t)max_blocks * c->spp;
@@ -1004,7 +1041,7 @@ template <int DK, bool E4M3, int HT>
 static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
     constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    static_assert(Shape<DK, E4M3, HT>::kStage >= 32 * kLd<DK> * 4, "the join of the warps fits a stage");
+    static_assert(Shape<DK, E4M3, HT>::kStage >= 8 * kWarps * kLd<DK> * 4, "the join of the warps fits a stage");
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
@@ -1012,6 +1049,20 @@ static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, cons
     });
     if (attr != cudaSuccess) return attr;
     return launch_pdl(split_kernel<DK, E4M3, HT>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
+}
+
+// The join asks for the split's division of an SM's memory (nearly all of it shared): with the default one an SM
+// would have to run empty between the two.
+template <int DK, int W>
+static cudaError_t launch_join(const Args& a, int64_t ctas, cudaStream_t st) {
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(join_kernel<DK, W>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
+    });
+    if (attr != cudaSuccess) return attr;
+    return launch_pdl(join_kernel<DK, W>, dim3(static_cast<unsigned>(ctas)), dim3(W == 16 ? 512 : 128), 0, st, a);
 }
 
 template <int DK>
@@ -1022,9 +1073,9 @@ static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args
     else
         e = e4m3 ? launch_split<DK, true, 16>(k, v, a, st) : launch_split<DK, false, 16>(k, v, a, st);
     if (e != cudaSuccess) return e;
-    const bool few = (int64_t)a.Hq * a.R <= 4 * num_sms();
-    return few ? launch_pdl(join_kernel<DK, 16>, dim3(a.Hq, a.R), dim3(512), 0, st, a)
-               : launch_pdl(join_kernel<DK, 4>, dim3(a.Hq, a.R), dim3(128), 0, st, a);
+    const int64_t rows = (int64_t)a.Hq * a.R;
+    if (rows <= 4 * num_sms()) return launch_join<DK, 16>(a, rows, st);
+    return a.cut.max_splits > kJoinAlone ? launch_join<DK, 4>(a, rows, st) : launch_join<DK, 1>(a, cdiv(rows, 4), st);
 }
 
 }  // namespace decode
