@@ -122,10 +122,11 @@ struct Args {
 __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
 
 // ------------------------------------------------------------------------------------------------
-// the walk over a CTA's run of items.  Item order: request, unit (KV head, head tile), chunk.
+// the walk over a CTA's run of items.  Item order: request, KV head, chunk, head tile (the tiles of queries that read
+// the same keys follow one another: the second finds them in L2).
 
 struct Walk {
-    int r, unit, ch;           // unit: KV head * head_tiles + head tile
+    int r, head, ch, ht;       // request, KV head, chunk, head tile
     Range g;
     int q, rem, err;           // tiles = q * splits + rem: chunk ch starts at tile ch q + floor(ch rem / splits);
                                // err = ch rem mod splits
@@ -133,7 +134,6 @@ struct Walk {
     int64_t start, end;        // tiles before the item, and where the run ends
     int next_len;
 
-    __device__ __forceinline__ int units(const Args& a) const { return a.c.Hkv * a.head_tiles; }
     // an item belongs to the run that its middle falls into
     __device__ __forceinline__ bool live(const Args& a) const { return r < a.R && 2 * start + n < 2 * end; }
 
@@ -149,12 +149,14 @@ struct Walk {
         g.splits = splits_of(g.tiles, a.cut);
         q = g.splits ? static_cast<int>(static_cast<unsigned>(g.tiles) / static_cast<unsigned>(g.splits)) : 0;
         rem = g.tiles - q * g.splits;
-        unit = 0;
+        head = ht = 0;
         chunk(0, 0, 0);
         next_len = r + 1 < a.R ? length_of(a, r + 1) : 0;
     }
     __device__ __forceinline__ void next(const Args& a) {
         start += n;
+        if (++ht < a.head_tiles) return;
+        ht = 0;
         if (++ch < g.splits) {
             t0 += n;
             err += rem;
@@ -163,7 +165,7 @@ struct Walk {
             return;
         }
         chunk(0, 0, 0);
-        if (++unit < units(a)) return;
+        if (++head < a.c.Hkv) return;
         do {
             if (++r >= a.R) return;
             enter(a, next_len);
@@ -173,8 +175,8 @@ struct Walk {
 
 // x / y of numbers that mostly fit 32 bits (a 64-bit division takes a third of a microsecond, here in the way of
 // the first copy)
-__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
-    return x >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
 
 // Every warp finds its CTA's run: the tiles of all requests, then the first item whose middle lies in its
@@ -183,7 +185,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int y) {
 __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     const int lane = threadIdx.x & 31;
     const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
-    const int units = w.units(a);
+    const int units = a.c.Hkv * a.head_tiles;
     // 32 requests at a time: a lane's length, its tiles and the tiles up to it.  Up to 32 requests are read once.
     int len = 0, mine = 0, upto = 0;
     auto scan = [&](int r0) {
@@ -227,12 +229,12 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     }
     w.enter(a, found);
     const int64_t local = want - before;
-    w.unit = static_cast<int>(quotient(local, w.g.tiles));
-    const int u = static_cast<int>(local - (int64_t)w.unit * w.g.tiles);
-    const int i = max(0, static_cast<int>(quotient((int64_t)u * w.g.splits, w.g.tiles)) - 1);
+    const int64_t per_head = (int64_t)w.g.tiles * a.head_tiles;
+    w.head = static_cast<int>(quotient(local, per_head));
+    const int i = max(0, static_cast<int>(quotient((local - w.head * per_head) * w.g.splits, per_head)) - 1);
     const int whole = static_cast<int>(static_cast<unsigned>(i * w.rem) / static_cast<unsigned>(w.g.splits));
     w.chunk(i, whole, i * w.rem - whole * w.g.splits);
-    w.start = before + (int64_t)w.unit * w.g.tiles + w.t0;
+    w.start = before + w.head * per_head + (int64_t)w.t0 * a.head_tiles;
     while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
 }
 
@@ -380,11 +382,11 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
         }
     };
     int pages_next = fetch(nw, 0);
-    int q_r = -1, q_unit = -1;                                          // whose queries were sent last
+    int q_r = -1, q_head = -1, q_ht = -1;                               // whose queries were sent last
     for (; w.live(a) && !dead; w.next(a)) {
-        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
-        if (w.r != q_r || w.unit != q_unit) {
-            q_r = w.r, q_unit = w.unit;
+        const int head = w.head, h0 = w.ht * HT;
+        if (w.r != q_r || head != q_head || w.ht != q_ht) {
+            q_r = w.r, q_head = head, q_ht = w.ht;
             const int bytes = min(HT, a.group - h0) * DK * 2;
             if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
             if (lane == 0) {
@@ -538,12 +540,12 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         if (++qslot == 2) qslot = 0, qphase ^= 1;
     };
 
-    int q_r = -1, q_unit = -1;                         // whose queries the registers hold
+    int q_r = -1, q_head = -1, q_ht = -1;              // whose queries the registers hold
     for (; w.live(a); w.next(a)) {
-        const int head = w.unit / a.head_tiles, h0 = (w.unit - head * a.head_tiles) * HT;
+        const int head = w.head, h0 = w.ht * HT;
         const int heads = min(HT, a.group - h0);
-        if (w.r != q_r || w.unit != q_unit) {
-            q_r = w.r, q_unit = w.unit;
+        if (w.r != q_r || head != q_head || w.ht != q_ht) {
+            q_r = w.r, q_head = head, q_ht = w.ht;
             load_queries();
         }
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
