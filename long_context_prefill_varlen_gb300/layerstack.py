@@ -10,7 +10,8 @@ This module is the consumer of the drop step, not part of it: its layers are lib
 GEMMs through torch.matmul, PyTorch's varlen flash-attention forward, torch elementwise ops), with
 random weights, so that the time a drop saves on a real layer stack can be measured.  The drop step
 itself (score, top-p select, compaction with its metadata and drop history, Eq. 8 scatter) runs in
-libuniprefill through DropStep.
+libuniprefill through DropStep, and so do the paged key-value cache that a prefill can fill (StackCache:
+every layer holds the tokens its stream held, Eqs. 16-17) and the attention of the tokens decoded from it.
 
 Layer l (pre-norm LLaMA block, GQA, rotary positions):
     x = h + Wo . attn(rope(Wq . rms(h)), rope(Wk . rms(h)), Wv . rms(h))     causal per request
@@ -32,6 +33,8 @@ from dataclasses import dataclass
 
 import torch
 
+from . import (up_kv_scale_row, up_kv_write, up_paged_decode, up_paged_decode_workspace_bytes, up_read_status,
+               up_seqused, up_slot_mapping, up_status_string)
 from .step import DropStep
 
 
@@ -94,6 +97,85 @@ def stack_flops(lengths, g: StackGeometry, L, drops=()):
     return total
 
 
+# ------------------------------------------------------------------------------------------ the cache
+
+class StackCache:
+    """The paged key-value cache of an L-layer stack for R requests of up to `max_len` tokens each: per
+    layer keys and values [num_blocks, Hkv, B, dk], in bf16 or in e4m3 with a scale byte per row, one block
+    table for all layers, and the drop history that says how many tokens each layer holds.
+
+    A layer's cache positions count the tokens of its own stream: the i-th token that a request has at that
+    layer is position i, whatever its rotary position.  A prefill's dropped tokens therefore leave no holes, and
+    the tokens decoded later follow at up_seqused's length (Eq. 17)."""
+
+    def __init__(self, L, R, Hkv, dk, max_len, B=16, e4m3=True, device="cuda"):
+        dev = torch.device(device)
+        self.L, self.R, self.B, self.max_blocks = L, R, B, -(-int(max_len) // B)
+        num_blocks = max(1, R * self.max_blocks)
+        i32 = dict(device=dev, dtype=torch.int32)
+        self.block_table = torch.arange(num_blocks, **i32).view(R, self.max_blocks)
+        dtype = torch.uint8 if e4m3 else torch.bfloat16
+        self.layers = []
+        for _ in range(L):
+            k, v = (torch.zeros(num_blocks, Hkv, B, dk, device=dev, dtype=dtype) for _ in "kv")
+            scales = {}
+            if e4m3:
+                k, v = k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+                rows = (num_blocks, Hkv, up_kv_scale_row(B))
+                scales = {s: torch.zeros(rows, device=dev, dtype=torch.uint8) for s in ("k_scale", "v_scale")}
+            self.layers.append((k, v, scales))
+        self.kept_len = torch.zeros(L, R, **i32)
+        self.drop_layer = torch.zeros(L, device=dev, dtype=torch.uint8)
+        self.orig_len, self.kv_len = torch.zeros(R, **i32), torch.zeros(R, **i32)
+        self.status = torch.zeros(1, **i32)
+        self.one_each = torch.arange(R + 1, **i32)
+        self.ws = None
+
+    def start(self, cu_seqlens):
+        """Forget what was cached; the coming prefill's requests have these lengths."""
+        self.drop_layer.zero_()
+        self.orig_len.copy_(cu_seqlens.diff())
+        self.kv_len.copy_(self.orig_len)
+
+    def record_drop(self, step):
+        """Take over the drop history row that a DropStep's compaction wrote (section 3.5)."""
+        self.kept_len[step.layer].copy_(step.kept_len[step.layer])
+        self.drop_layer[step.layer:step.layer + 1].copy_(step.drop_layer[step.layer:step.layer + 1])
+
+    def slots(self, cu_seqlens, T):
+        """Eq. 16 for a packed stream of T tokens whose requests start at cache position 0."""
+        starts = cu_seqlens[:-1].long().repeat_interleave(cu_seqlens.diff().long(), output_size=T)
+        positions = torch.arange(T, device=starts.device) - starts
+        out = torch.empty(T, device=starts.device, dtype=torch.int64)
+        up_slot_mapping(positions, cu_seqlens, self.block_table, self.B, out, self.status)
+        return out
+
+    def write(self, layer, k, v, slots):
+        kc, vc, scales = self.layers[layer]
+        up_kv_write(k, v, slots, kc, vc, self.status, **scales)
+
+    def seqused(self, layer):
+        """Tokens that each request has at `layer` (Eq. 17), the one being decoded included."""
+        out = torch.empty_like(self.kv_len)
+        up_seqused(self.kept_len, self.drop_layer, layer, self.orig_len, self.kv_len, out)
+        return out
+
+    def attend(self, layer, q, seqused, sm_scale):
+        kc, vc, scales = self.layers[layer]
+        R, Hq, dk = q.shape
+        nbytes = up_paged_decode_workspace_bytes(R, Hq, kc.shape[1], dk, self.B, self.max_blocks)
+        if self.ws is None or self.ws.numel() < nbytes:
+            self.ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+        out = torch.empty_like(q)
+        up_paged_decode(q, kc, vc, self.block_table, seqused, out, self.ws, self.status, sm_scale=sm_scale, **scales)
+        return out
+
+    def check(self, stream=None):
+        code = up_read_status(self.status, stream)
+        if code != 0:
+            raise RuntimeError(f"device status {code}: {up_status_string(code, True)}")
+
+
 # ------------------------------------------------------------------------------------------ the stack
 
 def _rms(x, eps):
@@ -148,8 +230,8 @@ class RandomLlamaStack:
                                     wo=w(g.Hq * g.dk, g.d, res), wgu=w(g.d, 2 * g.ffn), wd=w(g.ffn, g.d, res)))
 
     # one sublayer each; T = rows of the stream they are given
-    def attention_sublayer(self, layer, h, positions, cu_seqlens, max_len):
-        """x = h + Wo . attn(...); also returns the rotated q [T, Hq, dk] and k [T, Hkv, dk]"""
+    def qkv(self, layer, h, positions):
+        """rotated q [T, Hq, dk] and k [T, Hkv, dk], and v, of the rows h"""
         g, Wt = self.g, self.layers[layer]
         T = h.shape[0]
         a = _rms(h, g.eps)
@@ -157,6 +239,16 @@ class RandomLlamaStack:
         q = apply_rope(torch.matmul(a, Wt["wq"]).view(T, g.Hq, g.dk), cos, sin)
         k = apply_rope(torch.matmul(a, Wt["wk"]).view(T, g.Hkv, g.dk), cos, sin)
         v = torch.matmul(a, Wt["wv"]).view(T, g.Hkv, g.dk)
+        return q, k, v
+
+    def attention_sublayer(self, layer, h, positions, cu_seqlens, max_len, cache=None, slots=None):
+        """x = h + Wo . attn(...); also returns the rotated q [T, Hq, dk] and k [T, Hkv, dk].  With a
+        StackCache, k and v go to its rows `slots` as well."""
+        g, Wt = self.g, self.layers[layer]
+        T = h.shape[0]
+        q, k, v = self.qkv(layer, h, positions)
+        if cache is not None:
+            cache.write(layer, k, v, slots)
         o = varlen_causal_attention(q, k, v, cu_seqlens, max_len, g.dk ** -0.5)
         x = h + torch.matmul(o.reshape(T, g.Hq * g.dk), Wt["wo"])
         return x, q, k
@@ -168,14 +260,15 @@ class RandomLlamaStack:
         return x + torch.matmul(act, Wt["wd"])
 
     def forward(self, hidden, positions, cu_seqlens, max_len, drops=(), upto=None, G=64, n=128, A=128,
-                keep_scored=False):
+                keep_scored=False, cache=None):
         """Run layers [0, upto) (all by default) over the packed stream `hidden` [T, d] bf16 with
         `positions` [T] int64 and `cu_seqlens` [R+1] int32 (device); `max_len` bounds every request's
         length.  `drops` lists (layer, p) in increasing layer order.  Returns the full-length output
         (a new tensor; `hidden` is not written) and, per drop, a dict with its DropStep, the kept token
         count and (keep_scored) the rotated q and k it was scored on, and the stream x and positions it
         compacted.  Each drop synchronises the host
-        once, to learn the compacted stream's length."""
+        once, to learn the compacted stream's length.  With a StackCache, every layer's keys and values are
+        written to it as the layer's stream holds them, and the drops to its history, for decode()."""
         upto = self.L if upto is None else upto
         drops = list(drops)
         h = hidden.clone()
@@ -183,8 +276,12 @@ class RandomLlamaStack:
         k = 0
         stack_of_blocks = []          # (block input buffer H^(b,0), DropStep), innermost last
         info = []
+        slots = None
+        if cache is not None:
+            cache.start(cu)
+            slots = cache.slots(cu, T)
         for layer in range(upto):
-            x, q, kk = self.attention_sublayer(layer, h, pos, cu, max_len)
+            x, q, kk = self.attention_sublayer(layer, h, pos, cu, max_len, cache, slots)
             if k < len(drops) and drops[k][0] == layer:
                 p = drops[k][1]
                 step = DropStep(cu, T, self.g.Hq, self.g.Hkv, self.g.dk, self.g.d, G=G, n=n, A=A, p=p, L=self.L,
@@ -200,6 +297,9 @@ class RandomLlamaStack:
                 x = step.out_hidden[:T]
                 pos = step.out_positions[:T]
                 cu = step.new_cu
+                if cache is not None:
+                    cache.record_drop(step)
+                    slots = cache.slots(cu, T)
                 k += 1
             h = self.ffn_sublayer(layer, x)
         for block_in, step in reversed(stack_of_blocks):       # Eq. 8, innermost block first
@@ -208,3 +308,22 @@ class RandomLlamaStack:
         for _, step in stack_of_blocks:
             step.check()
         return h, info
+
+    def decode(self, hidden, positions, cache):
+        """One new token per request through all layers: hidden [R, d] bf16, positions [R] int64 (rotary: the
+        tokens the request has had so far, dropped ones included).  Each layer appends the token's key and value to
+        its part of the cache and attends over the tokens it holds.  Returns the token's output [R, d]."""
+        g = self.g
+        R = hidden.shape[0]
+        cache.kv_len.add_(1)
+        h = hidden
+        for layer in range(self.L):
+            q, k, v = self.qkv(layer, h, positions)
+            seq = cache.seqused(layer)
+            slot = torch.empty(R, device=h.device, dtype=torch.int64)
+            up_slot_mapping(seq.long() - 1, cache.one_each, cache.block_table, cache.B, slot, cache.status)
+            cache.write(layer, k, v, slot)
+            o = cache.attend(layer, q, seq, g.dk ** -0.5)
+            x = h + torch.matmul(o.view(R, g.Hq * g.dk), self.layers[layer]["wo"])
+            h = self.ffn_sublayer(layer, x)
+        return h
