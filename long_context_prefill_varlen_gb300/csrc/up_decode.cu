@@ -11,9 +11,9 @@
 // A cached number is used once per query head of its group, so HBM bounds the call from the first
 // thousand positions on: 2 dk (dk + 1) bytes a row in bf16 (e4m3).  split_kernel keeps enough copies in flight
 // and the rest out of their way:
-//  * persistent CTAs take runs of (request, chunk, head) items of equal length in tiles; every CTA finds its
-//    run from seqused itself, so no launch plans and the host never waits for a length;
-//  * a producer warp walks the run and fills a ring of stages (the K and V tile of one head) by TMA, one
+//  * persistent CTAs take runs of (request, head, chunk) items of equal length in tiles, found from seqused on the
+//    device: the host never waits for a length;
+//  * a producer warp walks the run, tells the consumers of each item and fills a ring of stages (the K and V tile of one head) by TMA, one
 //    box per page, swizzled so that ldmatrix reads it without bank conflicts; the ring
 //    runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
@@ -45,6 +45,7 @@ constexpr int kFewSplits = 16;       // as many beyond this many chunks
 constexpr int kMaxTiles = 16;        // about as many tiles as a chunk holds, up to kMaxSplits chunks
 constexpr int kMaxSplits = 640;
 constexpr int kSpread = 2;           // items of one request on an SM
+constexpr int kItems = 4;            // items that the producer may be ahead
 constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or values) in a stage
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -179,9 +180,26 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
     return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
 
-// Every warp finds its CTA's run: the tiles of all requests, then the first item whose middle lies in its
-// share.  Items stay whole, so a run is off by at most one item, and equal items as many as CTAs (or a
-// multiple) fall one (or that many) to each.
+// the first item whose middle lies at or after `want` tiles: in request r, which starts at `before` of them
+__device__ __forceinline__ void seek(const Args& a, Walk& w, int64_t want, int64_t end, int r, int64_t before, int len) {
+    w.r = r;
+    w.end = end;
+    w.enter(a, len);
+    const int64_t per_head = (int64_t)w.g.tiles * a.head_tiles;
+    const int64_t local = want - before;
+    w.head = static_cast<int>(quotient(local, per_head));
+    const int i = max(0, static_cast<int>(quotient((local - w.head * per_head) * w.g.splits, per_head)) - 1);
+    const int whole = static_cast<int>(static_cast<unsigned>(i * w.rem) / static_cast<unsigned>(w.g.splits));
+    w.chunk(i, whole, i * w.rem - whole * w.g.splits);
+    w.start = before + w.head * per_head + (int64_t)w.t0 * a.head_tiles;
+    while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
+}
+
+// The CTA's run, found by its producer: the tiles of all requests, then the items whose middles lie in the CTA's
+// share.  Items stay whole, so a run is off by at most one, and equal items as many as CTAs (or a multiple) fall
+// one (or that many) to each.  CTAs move equal tiles in unequal time (64 requests of 0-8K in e4m3: the slowest 25%
+// above the mean), but what is left at the end has the memory to itself: handing out shorter runs by a ticket
+// measured 1 to 13% slower.
 __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     const int lane = threadIdx.x & 31;
     const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
@@ -190,7 +208,7 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     int len = 0, mine = 0, upto = 0;
     auto scan = [&](int r0) {
         len = r0 + lane < a.R ? length_of(a, r0 + lane) : 0;
-        upto = mine = range_of(a.cut, len, cap).tiles;         // at most 2^25 a request
+        upto = mine = range_of(a.cut, len, cap).tiles;         // at most 2^26 a request
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -201,41 +219,29 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     for (int r0 = 0; r0 < a.R; r0 += 32) {
         scan(r0);
         total += __shfl_sync(0xffffffffu, upto, 31);
-        if ((len < 0 || len > cap) && blockIdx.x == 0 && threadIdx.x < 32) set_status(a.status, UP_DEV_BAD_LENGTH);
+        if ((len < 0 || len > cap) && blockIdx.x == 0) set_status(a.status, UP_DEV_BAD_LENGTH);
     }
     total *= units;
     // neighbours in the order of runs are half a grid apart: a short list of items leaves no SM with two
     // before every SM has one
     const int n = gridDim.x, half = (n + 1) / 2, b = blockIdx.x;
     const int64_t at = b < half ? 2 * b : 2 * (b - half) + 1;
-    w.end = quotient(total * (at + 1), n);
-    const int64_t want = quotient(total * at, n);
-    w.start = 0;
+    const int64_t end = quotient(total * (at + 1), n), want = quotient(total * at, n);
     w.r = a.R;
-    if (want >= w.end) return;
+    w.start = w.end = 0;
+    if (want >= end) return;
     int64_t before = 0;        // tiles of the requests before
-    int found = 0;
     for (int r0 = 0; r0 < a.R; r0 += 32) {
         if (a.R > 32) scan(r0);
         const uint32_t hit = __ballot_sync(0xffffffffu, before + (int64_t)upto * units > want);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            w.r = r0 + l;
             before += (int64_t)__shfl_sync(0xffffffffu, upto - mine, l) * units;
-            found = __shfl_sync(0xffffffffu, len, l);
-            break;
+            seek(a, w, want, end, r0 + l, before, __shfl_sync(0xffffffffu, len, l));
+            return;
         }
         before += (int64_t)__shfl_sync(0xffffffffu, upto, 31) * units;
     }
-    w.enter(a, found);
-    const int64_t local = want - before;
-    const int64_t per_head = (int64_t)w.g.tiles * a.head_tiles;
-    w.head = static_cast<int>(quotient(local, per_head));
-    const int i = max(0, static_cast<int>(quotient((local - w.head * per_head) * w.g.splits, per_head)) - 1);
-    const int whole = static_cast<int>(static_cast<unsigned>(i * w.rem) / static_cast<unsigned>(w.g.splits));
-    w.chunk(i, whole, i * w.rem - whole * w.g.splits);
-    w.start = before + w.head * per_head + (int64_t)w.t0 * a.head_tiles;
-    while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -250,7 +256,7 @@ struct Shape {
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
     // As many CTAs on an SM as leave each a few stages (228 KB of shared memory, 1 KB of it per CTA reserved) and the
     // registers that its sums need: 16 warps have 128 a thread, 12 have 168, 8 have 255.
-    static constexpr int kControl = 4 * HT * DK + 1024 + 1024;         // queries, barriers and the join's; alignment
+    static constexpr int kControl = 4 * HT * DK + 1536 + 1024;         // queries; items, barriers and the join's; alignment
     static constexpr int kWarpsFit = DK == 256 && (HT == 16 || !E4M3) ? 8 : DK == 256 || HT == 16 || (DK == 128 && !E4M3) ? 12 : 16;
     static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 1024 - kControl) / kStage; }
     static constexpr int ctas(int c) { return c == 1 || (c * (kWarps + 1) <= kWarpsFit && fit(c) >= 3) ? c : ctas(c - 1); }
@@ -329,11 +335,19 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 // ------------------------------------------------------------------------------------------------
 // shared memory of a CTA: the stages, then this
 
+// what the consumers are told of an item; n = 0: no more
+struct Item {
+    int r, head, ch, h0;                       // h0: first query head of its tile, in the group
+    int t0, n, tiles, seg0;                    // its tiles, and the request's
+    int lo, len, fresh, unused;                // fresh: its queries are not the last item's
+};
+
 template <int DK, int HT, int NS>
 struct Control {
-    alignas(16) uint16_t q[2][HT * DK];        // the item's queries, double-buffered
+    alignas(16) uint16_t q[2][HT * DK];        // queries, double-buffered
+    Item item[kItems];
     float m[kWarps][16], f[kWarps][16], l[kWarps][16];
-    uint64_t full[NS], empty[NS], qfull[2], qempty[2];
+    uint64_t full[NS], empty[NS], qfull[2], qempty[2], ifull[kItems], iempty[kItems], joined;
     int abort;
 };
 
@@ -351,41 +365,36 @@ struct Sizes {
 
 template <int DK, bool E4M3, int HT>
 __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
-                        Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh, Walk w) {
+                        Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
     const int lane = threadIdx.x & 31;
     const Cut& c = a.cut;
-    int slot = 0, qslot = 0;
-    uint32_t phase = 0, qphase = 0;
+    int slot = 0, qslot = 0, islot = 0;
+    uint32_t phase = 0, qphase = 0, iphase = 0;
     int64_t issued = 0;
     bool dead = false;
     const int per = (32 / c.spt) * c.spt, tiles_per = 32 / c.spt;      // table entries and tiles of a batch
     // the 16 scale bytes that this lane copies: of which segment of the tile, and from which byte of its part of a page
     const int per_seg = (c.seg + 15) / 16, sc_seg = lane / per_seg, sc_part = (lane - sc_seg * per_seg) * 16;
-    // the table entries of the run's segments, 32 (or the most that make whole tiles) at a time, one batch ahead
-    Walk nw = w;
-    int ntile = 0;                                                      // next batch: its item and first tile
+
+    Walk w;
+    find_run(a, w);
+    // the table entries of an item's segments, 32 (or the most that make whole tiles) at a time, one batch ahead
     auto fetch = [&](const Walk& x, int tile) {
         const int s = x.g.seg0 + (x.t0 + tile) * c.spt + lane;
         int page = -1;
-        if (x.live(a) && lane < per && s <= x.g.seg1) {
+        if (x.live(a) && tile < x.n && lane < per && s <= x.g.seg1) {
             const int64_t e = (int64_t)x.r * a.max_blocks + div_of(s, c.by_spp);
             page = UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
         }
         return page;
     };
-    auto step = [&]() {
-        ntile += tiles_per;
-        if (ntile >= nw.n) {
-            nw.next(a);
-            ntile = 0;
-        }
-    };
-    int pages_next = fetch(nw, 0);
+    int first_pages = fetch(w, 0);
     int q_r = -1, q_head = -1, q_ht = -1;                               // whose queries were sent last
-    for (; w.live(a) && !dead; w.next(a)) {
+    while (w.live(a) && !dead) {
         const int head = w.head, h0 = w.ht * HT;
-        if (w.r != q_r || head != q_head || w.ht != q_ht) {
+        const bool fresh_q = w.r != q_r || head != q_head || w.ht != q_ht;
+        if (fresh_q) {
             q_r = w.r, q_head = head, q_ht = w.ht;
             const int bytes = min(HT, a.group - h0) * DK * 2;
             if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
@@ -396,11 +405,16 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
             }
             if (++qslot == 2) qslot = 0, qphase ^= 1;
         }
-        const int n = w.n, t0 = w.t0;
-        int pages = -1;
-        for (int i = 0, j = tiles_per; i < n; ++i, ++j) {
-            const bool fresh = j == tiles_per;                          // a new batch
-            if (fresh) {
+        if (!mbar_wait(smem_u32(&sh.iempty[islot]), iphase ^ 1, &sh.abort)) break;
+        if (lane == 0) {
+            sh.item[islot] = Item{w.r, head, w.ch, h0, w.t0, w.n, w.g.tiles, w.g.seg0, w.g.lo, w.g.len, fresh_q, 0};
+            mbar_arrive(smem_u32(&sh.ifull[islot]));
+        }
+        if (++islot == kItems) islot = 0, iphase ^= 1;
+        const int n = w.n, t0 = w.t0, seg0 = w.g.seg0, seg1 = w.g.seg1;
+        int pages = first_pages, pages_next = -1;
+        for (int i = 0, j = 0; i < n; ++i, ++j) {
+            if (j == tiles_per) {                                       // a new batch
                 j = 0;
                 pages = pages_next;
             }
@@ -409,7 +423,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                 break;
             }
             // segments s0 .. s0 + ns - 1 of the request (in a page of several segments one: part of its page)
-            const int s0 = w.g.seg0 + (t0 + i) * c.spt, ns = min(c.spt, w.g.seg1 - s0 + 1);
+            const int s0 = seg0 + (t0 + i) * c.spt, ns = min(c.spt, seg1 - s0 + 1);
             const int part = c.spp == 1 ? 0 : s0 - div_of(s0, c.by_spp) * c.spp;
             const uint32_t stage = ring + slot * S::kStage, bar = smem_u32(&sh.full[slot]);
             const uint32_t sc = stage + 2 * S::kTileBytes + 16 * lane;
@@ -450,11 +464,15 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
             }
             ++issued;
             if (++slot == S::kStages) slot = 0, phase ^= 1;
-            if (fresh) {
-                step();
-                pages_next = fetch(nw, ntile);
-            }
+            if (j == 0) pages_next = fetch(w, i + tiles_per);           // the batch after this one
         }
+        // the next item, while this one's tiles are on their way
+        w.next(a);
+        first_pages = fetch(w, 0);
+    }
+    if (!dead && mbar_wait(smem_u32(&sh.iempty[islot]), iphase ^ 1, &sh.abort) && lane == 0) {
+        sh.item[islot].n = 0;
+        mbar_arrive(smem_u32(&sh.ifull[islot]));
     }
     if (dead || sh.abort) {
         // let the copies in flight land before the CTA goes (they write its shared memory)
@@ -467,8 +485,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
 }
 
 template <int DK, bool E4M3, int HT>
-__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh,
-                        Walk w) {
+__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
     constexpr int KS = DK / 16, NH = HT / 8;           // steps of 16 columns; tiles of 8 query heads
     constexpr int PB = S::kPanelBytes;
@@ -540,14 +557,30 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         if (++qslot == 2) qslot = 0, qphase ^= 1;
     };
 
-    int q_r = -1, q_head = -1, q_ht = -1;              // whose queries the registers hold
-    for (; w.live(a); w.next(a)) {
-        const int head = w.head, h0 = w.ht * HT;
-        const int heads = min(HT, a.group - h0);
-        if (w.r != q_r || head != q_head || w.ht != q_ht) {
-            q_r = w.r, q_head = head, q_ht = w.ht;
-            load_queries();
+    // the consumer warps meet: a bounded wait like the others (a warp that has given up may have left)
+    uint32_t jphase = 0;
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.joined));
+        if (!dead && !mbar_wait(smem_u32(&sh.joined), jphase, &sh.abort)) dead = true;
+        jphase ^= 1;
+    };
+
+    int islot = 0;
+    uint32_t iphase = 0;
+    for (;;) {
+        if (!mbar_wait(smem_u32(&sh.ifull[islot]), iphase, &sh.abort)) {
+            dead = true;
+            break;
         }
+        const Item it = sh.item[islot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.iempty[islot]));
+        if (++islot == kItems) islot = 0, iphase ^= 1;
+        if (it.n == 0) break;
+        const int heads = min(HT, a.group - it.h0);
+        if (it.fresh) load_queries();
+
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
         float o[NH][KS][4];
@@ -567,7 +600,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             }
         }
 
-        const int n = w.n, t0 = w.t0;
+        const int n = it.n, t0 = it.t0;
         int last_slot = 0;
         for (int i = 0; i < n; ++i) {
             if (!dead && !mbar_wait(smem_u32(&sh.full[slot]), phase, &sh.abort)) dead = true;
@@ -576,12 +609,12 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 const uint32_t kb = ring + slot * S::kStage, vb = kb + S::kTileBytes, sb = vb + S::kTileBytes;
                 // bit i: the warp's i-th key counts
                 uint32_t counts = 0xffffu;
-                if (!whole || t0 + i == 0 || t0 + i == w.g.tiles - 1) {
-                    const int s = w.g.seg0 + (t0 + i) * c.spt + my_seg;
+                if (!whole || t0 + i == 0 || t0 + i == it.tiles - 1) {
+                    const int s = it.seg0 + (t0 + i) * c.spt + my_seg;
                     const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + my_off;
                     const int64_t pos = (int64_t)page * c.B + tok;
-                    counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= w.g.lo &&
-                                                            pos < w.g.len);
+                    counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= it.lo &&
+                                                            pos < it.len);
                 }
                 const bool masked = counts != 0xffffu;
                 if (counts != 0) {                     // else nothing for this warp (rows that odd pages leave unused)
@@ -768,7 +801,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[h][x] += __shfl_xor_sync(0xffffffffu, l[h][x], d);
-        named_bar_sync(1, 32 * kWarps);                // every warp is done with the stage, and with sh.m of the last item
+        meet();                                        // every warp is done with the stage, and with sh.m of the last item
         if (g == 0) {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
@@ -781,7 +814,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            if (h) named_bar_sync(1, 32 * kWarps);
+            if (h) meet();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float* row = scratch + (warp * 8 + 2 * t + x) * kLd<DK>;
@@ -795,7 +828,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                     }
                 }
             }
-            named_bar_sync(1, 32 * kWarps);
+            meet();
             constexpr int TPH = 4 * kWarps;            // threads of a head
             const int hh = threadIdx.x / TPH, x = threadIdx.x % TPH, hr = 8 * h + hh;
             float M = sh.m[0][hr];
@@ -822,7 +855,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
             }
-            const int64_t part = ((int64_t)w.r * a.Hq + head * a.group + h0 + hr) * c.max_splits + w.ch;
+            const int64_t part = ((int64_t)it.r * a.Hq + it.head * a.group + it.h0 + hr) * c.max_splits + it.ch;
             if (hr < heads && !dead && UP_IN(part, a.parts, a.status)) {
                 // L = 0: no score above -inf.  NaN goes through.
                 const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -856,6 +889,11 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             mbar_init(smem_u32(&sh.qfull[i]), 1);
             mbar_init(smem_u32(&sh.qempty[i]), kWarps);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(smem_u32(&sh.ifull[i]), 1);
+            mbar_init(smem_u32(&sh.iempty[i]), kWarps);
+        }
+        mbar_init(smem_u32(&sh.joined), kWarps);
         sh.abort = 0;
         fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -867,12 +905,10 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    Walk w;
-    find_run(a, w);
     if (warp == kWarps)
-        produce<DK, E4M3, HT>(a, &kmap, &vmap, smem_u32(base), sh, w);
+        produce<DK, E4M3, HT>(a, &kmap, &vmap, smem_u32(base), sh);
     else
-        consume<DK, E4M3, HT>(a, smem_u32(base), base, sh, w);
+        consume<DK, E4M3, HT>(a, smem_u32(base), base, sh);
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -336,6 +336,25 @@ def test_decode_values_of_very_different_size(e4m3):
     _check(c, table, [np.arange(n)], qb, [n])
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dk,B,R", [(8, 2, 128, 16, 40), (9, 1, 64, 24, 70), (4, 4, 256, 64, 33), (34, 2, 128, 16, 6)])
+def test_decode_does_not_depend_on_the_tables_width(Hq, Hkv, dk, B, R, e4m3):
+    """many requests, most of them short, in a narrow table and in one that could hold far more"""
+    rng = np.random.default_rng(R)
+    lens = tuple(int(x) for x in np.concatenate([[0, 1, 0, 2500, 0], rng.integers(0, 700, max(0, R - 6)), [0]]))
+    c, table, rows, qb = _decode_case(R, Hq, Hkv, dk, B, lens, e4m3)
+    out, lse = _check(c, table, rows, qb, lens)
+    wide = np.full((R, table.shape[1] + 1280 * 1024 // (B * R * Hkv)), -1, dtype=np.int32)
+    wide[:, :table.shape[1]] = table
+    status, out2, lse2 = _run_decode(c, wide, lens, _from_bits(qb))
+    assert status == 0
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    status, out3, lse3 = _run_decode(c, wide, (0,) * R, _from_bits(qb))
+    assert status == 0 and (out3 == 0).all() and torch.isneginf(lse3).all()
+    status, out4, _ = _run_decode(c, wide, lens[:-1] + (-5,), _from_bits(qb))
+    assert status == 10 and torch.equal(out4[:-1], out[:-1])
+
+
 def test_decode_requests_share_pages_and_queries_lie_at_a_stride():
     rng = np.random.default_rng(6)
     n, Hq, Hkv, dk, B = 333, 8, 2, 128, 16
