@@ -5,18 +5,23 @@
 //
 // e4m3 rows: one power of two 2^e per row, the least with max|x| 2^-e <= 448 = 1.75 * 2^8.  For a bf16
 // maximum of exponent field E and mantissa field M that is e + 127 = E - 8 + [M > 0x60] (1.75 has mantissa
-// 0x60): two integer operations on the row's largest bit pattern.  Scaling by a power of two is exact in
-// fp32, so a code has one rounding, and reading back is exact: a scale that is not a power of two would
-// round on both sides and take four bytes instead of one.
+// 0x60): (pattern + 0x1f) >> 7, less 8, of the row's largest bit pattern.  Scaling by a power of two is exact,
+// so a code has one rounding, and reading back is exact: a scale that is not a power of two would round on
+// both sides and take four bytes instead of one.
 //
 // Both kernels only move bytes (write: 2 dk in, dk + 1 or 2 dk out per row; read: the reverse): HBM-bound.  A
 // warp takes units of 16 (or 4) tokens of one head: one coalesced load brings their slots, each lane places one
 // token, and the tokens' scale bytes, neighbours in a page, leave (or come) in one access.  A row belongs to
 // dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that its maximum is a few shuffles; the warps of a CTA
 // take the heads of the same tokens, so that they read or write whole tokens of the stream together.
+// At 32K tokens of 8 heads of 128 in e4m3 the write takes 32.5 us (6.2 TB/s of what it must move, 0.92 of the
+// measured copy rate) and the read 36.3 us (5.6 TB/s); with bf16 rows both run at the copy rate (685K tokens written
+// in 811 us, 6.9 TB/s).  What the e4m3 forms lack is issue slots: the write's instructions filled 65% of them before
+// two rows' maxima shared a shuffle and the scaling moved to pairs of bf16 (35.4 us).
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "up_kv.cuh"
 
@@ -24,9 +29,9 @@ namespace up {
 namespace kv {
 
 // 128 threads, 64 registers: 1,024 threads on an SM with up to eight rows (or groups of rows) of 16 bytes in
-// flight each.  A unit of 16 tokens against 8 and 32: 35 / 38 / 41 us for a write of 32K tokens of 8 heads of 128 in
-// e4m3, 214 / 222 / 218 for a read of 462K of 2 heads of 256.  A call too small to give every SM four warps
-// that way takes units of 4: 2.1 against 3.0 us for 64 tokens.
+// flight each.  Units of 16 tokens against 8 and 32 (before the maxima were paired): 35 / 38 / 41 us for a write of 32K
+// tokens of 8 heads of 128 in e4m3, 214 / 222 / 218 for a read of 462K of 2 heads of 256.  A call too small to
+// give every SM four warps that way takes units of 4: 1.9 against 3.0 us for 64 tokens.
 constexpr int kThreads = 128, kCtas = 8;
 constexpr int kChunk = 16, kSmallChunk = 4;      // tokens of a warp's unit
 constexpr int kSmallWarps = 4;                   // warps of an SM below which units are small
@@ -81,12 +86,15 @@ __device__ __forceinline__ float f_of(uint32_t bits) { return __uint_as_float(bi
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// largest 16-bit half over the LPR lanes of a row
+// the larger half of a pair
+__device__ __forceinline__ uint32_t top_half(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+
+// the largest of each half over the LPR lanes of a row: two rows' maxima travel together
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t m) {
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return max(m & 0xffffu, m >> 16);
+    return m;
 }
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
@@ -145,6 +153,38 @@ __global__ void __launch_bounds__(kThreads, kCtas) write_kernel(const __grid_con
                 const int j = (i0 + u) * RPI + grp;
                 x[u] = t0 + j < n ? *reinterpret_cast<const uint4*>(src + j * s.stride) : make_uint4(0, 0, 0, 0);
             }
+            uint32_t top[(U + 1) / 2];             // largest bit patterns of the rows, two a word
+            if constexpr (E4M3) {
+                auto maxima = [&](auto finite) {
+                    uint32_t all = 0;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t w = reinterpret_cast<const uint32_t*>(&x[u])[j];
+                            m = max_u16x2(m, (decltype(finite)::value ? finite_or(w, 0) : w) & 0x7fff7fffu);
+                        }
+                        top[u / 2] = u & 1 ? top[u / 2] | (top_half(m) << 16) : top_half(m);
+                    }
+#pragma unroll
+                    for (int u = 0; u < (U + 1) / 2; ++u) {
+                        top[u] = row_max<LPR>(top[u]);
+                        all = max_u16x2(all, top[u]);
+                    }
+                    return top_half(all);
+                };
+                if (__any_sync(0xffffffffu, maxima(std::false_type{}) >= 0x7f80u)) {       // rows with infinities or NaN
+                    maxima(std::true_type{});
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t& w = reinterpret_cast<uint32_t*>(&x[u])[j];
+                            w = finite_or(w, 0x7fff7fffu);
+                        }
+                }
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t row = __shfl_sync(0xffffffffu, pl.row, (i0 + u) * RPI + grp);
@@ -152,25 +192,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) write_kernel(const __grid_con
                 if constexpr (!E4M3) {
                     if (row >= 0 && UP_IN(at, a.c.row_limit, a.status)) *reinterpret_cast<uint4*>(s.dst + at) = x[u];
                 } else {
-                    uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                    uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                           max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-                    m = row_max<LPR>(m);
-                    if (__any_sync(0xffffffffu, m >= 0x7f80u)) {      // a row with infinities or NaN
-                        uint32_t f = 0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f = max_u16x2(f, finite_or(w[j], 0) & 0x7fff7fffu);
-                            w[j] = finite_or(w[j], 0x7fff7fffu);
-                        }
-                        m = row_max<LPR>(f);
-                    }
-                    int b = static_cast<int>(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0);
-                    b = m == 0 ? 127 : max(b, 1);
-                    const float inv = f_of(static_cast<uint32_t>(254 - b) << 23);      // 2^(127 - b)
+                    const uint32_t m = u & 1 ? top[u / 2] >> 16 : top[u / 2] & 0xffffu;
+                    const int e = static_cast<int>((m + 0x1fu) >> 7) - 8;          // E - 8 + [M > 0x60]
+                    const int b = m == 0 ? 127 : max(e, 1);
+                    const uint32_t inv = static_cast<uint32_t>(254 - b) * 0x800080u;       // 2^(127 - b), twice
                     uint32_t c[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) c[j] = to_e4m3x2(f_of(w[j] << 16) * inv, f_of(w[j] & 0xffff0000u) * inv);
+                    for (int j = 0; j < 4; ++j) {
+                        // a bf16 number times a power of two is exact down to 2^-126, far below the least code
+                        uint32_t w;
+                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(reinterpret_cast<const uint32_t*>(&x[u])[j]), "r"(inv));
+                        c[j] = to_e4m3x2(f_of(w << 16), f_of(w & 0xffff0000u));
+                    }
                     if (row >= 0 && UP_IN(at, a.c.row_limit, a.status))
                         *reinterpret_cast<uint2*>(s.dst + at) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
                     // to the lane of the row's token
@@ -186,12 +219,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) write_kernel(const __grid_con
     }
 }
 
-// two f16 numbers times a power of two, to bf16
-__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
+// two f16 numbers that bf16 holds exactly, times a power of two (in both halves of `scale`), in bf16: one rounding
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, uint32_t scale) {
     float lo, hi;
     asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h2));
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi * scale), "f"(lo * scale));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(scale));
     return r;
 }
 
@@ -212,11 +246,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const __grid_cons
         const int head = static_cast<int>(unit - chunk * a.c.Hkv);
         const int64_t t0 = chunk * CHUNK;
         const Place pl = place_of(a, lane < CHUNK ? t0 + lane : n, n);
-        float factor = 0.f;            // 2^(b - 127) of the lane's token
+        uint32_t factor = 0;           // 2^(b - 127) of the lane's token in bf16, twice
         if constexpr (E4M3) {
             const int64_t at = pl.scale + head * a.c.Bp;
             if (lane < CHUNK && pl.row >= 0 && UP_IN(at, a.c.scale_limit, a.status))
-                factor = f_of(max(static_cast<uint32_t>(s.scale[at]) << 23, 0x00400000u));
+                factor = max(static_cast<uint32_t>(s.scale[at]) * 0x800080u, 0x00400040u);
         }
         const int64_t dst = (t0 * a.c.Hkv + head) * DK + sub * 8;
 #pragma unroll
@@ -242,10 +276,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const __grid_cons
                 const int j = (i0 + u) * RPI + grp;
                 const int64_t at = dst + (int64_t)j * a.c.Hkv * DK;
                 if constexpr (E4M3) {
-                    const float f = __shfl_sync(0xffffffffu, factor, j);
-                    const uint2 v = make_uint2(x[u].x, x[u].y);
-                    x[u] = make_uint4(scaled_bf16x2(e4m3x2_to_f16x2(v.x), f), scaled_bf16x2(e4m3x2_to_f16x2(v.x >> 16), f),
-                                      scaled_bf16x2(e4m3x2_to_f16x2(v.y), f), scaled_bf16x2(e4m3x2_to_f16x2(v.y >> 16), f));
+                    const uint32_t f = __shfl_sync(0xffffffffu, factor, j);
+                    uint32_t h[4];
+                    e4m3x4_to_f16x4(x[u].x, h[0], h[1]);
+                    e4m3x4_to_f16x4(x[u].y, h[2], h[3]);
+                    x[u] = make_uint4(scaled_bf16x2(h[0], f), scaled_bf16x2(h[1], f), scaled_bf16x2(h[2], f), scaled_bf16x2(h[3], f));
                 }
                 if (t0 + j < n && UP_IN(at, a.T * a.c.Hkv * DK, a.status)) *reinterpret_cast<uint4*>(s.dst + at * 2) = x[u];
             }

@@ -75,15 +75,7 @@ inline up_status check(const up_kv_cache* c, Cache* out) {
     return UP_OK;
 }
 
-// two e4m3 codes (low byte first) to f16, exact, NaN kept
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    const uint16_t c = static_cast<uint16_t>(codes);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-    return r;
-}
-
-// four codes: the lower two and the upper two
+// four e4m3 codes (low byte first) to f16, the lower two and the upper two: exact, NaN kept
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(lo), "=r"(hi)
