@@ -244,7 +244,8 @@ up_status up_seqused(const int32_t* kept_len, const uint8_t* drop_layer, int L, 
  * page * stride_block + head * stride_head + token * stride_token of k (v) and is contiguous.  The
  * layout the kernels read best is [num_blocks, Hkv, B, dk] (a head's page is one run); any other order of
  * the first three axes works too.  k and v are 16-byte aligned and every stride is a multiple of 16
- * bytes.  dk in {64, 128, 256}.
+ * bytes, below 2^40 bytes for up_paged_decode (the stride of an axis of one entry does not matter).
+ * dk in {64, 128, 256}.
  * UP_KV_E4M3: k_scale and v_scale are uint8 [num_blocks, Hkv, up_kv_scale_row(B)], 16-byte aligned (the
  * bytes past the B-th of a row are not used); byte b of a row means the row's numbers are code * 2^(b-127).
  * UP_KV_BF16: k_scale and v_scale are ignored. */

@@ -70,6 +70,8 @@ class _KvCache(ctypes.Structure):
                 ("Hkv", ctypes.c_int32), ("B", ctypes.c_int32), ("dk", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
+_BF16, _E4M3, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
+
 _lib = None
 
 
@@ -237,28 +239,27 @@ def up_seqused(kept_len, drop_layer, layer, orig_len, kv_len, seqused, stream=No
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
     """The up_kv_cache of tensors [num_blocks, Hkv, B, dk] (bf16, or float8_e4m3fn with uint8 scale tensors
     [num_blocks, Hkv, up_kv_scale_row(B)]); keys and values have the same shape and strides."""
-    num_blocks, Hkv, B, dk = k_cache.shape
-    sb, sh, st, sd = k_cache.stride()
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    assert v_cache.shape == k_cache.shape and v_cache.stride() == (sb, sh, st, sd) and sd == 1
-    assert (e4m3 or k_cache.dtype == torch.bfloat16) and v_cache.dtype == k_cache.dtype and k_cache.is_cuda
-    ks = vs = None
-    if e4m3:
-        assert k_scale is not None and v_scale is not None
-        rows = (num_blocks, Hkv, -(-B // 16) * 16)
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    num_blocks, Hkv, B, dk = shape
+    sb, sh, st, sd = strides
+    assert v_cache.shape == shape and v_cache.stride() == strides and sd == 1
+    assert v_cache.dtype == dtype and k_cache.is_cuda
+    if dtype == _E4M3:
+        rows = (num_blocks, Hkv, (B + 15) // 16 * 16)
         assert k_scale.shape == rows and v_scale.shape == rows and k_scale.is_contiguous() and v_scale.is_contiguous()
-        assert k_scale.dtype == torch.uint8 and v_scale.dtype == torch.uint8
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    return ctypes.byref(_KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, num_blocks, sb, sh, st, Hkv, B, dk,
-                                 KV_E4M3 if e4m3 else KV_BF16))
+        assert k_scale.dtype == _U8 and v_scale.dtype == _U8
+        return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num_blocks, sb,
+                        sh, st, Hkv, B, dk, KV_E4M3)
+    assert dtype == _BF16
+    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), None, None, num_blocks, sb, sh, st, Hkv, B, dk, KV_BF16)
 
 
-def _rows(t, heads, dk):
+def _rows(t, T, heads, dk):
     """A bf16 tensor [T, heads, dk] whose tokens may lie at a stride (pointer, stride in elements)."""
-    assert t.dtype == torch.bfloat16 and t.is_cuda and t.shape[1:] == (heads, dk)
     st, sh, sd = t.stride()
-    assert t.numel() == 0 or (sd == 1 and (sh == dk or heads == 1))
-    return ctypes.c_void_p(t.data_ptr()), st
+    assert t.shape == (T, heads, dk) and t.dtype == _BF16 and t.is_cuda
+    assert (sd == 1 and (sh == dk or heads == 1)) or T == 0
+    return t.data_ptr(), st
 
 
 def up_kv_scale_row(B):
@@ -268,27 +269,28 @@ def up_kv_scale_row(B):
 def up_kv_write(k, v, slots, k_cache, v_cache, dev_status, k_scale=None, v_scale=None, num_tokens=None, stream=None):
     """k, v [T, Hkv, dk] (either may be None) into the rows that slots [T] int64 names."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    Hkv, dk = k_cache.shape[1], k_cache.shape[3]
     T = slots.numel()
-    assert slots.dtype == torch.int64 and slots.is_contiguous()
-    assert (k is None or k.shape[0] == T) and (v is None or v.shape[0] == T)
-    kp, ks = (None, 0) if k is None else _rows(k, Hkv, dk)
-    vp, vs = (None, 0) if v is None else _rows(v, Hkv, dk)
-    _check(load_library().up_kv_write(cache, kp, ks, vp, vs, _p(slots), T, _p(num_tokens), _p(dev_status),
-                                      _stream(stream)),
-           "up_kv_write")
+    assert slots.dtype == _I64 and slots.is_contiguous()
+    kp, ks = (None, 0) if k is None else _rows(k, T, cache.Hkv, cache.dk)
+    vp, vs = (None, 0) if v is None else _rows(v, T, cache.Hkv, cache.dk)
+    code = load_library().up_kv_write(ctypes.byref(cache), kp, ks, vp, vs, slots.data_ptr(), T, _p(num_tokens),
+                                      dev_status.data_ptr(), _stream(stream))
+    if code:
+        raise UpError(code, "up_kv_write")
 
 
 def up_kv_read(k_cache, v_cache, slots, k, v, dev_status, k_scale=None, v_scale=None, num_tokens=None, stream=None):
     """The rows that slots [T] int64 names to the packed streams k, v [T, Hkv, dk] (either may be None)."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     T = slots.numel()
-    assert slots.dtype == torch.int64 and slots.is_contiguous()
-    for x in (k, v):
-        assert x is None or x.shape == (T, k_cache.shape[1], k_cache.shape[3])
-    _check(load_library().up_kv_read(cache, _p(slots), T, _p(num_tokens), None if k is None else _bf16(k),
-                                     None if v is None else _bf16(v), _p(dev_status), _stream(stream)),
-           "up_kv_read")
+    assert slots.dtype == _I64 and slots.is_contiguous()
+    want = (T, cache.Hkv, cache.dk)
+    assert (k is None or k.shape == want) and (v is None or v.shape == want)
+    code = load_library().up_kv_read(ctypes.byref(cache), slots.data_ptr(), T, _p(num_tokens),
+                                     None if k is None else _bf16(k), None if v is None else _bf16(v),
+                                     dev_status.data_ptr(), _stream(stream))
+    if code:
+        raise UpError(code, "up_kv_read")
 
 
 def up_paged_decode_workspace_bytes(R, Hq, Hkv, dk, B, max_blocks, window=0):
@@ -300,17 +302,20 @@ def up_paged_decode(q, k_cache, v_cache, block_table, seqused, out, ws, dev_stat
     """q [R, Hq, dk], one new token per request; block_table [R, max_blocks] int32; seqused [R] int32;
     out [R, Hq, dk]; ws of up_paged_decode_workspace_bytes(...) bytes; lse optional fp32 [R, Hq]."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    R, Hq, dk = q.shape
-    assert dk == k_cache.shape[3] and out.shape == q.shape
-    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.shape[0] == R
-    assert seqused.dtype == torch.int32 and seqused.is_contiguous() and seqused.numel() == R
+    shape = q.shape
+    R, Hq, dk = shape
+    rows, max_blocks = block_table.shape
+    assert dk == cache.dk and out.shape == shape
+    assert block_table.dtype == _I32 and block_table.is_contiguous() and rows == R
+    assert seqused.dtype == _I32 and seqused.is_contiguous() and seqused.numel() == R
     assert lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (R, Hq))
-    sm_scale = dk ** -0.5 if sm_scale is None else sm_scale
-    qp, qs = _rows(q, Hq, dk)
-    _check(load_library().up_paged_decode(qp, qs, cache, _p(block_table), _p(seqused), R, block_table.shape[1], Hq,
-                                          sm_scale, window, _bf16(out), _p(lse), _p(ws), ws.numel() * ws.element_size(),
-                                          _p(dev_status), _stream(stream)),
-           "up_paged_decode")
+    qp, qs = _rows(q, R, Hq, dk)
+    code = load_library().up_paged_decode(qp, qs, ctypes.byref(cache), block_table.data_ptr(), seqused.data_ptr(), R,
+                                          max_blocks, Hq, dk ** -0.5 if sm_scale is None else sm_scale, window,
+                                          _bf16(out), _p(lse), ws.data_ptr(), ws.nbytes, dev_status.data_ptr(),
+                                          _stream(stream))
+    if code:
+        raise UpError(code, "up_paged_decode")
 
 
 # ------------------------------------------------------------------------------------------ status

@@ -13,16 +13,22 @@
 // and the rest out of their way:
 //  * persistent CTAs take runs of (request, head, chunk) items of equal length in tiles, found from seqused on the
 //    device: the host never waits for a length;
-//  * a producer warp walks the run, tells the consumers of each item and fills a ring of stages (the K and V tile of one head) by TMA, one
-//    box per page, swizzled so that ldmatrix reads it without bank conflicts; the ring
-//    runs across items, so a new item's first tiles are there when the last one's sums are written;
+//  * a producer warp walks the run, tells the consumers of each item and fills a ring of stages (the K and V
+//    tile of one head) by TMA, one box per page, swizzled so that ldmatrix reads it without bank conflicts; the
+//    ring runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
 //    running maximum and sums, joined through the last stage when the item ends.
 // The products are m16n8k16 with the long side of each in the 16 rows: scores = keys x queries (16 keys, 8
 // heads), outputs = values transposed x weights transposed (16 columns, 8 heads), so that a group of up to 8
 // heads, and a second tile of 8 above that, leaves little of them empty.  The scores' own layout, transposed
 // in the registers, is the weights' operand.  A matrix unit with larger tiles has nothing to win here: 8 or
-// 16 queries are all there is to multiply with.
+// 16 queries are all there is to multiply with, and the products fill 12 to 16% of the tensor pipe.
+//
+// Measured (one GB300, 6.69 TB/s measured copy): 64 requests of 32K, 8 heads of 256 in bf16, 2.44 ms, 7.0 TB/s;
+// 16 of 4K-128K, 8 heads of 128 in bf16, 429 us, 6.5 TB/s; 4 of 128K, 2 heads of 256 in e4m3, 97 us, 5.6 TB/s;
+// 64 of 0-8K, 8 heads of 128 in e4m3, 111 us, 5.2 TB/s.  With e4m3 half the bytes come with the same work per
+// number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K takes 10 us, a chain of
+// latencies (its length, its pages, the copies, four tiles, the join); its bytes would take 2.5 us.
 #include <stdint.h>
 
 #include <algorithm>
