@@ -116,6 +116,7 @@ struct Args {
     const int32_t* table;
     const int32_t* seqused;
     int R, max_blocks, Hq, group, head_tiles;
+    FastDiv by_hq;
     float scale2;              // sm_scale * log2 e
     Cut cut;
     float* part_lse;           // [R, Hq, max_splits]
@@ -127,6 +128,12 @@ struct Args {
 };
 
 __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
+
+// x / y of numbers that mostly fit 32 bits (a 64-bit division takes a third of a microsecond, here in the way of
+// the first copy)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
 
 // ------------------------------------------------------------------------------------------------
 // the walk over a CTA's run of items.  Item order: request, KV head, chunk, head tile (the tiles of queries that read
@@ -154,7 +161,7 @@ struct Walk {
     __device__ __forceinline__ void enter(const Args& a, int len) {
         g = range_of(a.cut, len, (int64_t)a.max_blocks * a.cut.B);
         g.splits = splits_of(g.tiles, a.cut);
-        q = g.splits ? static_cast<int>(static_cast<unsigned>(g.tiles) / static_cast<unsigned>(g.splits)) : 0;
+        q = g.splits ? static_cast<int>(quotient(g.tiles, g.splits)) : 0;
         rem = g.tiles - q * g.splits;
         head = ht = 0;
         chunk(0, 0, 0);
@@ -180,12 +187,6 @@ struct Walk {
     }
 };
 
-// x / y of numbers that mostly fit 32 bits (a 64-bit division takes a third of a microsecond, here in the way of
-// the first copy)
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    return (x | y) >> 32 ? x / y : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
-}
-
 // the first item whose middle lies at or after `want` tiles: in request r, which starts at `before` of them
 __device__ __forceinline__ void seek(const Args& a, Walk& w, int64_t want, int64_t end, int r, int64_t before, int len) {
     w.r = r;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void seek(const Args& a, Walk& w, int64_t want, int64
     const int64_t local = want - before;
     w.head = static_cast<int>(quotient(local, per_head));
     const int i = max(0, static_cast<int>(quotient((local - w.head * per_head) * w.g.splits, per_head)) - 1);
-    const int whole = static_cast<int>(static_cast<unsigned>(i * w.rem) / static_cast<unsigned>(w.g.splits));
+    const int whole = static_cast<int>(quotient(i * w.rem, w.g.splits));
     w.chunk(i, whole, i * w.rem - whole * w.g.splits);
     w.start = before + w.head * per_head + (int64_t)w.t0 * a.head_tiles;
     while (w.r < a.R && 2 * w.start + w.n < 2 * want) w.next(a);
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(W == 16 ? 512 : 128) join_kernel(const __grid_
     const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x >> 5 : 0;
     const int64_t row = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (int64_t)a.R * a.Hq || !UP_IN((row + 1) * a.cut.max_splits - 1, a.parts, a.status)) return;
-    const int n = splits_of(a.cut, length_of(a, static_cast<int>(row / a.Hq)), (int64_t)a.max_blocks * a.cut.B);
+    const int n = splits_of(a.cut, length_of(a, divided(static_cast<int>(row), a.by_hq)), (int64_t)a.max_blocks * a.cut.B);
     const float* pl = a.part_lse + row * a.cut.max_splits;
     const float* po = a.part_o + row * a.cut.max_splits * DK;
     float m = -INFINITY, l = 0.f;
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(W == 16 ? 512 : 128) join_kernel(const __grid_
 // 0 for arguments that the call refuses
 static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window, Cut* c) {
     if (R <= 0 || R > 65535 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq > 65535 || B <= 0 || B > (1 << 20)) return 0;
-    if (max_blocks <= 0 || window < 0) return 0;
+    if ((int64_t)R * Hq > 0x7fffffff || max_blocks <= 0 || window < 0) return 0;
     if (dk != 64 && dk != 128 && dk != 256) return 0;
     if ((int64_t)max_blocks * B > 0x7fffffff - 2 * kTile) return 0;
     c->B = B;
@@ -1157,6 +1158,7 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     a.R = R;
     a.max_blocks = max_blocks;
     a.Hq = Hq;
+    a.by_hq = kv::fast_div(Hq);
     a.group = Hq / cache->Hkv;
     a.head_tiles = a.group <= 8 ? 1 : static_cast<int>(cdiv(a.group, 16));
     a.scale2 = sm_scale * kLog2e;
