@@ -302,6 +302,7 @@ size_t up_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int dk, int B, in
  * (requests may share pages; entries past a request's last page are not read).
  * A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a table entry outside
  * [0, num_blocks) sets UP_DEV_BAD_PAGE and its keys and values count as zeros.
+ * Hq % Hkv == 0; R * Hq below 2^31; max_blocks * B at most 2^31 - 129 and B at most 2^20 (UP_ERR_SHAPE otherwise).
  * Arithmetic: products of the cache's numbers with q in full, fp32 accumulation and softmax.  The range
  * of a request is split by its own length alone, so a request's result does not depend on the others.
  * ws: device workspace of up_paged_decode_workspace_bytes(...) bytes, 16-byte aligned, no initialisation. */

@@ -526,7 +526,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     float qf[NH][2];                                   // factors of the scores of heads 2t, 2t + 1
     // queries to registers, as the products' second operand: head g (of each tile of 8), columns
     // 16k + {2t, 2t+1, 2t+8, 2t+9}; for e4m3 16k + 4t .. 4t+3, the order that the key bytes come in
-    auto load_queries = [&]() {
+    auto load_queries = [&](int heads) {
         if (!dead && !mbar_wait(smem_u32(&sh.qfull[qslot]), qphase, &sh.abort)) dead = true;
         const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
 #pragma unroll
@@ -536,6 +536,8 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             for (int k = 0; k < KS; ++k) {
                 qb[h][k][0] = E4M3 ? row[8 * k + 2 * t] : row[8 * k + t];
                 qb[h][k][1] = E4M3 ? row[8 * k + 2 * t + 1] : row[8 * k + t + 4];
+                // a row that no query fills holds another item's, whose scores would move the warp's references
+                if (g + 8 * h >= heads) qb[h][k][0] = qb[h][k][1] = 0;
             }
             qf[h][0] = qf[h][1] = a.scale2;
             if constexpr (E4M3) {
@@ -586,7 +588,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         if (++islot == kItems) islot = 0, iphase ^= 1;
         if (it.n == 0) break;
         const int heads = min(HT, a.group - it.h0);
-        if (it.fresh) load_queries();
+        if (it.fresh) load_queries(heads);
 
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
@@ -906,9 +908,6 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
-    // rows of a head tile that no query fills
-    for (int i = threadIdx.x; i < HT * DK; i += kThreads) reinterpret_cast<uint32_t*>(sh.q)[i] = 0;
-    fence_proxy_async_smem();
     __syncthreads();
     pdl_wait();
     pdl_trigger();
@@ -1035,7 +1034,7 @@ __global__ void __launch_bounds__(W == 16 ? 512 : 128) join_kernel(const __grid_
 
 // 0 for arguments that the call refuses
 static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window, Cut* c) {
-    if (R <= 0 || R > 65535 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq > 65535 || B <= 0 || B > (1 << 20)) return 0;
+    if (R <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq > 65535 || B <= 0 || B > (1 << 20)) return 0;
     if ((int64_t)R * Hq > 0x7fffffff || max_blocks <= 0 || window < 0) return 0;
     if (dk != 64 && dk != 128 && dk != 256) return 0;
     if ((int64_t)max_blocks * B > 0x7fffffff - 2 * kTile) return 0;

@@ -384,6 +384,24 @@ def test_decode_does_not_depend_on_the_other_requests_or_the_run(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dk", [(17, 1, 64), (40, 1, 128), (3, 1, 128), (33, 1, 256)])
+@pytest.mark.parametrize("R,longest", [(7, 3000), (400, 900), (200, 3000)])
+def test_decode_of_many_requests_is_that_of_each_alone(R, longest, Hq, Hkv, dk, e4m3):
+    """whatever a CTA worked on before (a head tile of 16 queries, then one of a single query; a request of a hundred
+    times larger queries) and however many rows the chunks' join has"""
+    rng = np.random.default_rng(R + Hq)
+    lens = tuple(int(x) for x in rng.integers(0, longest, R))
+    c, table, rows, qb = _decode_case(R + dk, Hq, Hkv, dk, 16, lens, e4m3, extra_cols=0)
+    size = torch.from_numpy(10.0 ** rng.integers(-2, 3, (R, 1, 1))).cuda()
+    q = (_from_bits(qb).double() * size).to(torch.bfloat16)
+    status, out, lse = _run_decode(c, table, lens, q)
+    assert status == 0
+    for r in [0, R - 1] + [int(x) for x in rng.integers(0, R, 12)]:
+        _, one, l1 = _run_decode(c, table[r:r + 1], lens[r:r + 1], q[r:r + 1].contiguous())
+        assert torch.equal(out[r], one[0]) and torch.equal(lse[r], l1[0]), r
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_decode_nan_and_infinity_in_attended_rows(e4m3):
     """NaN keys or values of one KV head reach the rows of that head alone"""
     lens = (100, 90)
