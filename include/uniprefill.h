@@ -245,7 +245,7 @@ up_status up_seqused(const int32_t* kept_len, const uint8_t* drop_layer, int L, 
  * layout the kernels read best is [num_blocks, Hkv, B, dk] (a head's page is one run); any other order of
  * the first three axes works too.  k and v are 16-byte aligned and every stride is a multiple of 16
  * bytes, below 2^40 bytes for up_paged_decode (the stride of an axis of one entry does not matter).
- * dk in {64, 128, 256}.
+ * dk in {64, 128, 256}; 1 <= B <= 2^20; 1 <= num_blocks < 2^31.
  * UP_KV_E4M3: k_scale and v_scale are uint8 [num_blocks, Hkv, up_kv_scale_row(B)], 16-byte aligned (the
  * bytes past the B-th of a row are not used); byte b of a row means the row's numbers are code * 2^(b-127).
  * UP_KV_BF16: k_scale and v_scale are ignored. */
@@ -302,7 +302,7 @@ size_t up_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int dk, int B, in
  * (requests may share pages; entries past a request's last page are not read).
  * A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a table entry outside
  * [0, num_blocks) sets UP_DEV_BAD_PAGE and its keys and values count as zeros.
- * Hq % Hkv == 0; R * Hq below 2^31; max_blocks * B at most 2^31 - 129 and B at most 2^20 (UP_ERR_SHAPE otherwise).
+ * Hq % Hkv == 0; R * Hq below 2^31; max_blocks * B at most 2^31 - 129 (UP_ERR_SHAPE otherwise).
  * Arithmetic: products of the cache's numbers with q in full, fp32 accumulation and softmax.  The range
  * of a request is split by its own length alone, so a request's result does not depend on the others.
  * ws: device workspace of up_paged_decode_workspace_bytes(...) bytes, 16-byte aligned, no initialisation. */

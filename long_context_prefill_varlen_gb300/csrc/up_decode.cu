@@ -50,7 +50,6 @@ constexpr int kMinTiles = 4;         // a chunk holds at least this many tiles, 
 constexpr int kFewSplits = 16;       // as many beyond this many chunks
 constexpr int kMaxTiles = 16;        // about as many tiles as a chunk holds, up to kMaxSplits chunks
 constexpr int kMaxSplits = 640;
-constexpr int kSpread = 2;           // items of one request on an SM
 constexpr int kItems = 4;            // items that the producer may be ahead
 constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or values) in a stage
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1032,9 +1031,15 @@ __global__ void __launch_bounds__(W == 16 ? 512 : 128) join_kernel(const __grid_
 // ------------------------------------------------------------------------------------------------
 // host side
 
+template <int DK>
+static int ctas_of(bool e4m3, int group) {
+    if (group <= 8) return e4m3 ? Shape<DK, true, 8>::kCtas : Shape<DK, false, 8>::kCtas;
+    return e4m3 ? Shape<DK, true, 16>::kCtas : Shape<DK, false, 16>::kCtas;
+}
+
 // 0 for arguments that the call refuses
-static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window, Cut* c) {
-    if (R <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq > 65535 || B <= 0 || B > (1 << 20)) return 0;
+static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window, bool e4m3, Cut* c) {
+    if (R <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || B <= 0 || B > (1 << 20)) return 0;
     if ((int64_t)R * Hq > 0x7fffffff || max_blocks <= 0 || window < 0) return 0;
     if (dk != 64 && dk != 128 && dk != 256) return 0;
     if ((int64_t)max_blocks * B > 0x7fffffff - 2 * kTile) return 0;
@@ -1048,15 +1053,16 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
     c->by_spt = kv::fast_div(c->spt);
     c->by_spp = kv::fast_div(c->spp);
     c->by_segp = kv::fast_div(c->segp);
-    // the least number of chunks that makes one request's items a multiple of two CTAs on every SM
+    // the least number of chunks that makes one request's items a multiple of the grid
     const int group = Hq / Hkv, units = Hkv * (group <= 8 ? 1 : static_cast<int>(cdiv(group, 16)));
-    int x = kSpread * num_sms(), y = units;
+    const int grid = num_sms() * (dk == 64 ? ctas_of<64>(e4m3, group) : dk == 128 ? ctas_of<128>(e4m3, group) : ctas_of<256>(e4m3, group));
+    int x = grid, y = units;
     while (y) {
         const int z = x % y;
         x = y;
         y = z;
     }
-    c->s0 = std::min(kSpread * num_sms() / x, kMaxSplits);
+    c->s0 = std::min(grid / x, kMaxSplits);
     c->most = kMaxSplits / c->s0;
     c->by_wave = kv::fast_div(c->s0 * kMaxTiles);
     int64_t segs = (int64_t)max_blocks * c->spp;
@@ -1128,9 +1134,11 @@ static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args
 using namespace up;
 
 extern "C" size_t up_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window) {
-    decode::Cut c{};
-    if (!decode::make_cut(R, Hq, Hkv, dk, B, max_blocks, window, &c)) return 0;
-    const size_t parts = static_cast<size_t>(R) * Hq * c.max_splits;
+    decode::Cut c{}, d{};          // of a bf16 and an e4m3 cache
+    if (!decode::make_cut(R, Hq, Hkv, dk, B, max_blocks, window, false, &c) ||
+        !decode::make_cut(R, Hq, Hkv, dk, B, max_blocks, window, true, &d))
+        return 0;
+    const size_t parts = static_cast<size_t>(R) * Hq * std::max(c.max_splits, d.max_splits);
     return align_up(parts * sizeof(float), 256) + parts * dk * sizeof(float);
 }
 
@@ -1144,12 +1152,12 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     const up_status s = kv::check(cache, &a.c);
     if (s != UP_OK) return s;
     if (R <= 0 || max_blocks <= 0 || Hq <= 0 || window < 0 || !(sm_scale > -INFINITY && sm_scale < INFINITY)) return UP_ERR_ARG;
-    if (!make_cut(R, Hq, cache->Hkv, cache->dk, cache->B, max_blocks, window, &a.cut)) return UP_ERR_SHAPE;
+    const bool e4m3 = cache->format == UP_KV_E4M3;
+    if (!make_cut(R, Hq, cache->Hkv, cache->dk, cache->B, max_blocks, window, e4m3, &a.cut)) return UP_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(out) || q_stride % 8 || (R > 1 && q_stride < (int64_t)Hq * cache->dk)) return UP_ERR_SHAPE;
     const size_t parts = static_cast<size_t>(R) * Hq * a.cut.max_splits;
     const size_t lse_bytes = align_up(parts * sizeof(float), 256);
     if (ws_bytes < lse_bytes + parts * cache->dk * sizeof(float) || !aligned16(ws)) return UP_ERR_WORKSPACE;
-    const bool e4m3 = cache->format == UP_KV_E4M3;
     a.q = reinterpret_cast<const uint8_t*>(q);
     a.q_stride = q_stride * 2;
     a.table = block_table;
