@@ -17,7 +17,9 @@
 //    tile of one head) by TMA, one box per page, swizzled so that ldmatrix reads it without bank conflicts; the
 //    ring runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
-//    running maximum and sums, joined through the last stage when the item ends.
+//    running maximum and sums, joined through the last stage when the item ends;
+//  * a call so short that every chunk can have a CTA at once is one launch: the chunks of a row are a cluster and
+//    join through its shared memory (one 4K request: 9.9 -> 8.4 us, and one launch less for the host).
 // The products are m16n8k16 with the long side of each in the 16 rows: scores = keys x queries (16 keys, 8
 // heads), outputs = values transposed x weights transposed (16 columns, 8 heads), so that a group of up to 8
 // heads, and a second tile of 8 above that, leaves little of them empty.  The scores' own layout, transposed
@@ -27,7 +29,7 @@
 // Measured (one GB300, 6.69 TB/s measured copy): 64 requests of 32K, 8 heads of 256 in bf16, 2.44 ms, 7.0 TB/s;
 // 16 of 4K-128K, 8 heads of 128 in bf16, 429 us, 6.5 TB/s; 4 of 128K, 2 heads of 256 in e4m3, 97 us, 5.6 TB/s;
 // 64 of 0-8K, 8 heads of 128 in e4m3, 111 us, 5.2 TB/s.  With e4m3 half the bytes come with the same work per
-// number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K takes 10 us, a chain of
+// number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K takes 8.4 us, a chain of
 // latencies (its length, its pages, the copies, four tiles, the join); its bytes would take 2.5 us.
 #include <stdint.h>
 
@@ -250,6 +252,24 @@ __device__ __forceinline__ void find_run(const Args& a, Walk& w) {
     }
 }
 
+// A cluster's CTA has one item: chunk blockIdx.x of (head, head tile) blockIdx.y of request blockIdx.z, if the
+// request has as many.
+__device__ __forceinline__ void own_chunk(const Args& a, Walk& w) {
+    const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
+    const int len = length_of(a, blockIdx.z), ch = blockIdx.x;
+    if ((len < 0 || len > cap) && blockIdx.x == 0 && blockIdx.y == 0) set_status(a.status, UP_DEV_BAD_LENGTH);
+    w.r = blockIdx.z;
+    w.enter(a, len);
+    w.start = 0;
+    w.end = 0;
+    if (ch >= w.g.splits) return;
+    w.head = static_cast<int>(blockIdx.y) / a.head_tiles;
+    w.ht = static_cast<int>(blockIdx.y) - w.head * a.head_tiles;
+    const int whole = static_cast<int>(static_cast<unsigned>(ch * w.rem) / static_cast<unsigned>(w.g.splits));
+    w.chunk(ch, whole, ch * w.rem - whole * w.g.splits);
+    w.end = w.n;               // live once: next() moves the start to the end
+}
+
 // ------------------------------------------------------------------------------------------------
 // tiles in shared memory
 
@@ -353,6 +373,7 @@ struct Control {
     alignas(16) uint16_t q[2][HT * DK];        // queries, double-buffered
     Item item[kItems];
     float m[kWarps][16], f[kWarps][16], l[kWarps][16];
+    float lse[16];                             // of a cluster's chunk; its sums take the queries' place
     uint64_t full[NS], empty[NS], qfull[2], qempty[2], ifull[kItems], iempty[kItems], joined;
     int abort;
 };
@@ -369,7 +390,7 @@ struct Sizes {
 
 // ------------------------------------------------------------------------------------------------
 
-template <int DK, bool E4M3, int HT>
+template <int DK, bool E4M3, int HT, bool TEAM>
 __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
                         Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
@@ -384,7 +405,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     const int per_seg = (c.seg + 15) / 16, sc_seg = lane / per_seg, sc_part = (lane - sc_seg * per_seg) * 16;
 
     Walk w;
-    find_run(a, w);
+    if constexpr (TEAM) own_chunk(a, w); else find_run(a, w);
     // the table entries of an item's segments, 32 (or the most that make whole tiles) at a time, one batch ahead
     auto fetch = [&](const Walk& x, int tile) {
         const int s = x.g.seg0 + (x.t0 + tile) * c.spt + lane;
@@ -490,7 +511,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     }
 }
 
-template <int DK, bool E4M3, int HT>
+template <int DK, bool E4M3, int HT, bool TEAM>
 __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
     constexpr int KS = DK / 16, NH = HT / 8;           // steps of 16 columns; tiles of 8 query heads
@@ -864,21 +885,86 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
             }
             const int64_t part = ((int64_t)it.r * a.Hq + it.head * a.group + it.h0 + hr) * c.max_splits + it.ch;
-            if (hr < heads && !dead && UP_IN(part, a.parts, a.status)) {
+            if (hr < heads && !dead && (TEAM || UP_IN(part, a.parts, a.status))) {
+                float* sums = TEAM ? reinterpret_cast<float*>(sh.q) + hr * DK : a.part_o + part * DK;
                 // L = 0: no score above -inf.  NaN goes through.
                 const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
                 for (int k = 0; k < DK / (4 * TPH); ++k)
-                    *reinterpret_cast<float4*>(a.part_o + part * DK + 4 * (x + k * TPH)) =
+                    *reinterpret_cast<float4*>(sums + 4 * (x + k * TPH)) =
                         make_float4(s[k].x * inv, s[k].y * inv, s[k].z * inv, s[k].w * inv);
-                if (x == 0) a.part_lse[part] = L == 0.f ? -INFINITY : M + log2f(L);
+                if (x == 0) *(TEAM ? sh.lse + hr : a.part_lse + part) = L == 0.f ? -INFINITY : M + log2f(L);
             }
         }
     }
     if (dead && threadIdx.x == 0) set_status(a.status, UP_DEV_WAIT_TIMEOUT);
 }
 
-template <int DK, bool E4M3, int HT>
+// ------------------------------------------------------------------------------------------------
+// the join of a cluster's chunks, through its CTAs' shared memory.  Same arithmetic, in the same order, as
+// join_kernel's for up to 16 chunks.
+
+constexpr int kTeam = 16;
+
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int DK, int HT, int NS>
+__device__ void join_team(const Args& a, Control<DK, HT, NS>& sh) {
+    const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
+    const int r = blockIdx.z, n = splits_of(a.cut, length_of(a, r), cap);
+    const int head = static_cast<int>(blockIdx.y) / a.head_tiles, h0 = (static_cast<int>(blockIdx.y) - head * a.head_tiles) * HT;
+    const int pairs = min(HT, a.group - h0) * (DK / 2);
+    const uint32_t sums = smem_u32(sh.q), lses = smem_u32(sh.lse);
+    for (int i = blockIdx.x * 32 * kWarps + threadIdx.x; i < pairs; i += gridDim.x * 32 * kWarps) {
+        const int h = i / (DK / 2), d = i - h * (DK / 2);
+        float v[kTeam], x[kTeam], y[kTeam], m = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kTeam; ++c) {
+            v[c] = -INFINITY;
+            x[c] = y[c] = 0.f;
+            if (c < n) {
+                v[c] = ld_cluster(of_rank(lses + 4 * h, c));
+                x[c] = ld_cluster(of_rank(sums + 4 * (h * DK + 2 * d), c));
+                y[c] = ld_cluster(of_rank(sums + 4 * (h * DK + 2 * d + 1), c));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kTeam; ++c) m = fmaxf(m, v[c]);
+        float l[kTeam], ox = 0.f, oy = 0.f;
+#pragma unroll
+        for (int c = 0; c < kTeam; ++c) {
+            l[c] = c < n ? weight(v[c], m) : 0.f;
+            if (c < n) {
+                ox = __fadd_rn(ox, __fmul_rn(l[c], x[c]));
+                oy = __fadd_rn(oy, __fmul_rn(l[c], y[c]));
+            }
+        }
+#pragma unroll
+        for (int o = kTeam / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int c = 0; c < o; ++c) l[c] += l[c + o];
+        const float inv = l[0] == 0.f ? 0.f : 1.f / l[0];
+        const int64_t row = (int64_t)r * a.Hq + head * a.group + h0 + h;
+        reinterpret_cast<uint32_t*>(a.out)[row * (DK / 2) + d] = bf16x2(ox * inv, oy * inv);
+        if (a.lse && d == 0) a.lse[row] = l[0] == 0.f ? -INFINITY : (m + log2f(l[0])) * kLn2;
+    }
+}
+
+// TEAM: a call short enough for every chunk to have a CTA at once (one request of up to 8K tokens on 8 key heads);
+// the chunks of a row are a cluster and join there, without a second launch.
+template <int DK, bool E4M3, int HT, bool TEAM>
 __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, HT>::kCtas))
 split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
              const __grid_constant__ Args a) {
@@ -911,9 +997,16 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     pdl_wait();
     pdl_trigger();
     if (warp == kWarps)
-        produce<DK, E4M3, HT>(a, &kmap, &vmap, smem_u32(base), sh);
+        produce<DK, E4M3, HT, TEAM>(a, &kmap, &vmap, smem_u32(base), sh);
     else
-        consume<DK, E4M3, HT>(a, smem_u32(base), base, sh);
+        consume<DK, E4M3, HT, TEAM>(a, smem_u32(base), base, sh);
+    if constexpr (TEAM) {
+        __syncwarp();
+        cluster_meet();
+        if (warp < kWarps) join_team<DK, HT, S::kStages>(a, sh);
+        __syncwarp();
+        cluster_meet();        // no CTA leaves while another reads its sums
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1087,18 +1180,54 @@ static bool make_map(CUtensorMap* m, const uint8_t* ptr, const Cache& c, const C
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the cluster that holds a row's chunks, 0 where they do not all run at once
 template <int DK, bool E4M3, int HT>
-static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
+static int team_of(const Args& a) {
+    int team = 1;
+    while (team < a.cut.max_splits) team *= 2;
+    const int64_t units = (int64_t)a.c.Hkv * a.head_tiles;
+    return team <= kTeam && units <= 65535 && a.R <= 65535 && team * units * a.R <= (int64_t)Shape<DK, E4M3, HT>::kCtas * num_sms() ? team : 0;
+}
+
+template <int DK, bool E4M3, int HT, bool TEAM>
+static cudaError_t prepare_split() {
     constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     static_assert(Shape<DK, E4M3, HT>::kStage >= 8 * kWarps * kLd<DK> * 4, "the join of the warps fits a stage");
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (TEAM && attr == cudaSuccess)
+            attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
-    if (attr != cudaSuccess) return attr;
-    return launch_pdl(split_kernel<DK, E4M3, HT>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
+    return attr;
+}
+
+template <int DK, bool E4M3, int HT>
+static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, int team, cudaStream_t st) {
+    constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
+    if (team == 0) {
+        const cudaError_t e = prepare_split<DK, E4M3, HT, false>();
+        if (e != cudaSuccess) return e;
+        return launch_pdl(split_kernel<DK, E4M3, HT, false>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
+    }
+    const cudaError_t e = prepare_split<DK, E4M3, HT, true>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(team, a.c.Hkv * a.head_tiles, a.R);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = team;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, split_kernel<DK, E4M3, HT, true>, k, v, a);
 }
 
 // The join asks for the split's division of an SM's memory (nearly all of it shared): with the default one an SM
@@ -1115,17 +1244,21 @@ static cudaError_t launch_join(const Args& a, int64_t ctas, cudaStream_t st) {
     return launch_pdl(join_kernel<DK, W>, dim3(static_cast<unsigned>(ctas)), dim3(W == 16 ? 512 : 128), 0, st, a);
 }
 
-template <int DK>
-static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, bool e4m3, cudaStream_t st) {
-    cudaError_t e;
-    if (a.group <= 8)
-        e = e4m3 ? launch_split<DK, true, 8>(k, v, a, st) : launch_split<DK, false, 8>(k, v, a, st);
-    else
-        e = e4m3 ? launch_split<DK, true, 16>(k, v, a, st) : launch_split<DK, false, 16>(k, v, a, st);
-    if (e != cudaSuccess) return e;
+template <int DK, bool E4M3, int HT>
+static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
+    const int team = team_of<DK, E4M3, HT>(a);
+    const cudaError_t e = launch_split<DK, E4M3, HT>(k, v, a, team, st);
+    count_launch(team ? 1 : 2);
+    if (e != cudaSuccess || team) return e;
     const int64_t rows = (int64_t)a.Hq * a.R;
     if (rows <= 4 * num_sms()) return launch_join<DK, 16>(a, rows, st);
     return a.cut.max_splits > kJoinAlone ? launch_join<DK, 4>(a, rows, st) : launch_join<DK, 1>(a, cdiv(rows, 4), st);
+}
+
+template <int DK>
+static cudaError_t launch_dk(const CUtensorMap& k, const CUtensorMap& v, const Args& a, bool e4m3, cudaStream_t st) {
+    if (a.group <= 8) return e4m3 ? launch<DK, true, 8>(k, v, a, st) : launch<DK, false, 8>(k, v, a, st);
+    return e4m3 ? launch<DK, true, 16>(k, v, a, st) : launch<DK, false, 16>(k, v, a, st);
 }
 
 }  // namespace decode
@@ -1180,14 +1313,9 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     if (!make_map(&km, a.c.k, a.c, a.cut, cache->dk, e4m3) || !make_map(&vm, a.c.v, a.c, a.cut, cache->dk, e4m3))
         return UP_ERR_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaErrorInvalidValue;
-    switch (cache->dk) {
-        case 64: e = launch<64>(km, vm, a, e4m3, st); break;
-        case 128: e = launch<128>(km, vm, a, e4m3, st); break;
-        case 256: e = launch<256>(km, vm, a, e4m3, st); break;
-        default: return UP_ERR_SHAPE;
-    }
+    const cudaError_t e = cache->dk == 64    ? launch_dk<64>(km, vm, a, e4m3, st)
+                          : cache->dk == 128 ? launch_dk<128>(km, vm, a, e4m3, st)
+                                             : launch_dk<256>(km, vm, a, e4m3, st);
     if (e != cudaSuccess) return UP_ERR_CUDA;
-    count_launch(2);
     return check_launch();
 }
