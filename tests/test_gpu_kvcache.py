@@ -245,8 +245,15 @@ def _run_decode(c, table, lens, q, window=0, sm_scale=None, with_lse=True):
 
 
 def _check(c, table, rows, qb, lens, window=0, sm_scale=None):
+    """Against the reference, as a call of these requests (one launch, where every chunk can have a CTA at once) and
+    as one of 40 times as many (persistent CTAs and a join)."""
     status, out, lse = _run_decode(c, table, lens, _from_bits(qb), window, sm_scale)
     assert status == 0
+    launches = up.up_kernel_launches()
+    status, many, many_lse = _run_decode(c, np.tile(table, (40, 1)), tuple(lens) * 40, _from_bits(np.tile(qb, (40, 1, 1))),
+                                         window, sm_scale)
+    assert status == 0 and (len(lens) * 40 * c.Hkv < 500 or up.up_kernel_launches() - launches == 2)
+    assert torch.equal(many, out.repeat(40, 1, 1)) and torch.equal(many_lse, lse.repeat(40, 1))
     k, v = [c.rows("k", s) for s in rows], [c.rows("v", s) for s in rows]
     scale = qb.shape[2] ** -0.5 if sm_scale is None else sm_scale
     o, l, to, tl = kv_ref.decode(kv_ref.bf16_value(qb), k, v, scale)
@@ -462,8 +469,9 @@ def test_decode_in_a_graph_and_on_another_stream():
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("Hq,Hkv,dk,B", [(8, 2, 128, 16), (4, 4, 64, 24), (9, 1, 256, 100)])
-def test_bounds_checked_build_is_clean_and_identical(Hq, Hkv, dk, B, e4m3):
-    lens = (0, 1, 65, 700, 129)
+@pytest.mark.parametrize("times", [1, 60])
+def test_bounds_checked_build_is_clean_and_identical(times, Hq, Hkv, dk, B, e4m3):
+    lens = (0, 1, 65, 700, 129) * times
 
     def once():
         c, table, rows, qb = _decode_case(61, Hq, Hkv, dk, B, lens, e4m3, window=400)
