@@ -581,6 +581,9 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 }
             }
         }
+        // The reads may still be in flight here (rows of 2 dk bytes fall into the same banks), and the copy that the arrival
+        // allows is another proxy's: without the fence it overtook them.
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.qempty[qslot]));
         if (++qslot == 2) qslot = 0, qphase ^= 1;
@@ -816,6 +819,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 }
             }
             if (i + 1 < n) {                           // the last stage is kept for the join of the warps
+                fence_proxy_async_smem();              // its next content comes by the async proxy
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
             }

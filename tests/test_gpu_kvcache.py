@@ -409,6 +409,24 @@ def test_decode_of_many_requests_is_that_of_each_alone(R, longest, Hq, Hkv, dk, 
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dk,B", [(8, 2, 128, 16), (8, 2, 128, 1), (16, 2, 256, 16), (32, 2, 64, 64)])
+def test_decode_of_short_requests_over_and_over(Hq, Hkv, dk, B, e4m3):
+    """items of a tile or two, whose queries follow one another at the shortest distance, and calls in turn on two sets of
+    inputs, so that a row that keeps another item's or call's numbers differs"""
+    sets = []
+    for seed in (31, 32):
+        c, table, _, qb = _decode_case(seed + dk, Hq, Hkv, dk, B, LENS, e4m3)
+        _, out, lse = _run_decode(c, table, LENS, _from_bits(qb))
+        sets.append((c, np.tile(table, (40, 1)), _from_bits(np.tile(qb, (40, 1, 1))), out.repeat(40, 1, 1), lse.repeat(40, 1)))
+    wrong = 0
+    for _ in range(100):
+        for c, table, q, out, lse in sets:
+            status, o, l = _run_decode(c, table, LENS * 40, q)
+            wrong += status != 0 or not torch.equal(o, out) or not torch.equal(l, lse)
+    assert wrong == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_decode_nan_and_infinity_in_attended_rows(e4m3):
     """NaN keys or values of one KV head reach the rows of that head alone"""
     lens = (100, 90)
