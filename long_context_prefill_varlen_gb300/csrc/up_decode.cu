@@ -14,7 +14,7 @@
 //  * persistent CTAs take runs of (request, head, chunk) items of equal length in tiles, found from seqused on the
 //    device: the host never waits for a length;
 //  * a producer warp walks the run, tells the consumers of each item and fills a ring of stages (the K and V
-//    tile of one head) by TMA, one box per page, swizzled so that ldmatrix reads it without bank conflicts; the
+//    tile of one head) by TMA, a box or two per page, swizzled so that ldmatrix reads it without bank conflicts; the
 //    ring runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
 //    running maximum and sums, joined through the last stage when the item ends;
@@ -27,8 +27,8 @@
 // 16 queries are all there is to multiply with, and the products fill 12 to 16% of the tensor pipe.
 //
 // Measured (one GB300, 6.69 TB/s measured copy): 64 requests of 32K, 8 heads of 256 in bf16, 2.44 ms, 7.0 TB/s;
-// 16 of 4K-128K, 8 heads of 128 in bf16, 429 us, 6.5 TB/s; 4 of 128K, 2 heads of 256 in e4m3, 97 us, 5.6 TB/s;
-// 64 of 0-8K, 8 heads of 128 in e4m3, 111 us, 5.2 TB/s.  With e4m3 half the bytes come with the same work per
+// 16 of 4K-128K, 8 heads of 128 in bf16, 426 us, 6.6 TB/s; 4 of 128K, 2 heads of 256 in e4m3, 97 us, 5.6 TB/s;
+// 64 of 0-8K, 8 heads of 128 in e4m3, 109 us, 5.3 TB/s.  With e4m3 half the bytes come with the same work per
 // number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K takes 8.4 us, a chain of
 // latencies (its length, its pages, the copies, four tiles, the join); its bytes would take 2.5 us.
 #include <stdint.h>
@@ -118,6 +118,9 @@ struct Args {
     const int32_t* seqused;
     int R, max_blocks, Hq, group, head_tiles;
     FastDiv by_hq;
+    int both;                  // one copy brings keys and values: see make_maps
+    int pitch;                 // bytes from a segment's place in a stage to the next one's
+    int k_at, v_at;            // and from it to its keys, its values: multiples of 1024
     float scale2;              // sm_scale * log2 e
     Cut cut;
     float* part_lse;           // [R, Hq, max_splits]
@@ -127,6 +130,14 @@ struct Args {
     float* lse;
     int32_t* status;
 };
+
+// The two forms of a call give the same bits, so where a product meets a sum the code says whether they round
+// together: left to the compiler, each kernel could differ.
+
+// ln of the sum 2^m l
+__device__ __forceinline__ float natural(float m, float l) {
+    return l == 0.f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
+}
 
 __device__ __forceinline__ int length_of(const Args& a, int r) { return UP_IN(r, a.R, a.status) ? a.seqused[r] : 0; }
 
@@ -282,7 +293,8 @@ struct Shape {
     static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 2 * kScaleBytes : 0);
     // As many CTAs on an SM as leave each a few stages (228 KB of shared memory, 1 KB of it per CTA reserved) and the
     // registers that its sums need: 16 warps have 128 a thread, 12 have 168, 8 have 255.
-    static constexpr int kControl = 4 * HT * DK + 1536 + 1024;         // queries; items, barriers and the join's; alignment
+    static constexpr int kLdq = DK + (HT == 16 ? 8 : 0);               // numbers of a query's row
+    static constexpr int kControl = 4 * HT * kLdq + 1536 + 1024;       // queries; items, barriers and the join's; alignment
     static constexpr int kWarpsFit = DK == 256 && (HT == 16 || !E4M3) ? 8 : DK == 256 || HT == 16 || (DK == 128 && !E4M3) ? 12 : 16;
     static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 1024 - kControl) / kStage; }
     static constexpr int ctas(int c) { return c == 1 || (c * (kWarps + 1) <= kWarpsFit && fit(c) >= 3) ? c : ctas(c - 1); }
@@ -290,7 +302,7 @@ struct Shape {
     static constexpr int kStages = fit(kCtas) < 8 ? fit(kCtas) : 8;
 };
 
-// Byte offset of 16-byte column c of a panel's row that starts at byte `row` of a tile (the tile 1024-byte aligned):
+// Byte offset of 16-byte column c of a panel's row that starts at byte `row` of a stage (1024-byte aligned):
 // the TMA swizzle takes the address bits above the row into the column.
 template <int PANEL>
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, int c) {
@@ -368,9 +380,9 @@ struct Item {
     int lo, len, fresh, unused;                // fresh: its queries are not the last item's
 };
 
-template <int DK, int HT, int NS>
+template <int LDQ, int HT, int NS>
 struct Control {
-    alignas(16) uint16_t q[2][HT * DK];        // queries, double-buffered
+    alignas(16) uint16_t q[2][HT * LDQ];       // queries, double-buffered
     Item item[kItems];
     float m[kWarps][16], f[kWarps][16], l[kWarps][16];
     float lse[16];                             // of a cluster's chunk; its sums take the queries' place
@@ -384,15 +396,15 @@ constexpr int kLd = DK + 4;      // floats of a row in the join of the warps: he
 template <int DK, bool E4M3, int HT>
 struct Sizes {
     using S = Shape<DK, E4M3, HT>;
-    static constexpr int kSmem = S::kStages * S::kStage + static_cast<int>(sizeof(Control<DK, HT, S::kStages>)) + 1024;
-    static_assert(sizeof(Control<DK, HT, S::kStages>) + 1024 <= S::kControl, "room of the control block");
+    static constexpr int kSmem = S::kStages * S::kStage + static_cast<int>(sizeof(Control<S::kLdq, HT, S::kStages>)) + 1024;
+    static_assert(sizeof(Control<S::kLdq, HT, S::kStages>) + 1024 <= S::kControl, "room of the control block");
 };
 
 // ------------------------------------------------------------------------------------------------
 
 template <int DK, bool E4M3, int HT, bool TEAM>
 __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
-                        Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
+                        Control<Shape<DK, E4M3, HT>::kLdq, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
     const int lane = threadIdx.x & 31;
     const Cut& c = a.cut;
@@ -423,12 +435,18 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
         const bool fresh_q = w.r != q_r || head != q_head || w.ht != q_ht;
         if (fresh_q) {
             q_r = w.r, q_head = head, q_ht = w.ht;
-            const int bytes = min(HT, a.group - h0) * DK * 2;
+            const int heads = min(HT, a.group - h0);
             if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
-            if (lane == 0) {
-                const uint32_t bar = smem_u32(&sh.qfull[qslot]);
-                mbar_arrive_expect_tx(bar, bytes);
-                bulk_load(smem_u32(sh.q[qslot]), a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2, bytes, bar);
+            const uint32_t bar = smem_u32(&sh.qfull[qslot]), dst = smem_u32(sh.q[qslot]);
+            const uint8_t* src = a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2;
+            if (lane == 0) mbar_arrive_expect_tx(bar, heads * DK * 2);
+            // up to 8 rows by one copy, where eight would hold up the first tile's; more at a distance that spreads the
+            // banks (32 requests of 0-32K with 32 heads on one of 128 in bf16: 106 -> 99 us)
+            if (S::kLdq == DK) {
+                if (lane == 0) bulk_load(dst, src, heads * DK * 2, bar);
+            } else {
+                __syncwarp();
+                if (lane < heads) bulk_load(dst + lane * S::kLdq * 2, src + lane * DK * 2, DK * 2, bar);
             }
             if (++qslot == 2) qslot = 0, qphase ^= 1;
         }
@@ -476,9 +494,13 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                     set_status(a.status, UP_DEV_BAD_PAGE);
                     at = static_cast<int>(a.c.num_blocks);              // out of the map's bounds: zeros
                 }
-                const uint32_t dst = stage + lane * c.segp * S::kRowBytes;
-                tma_load_5d(dst, kmap, bar, 0, part * kTile, 0, head, at);
-                tma_load_5d(dst + S::kTileBytes, vmap, bar, 0, part * kTile, 0, head, at);
+                const uint32_t dst = stage + lane * a.pitch;
+                if (a.both) {
+                    tma_load_5d(dst, kmap, bar, 0, part * kTile, 0, 0, at * a.c.Hkv + head);
+                } else {
+                    tma_load_5d(dst + a.k_at, kmap, bar, 0, part * kTile, 0, head, at);
+                    tma_load_5d(dst + a.v_at, vmap, bar, 0, part * kTile, 0, head, at);
+                }
             }
             __syncwarp();
             if constexpr (E4M3) {
@@ -512,7 +534,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
 }
 
 template <int DK, bool E4M3, int HT, bool TEAM>
-__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<DK, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
+__device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<Shape<DK, E4M3, HT>::kLdq, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
     constexpr int KS = DK / 16, NH = HT / 8;           // steps of 16 columns; tiles of 8 query heads
     constexpr int PB = S::kPanelBytes;
@@ -525,10 +547,11 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     // tile row 16 warp + (lane & 15): its segment of the tile and its token there
     const int my_row = 16 * warp + (lane & 15);
     const int my_seg = div_of(my_row, c.by_segp), my_off = my_row - my_seg * c.segp;
-    // where the rows that this lane addresses for ldmatrix start: a segment is all panels of its rows, one after another
+    // where the rows that this lane addresses for ldmatrix start: a segment's place holds all panels of its rows, one
+    // after another.  Keys and values are a multiple of 1024 bytes apart, so that they share the swizzled addresses.
     auto row_at = [&](int row) {
         const int j = div_of(row, c.by_segp);
-        return static_cast<uint32_t>((j * c.segp * S::kPanels + row - j * c.segp) * PB);
+        return static_cast<uint32_t>(j * a.pitch + (row - j * c.segp) * PB);
     };
     const uint32_t krow = row_at(my_row), vrow = E4M3 ? krow : row_at(16 * warp + (lane & 7) + ((lane >> 4) << 3));
     const uint32_t panel = c.seg * PB;
@@ -551,7 +574,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            const uint32_t* row = qs + (g + 8 * h) * (DK / 2);
+            const uint32_t* row = qs + (g + 8 * h) * (S::kLdq / 2);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qb[h][k][0] = E4M3 ? row[8 * k + 2 * t] : row[8 * k + t];
@@ -638,7 +661,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             if (!dead && !mbar_wait(smem_u32(&sh.full[slot]), phase, &sh.abort)) dead = true;
             last_slot = slot;
             if (!dead) {
-                const uint32_t kb = ring + slot * S::kStage, vb = kb + S::kTileBytes, sb = vb + S::kTileBytes;
+                const uint32_t st = ring + slot * S::kStage, sk = st + a.k_at, sv = st + a.v_at, sb = st + 2 * S::kTileBytes;
                 // bit i: the warp's i-th key counts
                 uint32_t counts = 0xffffu;
                 if (!whole || t0 + i == 0 || t0 + i == it.tiles - 1) {
@@ -661,7 +684,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
                         uint32_t b[4];                 // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                        ldsm4(b, kb + swizzled<PB>(krow + (k >> 3) * panel, k + (lane >> 4)));
+                        ldsm4(b, sk + swizzled<PB>(krow + (k >> 3) * panel, k + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint32_t a0, a1, a2, a3;
@@ -675,7 +698,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         uint32_t b[4];                 // (keys 0-7, 8-15) of 8 columns, then of the next 8
-                        ldsm4(b, kb + swizzled<PB>(krow + (k >> 2) * panel, 2 * k + (lane >> 4)));
+                        ldsm4(b, sk + swizzled<PB>(krow + (k >> 2) * panel, 2 * k + (lane >> 4)));
 #pragma unroll
                         for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
                     }
@@ -706,7 +729,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
-                                float d = (s[h][0][2 * j + x] + s[h][1][2 * j + x]) * f - rs[h][x];
+                                float d = __fmaf_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f, -rs[h][x]);
                                 if (masked && !ok[j]) d = -INFINITY;
                                 good &= d <= kSlack;
                                 y[h][j][x] = ex2(d);
@@ -727,7 +750,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
-                                p[j] = masked && !ok[j] ? -INFINITY : (s[h][0][2 * j + x] + s[h][1][2 * j + x]) * f;
+                                p[j] = masked && !ok[j] ? -INFINITY : __fmul_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f);
                                 top = fmaxf(top, p[j]);
                                 if constexpr (E4M3) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
                             }
@@ -755,7 +778,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                             }
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                y[h][j][x] = ex2(p[j] - us);
+                                y[h][j][x] = ex2(__fsub_rn(p[j], us));
                                 pw[h][j][x] = E4M3 ? y[h][j][x] * vf[j] * rf[h][x] : y[h][j][x];
                             }
                         }
@@ -788,7 +811,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                         for (int k = 0; k < KS; k += 2) {
                             uint32_t b[4];             // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                            ldsm4t(b, vb + swizzled<PB>(vrow + (k >> 3) * panel, k + (lane >> 4)));
+                            ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 3) * panel, k + (lane >> 4)));
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
@@ -805,7 +828,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             uint32_t b[4];             // keys 0-7 of 8 columns and the next 8, then keys 8-15
-                            ldsm4t(b, vb + swizzled<PB>(vrow + (k >> 2) * panel, 2 * k + ((lane >> 3) & 1)));
+                            ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 2) * panel, 2 * k + ((lane >> 3) & 1)));
                             if constexpr (M) b[0] &= z0, b[1] &= z0, b[2] &= z1, b[3] &= z1;
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
@@ -870,7 +893,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             float L = 0.f, f[kWarps];
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-                L += sh.l[i][hr] * weight(sh.m[i][hr], M);
+                L = __fmaf_rn(sh.l[i][hr], weight(sh.m[i][hr], M), L);
                 f[i] = weight(sh.f[i][hr], M);
             }
             float4 s[DK / (4 * TPH)];
@@ -880,7 +903,8 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
                     const float4 y = *reinterpret_cast<const float4*>(scratch + (i * 8 + hh) * kLd<DK> + 4 * (x + k * TPH));
-                    s[k].x += f[i] * y.x, s[k].y += f[i] * y.y, s[k].z += f[i] * y.z, s[k].w += f[i] * y.w;
+                    s[k].x = __fmaf_rn(f[i], y.x, s[k].x), s[k].y = __fmaf_rn(f[i], y.y, s[k].y);
+                    s[k].z = __fmaf_rn(f[i], y.z, s[k].z), s[k].w = __fmaf_rn(f[i], y.w, s[k].w);
                 }
             }
             if (h == NH - 1) {                         // the stage goes back before the sums leave
@@ -897,7 +921,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 for (int k = 0; k < DK / (4 * TPH); ++k)
                     *reinterpret_cast<float4*>(sums + 4 * (x + k * TPH)) =
                         make_float4(s[k].x * inv, s[k].y * inv, s[k].z * inv, s[k].w * inv);
-                if (x == 0) *(TEAM ? sh.lse + hr : a.part_lse + part) = L == 0.f ? -INFINITY : M + log2f(L);
+                if (x == 0) *(TEAM ? sh.lse + hr : a.part_lse + part) = L == 0.f ? -INFINITY : __fadd_rn(M, log2f(L));
             }
         }
     }
@@ -924,8 +948,8 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-template <int DK, int HT, int NS>
-__device__ void join_team(const Args& a, Control<DK, HT, NS>& sh) {
+template <int DK, int LDQ, int HT, int NS>
+__device__ void join_team(const Args& a, Control<LDQ, HT, NS>& sh) {
     const int64_t cap = (int64_t)a.max_blocks * a.cut.B;
     const int r = blockIdx.z, n = splits_of(a.cut, length_of(a, r), cap);
     const int head = static_cast<int>(blockIdx.y) / a.head_tiles, h0 = (static_cast<int>(blockIdx.y) - head * a.head_tiles) * HT;
@@ -962,7 +986,7 @@ __device__ void join_team(const Args& a, Control<DK, HT, NS>& sh) {
         const float inv = l[0] == 0.f ? 0.f : 1.f / l[0];
         const int64_t row = (int64_t)r * a.Hq + head * a.group + h0 + h;
         reinterpret_cast<uint32_t*>(a.out)[row * (DK / 2) + d] = bf16x2(ox * inv, oy * inv);
-        if (a.lse && d == 0) a.lse[row] = l[0] == 0.f ? -INFINITY : (m + log2f(l[0])) * kLn2;
+        if (a.lse && d == 0) a.lse[row] = natural(m, l[0]);
     }
 }
 
@@ -973,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, HT>::kCtas))
 split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
              const __grid_constant__ Args a) {
     using S = Shape<DK, E4M3, HT>;
-    using C = Control<DK, HT, S::kStages>;
+    using C = Control<S::kLdq, HT, S::kStages>;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     C& sh = *reinterpret_cast<C*>(base + S::kStages * S::kStage);
@@ -1007,7 +1031,7 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     if constexpr (TEAM) {
         __syncwarp();
         cluster_meet();
-        if (warp < kWarps) join_team<DK, HT, S::kStages>(a, sh);
+        if (warp < kWarps) join_team<DK>(a, sh);
         __syncwarp();
         cluster_meet();        // no CTA leaves while another reads its sums
     }
@@ -1054,7 +1078,7 @@ struct Row {
 #pragma unroll
             for (int e = 0; e < VE; e += 2) out[e / 2] = bf16x2(x[v * VE + e] * inv, x[v * VE + e + 1] * inv);
         }
-        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (a.lse && lane == 0) a.lse[row] = natural(m, l);
     }
 };
 
@@ -1169,19 +1193,47 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
     return 1;
 }
 
-static bool make_map(CUtensorMap* m, const uint8_t* ptr, const Cache& c, const Cut& cut, int dk, bool e4m3) {
+// Maps of (columns of a panel, tokens, panels, heads, pages): a box is every panel of a segment's rows.  Where a
+// page's heads follow one another at the same stride as pages do, heads and pages can be one axis, and the axis that
+// frees holds keys and values, |v - k| bytes apart: one box brings both, and the producer, which issues one in 85 cycles,
+// needs half as many.  That counts where a tile is many pages (32 requests of 0-16K in e4m3: pages of 8 tokens, 8 heads of
+// 128, 101 -> 92 us; pages of 16, heads of 64, 68 -> 59 us; one request of 4K, 9.2 -> 8.8 us); from pages of 24 tokens
+// on nothing is left of it.
+static bool make_maps(CUtensorMap* km, CUtensorMap* vm, Args* a, int dk, bool e4m3) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
-    const int e = e4m3 ? 1 : 2, inner = std::min(dk, 128 / e);
-    // (columns of a panel, tokens, panels, heads, pages): a box is every panel of a segment's rows
-    cuuint64_t dims[5] = {(cuuint64_t)inner, (cuuint64_t)c.B, (cuuint64_t)(dk / inner), (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks};
-    cuuint64_t strides[4] = {(cuuint64_t)c.st, (cuuint64_t)(inner * e), (cuuint64_t)c.sh, (cuuint64_t)c.sb};
-    cuuint32_t box[5] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, (cuuint32_t)(dk / inner), 1, 1};
-    cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(ptr),
-              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const Cache& c = a->c;
+    const Cut& cut = a->cut;
+    const int e = e4m3 ? 1 : 2, inner = std::min(dk, 128 / e), panels = dk / inner, row = dk * e;
+    const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle swizzle = inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    auto encode = [&](CUtensorMap* m, const uint8_t* ptr, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+        return fn(m, type, 5, const_cast<uint8_t*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const bool keys_first = c.k < c.v;
+    const uint64_t apart = keys_first ? c.v - c.k : c.k - c.v;
+    const bool one_axis = c.num_blocks == 1 || c.Hkv == 1 || c.sb == c.Hkv * c.sh;
+    a->both = cut.spt >= 4 && cut.seg * row % 1024 == 0 && apart != 0 && one_axis && (c.num_blocks + 1) * c.Hkv < 0x7fffffff;
+    if (a->both) {
+        const cuuint64_t dims[5] = {(cuuint64_t)inner, (cuuint64_t)c.B, (cuuint64_t)panels, 2, (cuuint64_t)(c.num_blocks * c.Hkv)};
+        const cuuint64_t strides[4] = {(cuuint64_t)c.st, (cuuint64_t)(inner * e), apart, (cuuint64_t)(c.Hkv == 1 ? c.sb : c.sh)};
+        const cuuint32_t box[5] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, (cuuint32_t)panels, 2, 1};
+        a->both = encode(km, keys_first ? c.k : c.v, dims, strides, box);      // not where they lie too far apart
+        a->pitch = 2 * cut.seg * row;
+        a->k_at = keys_first ? 0 : cut.seg * row;
+        a->v_at = keys_first ? cut.seg * row : 0;
+        *vm = *km;
+    }
+    if (a->both) return true;
+    const cuuint64_t dims[5] = {(cuuint64_t)inner, (cuuint64_t)c.B, (cuuint64_t)panels, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_blocks};
+    const cuuint64_t strides[4] = {(cuuint64_t)c.st, (cuuint64_t)(inner * e), (cuuint64_t)c.sh, (cuuint64_t)c.sb};
+    const cuuint32_t box[5] = {(cuuint32_t)inner, (cuuint32_t)cut.seg, (cuuint32_t)panels, 1, 1};
+    a->pitch = cut.segp * row;             // a copy starts on a 128-byte boundary
+    a->k_at = 0;
+    a->v_at = kTile * row;
+    return encode(km, c.k, dims, strides, box) && encode(vm, c.v, dims, strides, box);
 }
 
 // the cluster that holds a row's chunks, 0 where they do not all run at once
@@ -1314,8 +1366,7 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     a.status = dev_status;
     CUtensorMap km, vm;
     if (!encode_tiled_fn()) return UP_ERR_CUDA;
-    if (!make_map(&km, a.c.k, a.c, a.cut, cache->dk, e4m3) || !make_map(&vm, a.c.v, a.c, a.cut, cache->dk, e4m3))
-        return UP_ERR_SHAPE;
+    if (!make_maps(&km, &vm, &a, cache->dk, e4m3)) return UP_ERR_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = cache->dk == 64    ? launch_dk<64>(km, vm, a, e4m3, st)
                           : cache->dk == 128 ? launch_dk<128>(km, vm, a, e4m3, st)

@@ -427,6 +427,27 @@ def test_decode_of_short_requests_over_and_over(Hq, Hkv, dk, B, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hkv,dk", [(1, 64), (2, 128), (3, 256)])
+@pytest.mark.parametrize("B", [2, 8, 16, 32])
+def test_decode_wherever_keys_and_values_lie(B, Hkv, dk, e4m3):
+    """the same cache with keys before values, after them, interleaved by page and by head, and its pages in a wider stride"""
+    c, table, rows, qb = _decode_case(B + dk, 4 * Hkv, Hkv, dk, B, LENS, e4m3)
+    k, v, n = c.k, c.v, c.num_blocks
+    first = _check(c, table, rows, qb, LENS)
+    zeros = lambda *shape: torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.int16, device="cuda").view(k.dtype)
+    pair = zeros(2, n, Hkv, B, dk)
+    page = zeros(n, 2, Hkv, B, dk)
+    head = zeros(n, Hkv, 2, B, dk)
+    wide = zeros(2, n, Hkv + 1, B, dk)
+    for kk, vv in [(pair[0], pair[1]), (pair[1], pair[0]), (page[:, 0], page[:, 1]), (page[:, 1], page[:, 0]),
+                   (head[:, :, 0], head[:, :, 1]), (head[:, :, 1], head[:, :, 0]), (wide[0, :, :Hkv], wide[1, :, 1:])]:
+        kk.copy_(k), vv.copy_(v)
+        c.k, c.v = kk, vv
+        status, out, lse = _run_decode(c, table, LENS, _from_bits(qb))
+        assert status == 0 and torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_decode_nan_and_infinity_in_attended_rows(e4m3):
     """NaN keys or values of one KV head reach the rows of that head alone"""
     lens = (100, 90)
