@@ -2,8 +2,8 @@
 // lengths that the drop history leaves each layer (up_seqused, section 3.5, Eq. 17 of "UniPrefill:
 // Universal Long-Context Prefill Acceleration via Block-wise Dynamic Sparsification", arXiv 2605.06221).
 //
-// The positions [lo, len) of a request are cut into tiles of up to kTile rows (whole pages, or parts of
-// one page) and the tiles into chunks, by the request's own length alone.  Each (request, KV head, chunk)
+// The positions [lo, len) of a request are cut into tiles of up to kTile rows (whole pages, or equal parts of
+// pages) and the tiles into chunks, by the request's own length alone.  Each (request, KV head, chunk)
 // gives for each query head of the group
 //   lse2 = log2 sum_i 2^(s_i)   and   o = sum_i 2^(s_i - lse2) v_i,   s_i = q . k_i * sm_scale * log2 e
 // and the join adds the chunks in order: out = sum_c 2^(lse2_c - L) o_c, L = log2 sum_c 2^(lse2_c).
@@ -59,11 +59,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // a running maximum moves once a score passes it by this much (log2)
 constexpr float kTop = 256.f;        // 2^kSlack
 
-// How the positions of a request fall into segments (a page, or up to kTile rows of one), tiles of spt
-// segments, and chunks of tiles.
+// How the positions of a request fall into segments (a page, or seg rows of one), tiles of spt segments, and chunks
+// of tiles.
 struct Cut {
     int B, seg, segp, spp, spt;      // page; rows of a segment, and of its place in a tile; segments of a
-                                     // page, of a tile
+                                     // page, of a tile.  Where spp > 1, segp = seg.
+    int sc;                          // bytes of a copy of scale bytes: 16, or 8 where segments have 8 rows of a longer page
     int window, s0, most;            // s0: chunks that spread one request's heads evenly over the grid; at most
                                      // `most` times as many
     int max_splits;
@@ -98,8 +99,8 @@ __device__ __forceinline__ Range range_of(const Cut& c, int len, int64_t cap) {
     r.lo = c.window > 0 && r.len > c.window ? r.len - c.window : 0;
     const int last = r.len > 0 ? r.len - 1 : 0;
     const int p0 = r.lo ? divided(r.lo, c.by_b) : 0, p1 = divided(last, c.by_b);
-    r.seg0 = p0 * c.spp + (r.lo - p0 * c.B) / kTile;
-    r.seg1 = p1 * c.spp + (last - p1 * c.B) / kTile;
+    r.seg0 = p0 * c.spp + divided(r.lo - p0 * c.B, c.by_segp);
+    r.seg1 = p1 * c.spp + divided(last - p1 * c.B, c.by_segp);
     r.tiles = r.len > 0 ? divided(r.seg1 - r.seg0, c.by_spt) + 1 : 0;
     r.splits = 0;
     return r;
@@ -351,9 +352,16 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float low_of(uint32_t bf2) { return __uint_as_float(bf2 << 16); }
 __device__ __forceinline__ float high_of(uint32_t bf2) { return __uint_as_float(bf2 & 0xffff0000u); }
-// 16 bytes to shared memory, and one arrival of this thread at `bar` once its copies so far have landed
+// 16 or 8 bytes to shared memory, and one arrival of this thread at `bar` once its copies so far have landed
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// eight scale bytes of 1
+__device__ __forceinline__ void ones8(uint32_t dst) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0x7f7f7f7fu) : "memory");
 }
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -413,8 +421,9 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     int64_t issued = 0;
     bool dead = false;
     const int per = (32 / c.spt) * c.spt, tiles_per = 32 / c.spt;      // table entries and tiles of a batch
-    // the 16 scale bytes that this lane copies: of which segment of the tile, and from which byte of its part of a page
+    // the scale bytes that this lane copies: of which segment of the tile, and from which byte of its part of a page
     const int per_seg = (c.seg + 15) / 16, sc_seg = lane / per_seg, sc_part = (lane - sc_seg * per_seg) * 16;
+    auto part_of = [&](int s) { return c.spp == 1 ? 0 : s - div_of(s, c.by_spp) * c.spp; };      // of its page
 
     Walk w;
     if constexpr (TEAM) own_chunk(a, w); else find_run(a, w);
@@ -467,20 +476,21 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                 dead = true;
                 break;
             }
-            // segments s0 .. s0 + ns - 1 of the request (in a page of several segments one: part of its page)
+            // segments s0 .. s0 + ns - 1 of the request
             const int s0 = seg0 + (t0 + i) * c.spt, ns = min(c.spt, seg1 - s0 + 1);
-            const int part = c.spp == 1 ? 0 : s0 - div_of(s0, c.by_spp) * c.spp;
             const uint32_t stage = ring + slot * S::kStage, bar = smem_u32(&sh.full[slot]);
-            const uint32_t sc = stage + 2 * S::kTileBytes + 16 * lane;
-            int sc_page = -1;
+            const uint32_t sc = stage + 2 * S::kTileBytes + c.sc * lane;
+            int sc_page = -1, sc_from = 0;
             bool sc_mine = false;
             if constexpr (E4M3) {
                 sc_page = __shfl_sync(0xffffffffu, pages, (j * c.spt + sc_seg) & 31);
-                sc_mine = sc_seg < ns && part * kTile + sc_part < a.c.Bp;
+                sc_from = part_of(s0 + sc_seg) * c.seg + sc_part;
+                sc_mine = sc_seg < ns && sc_from < a.c.Bp;
                 if (sc_mine && (sc_page < 0 || sc_page >= a.c.num_blocks)) {       // codes of zero, scale 1
-                    const uint32_t one = 0x7f7f7f7fu;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sc), "r"(one) : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sc + kScaleBytes), "r"(one) : "memory");
+                    for (int x = 0; x < c.sc; x += 8) {
+                        ones8(sc + x);
+                        ones8(sc + kScaleBytes + x);
+                    }
                     sc_mine = false;
                 }
                 __syncwarp();
@@ -495,19 +505,25 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                     at = static_cast<int>(a.c.num_blocks);              // out of the map's bounds: zeros
                 }
                 const uint32_t dst = stage + lane * a.pitch;
+                const int from = part_of(s0 + lane) * c.seg;
                 if (a.both) {
-                    tma_load_5d(dst, kmap, bar, 0, part * kTile, 0, 0, at * a.c.Hkv + head);
+                    tma_load_5d(dst, kmap, bar, 0, from, 0, 0, at * a.c.Hkv + head);
                 } else {
-                    tma_load_5d(dst + a.k_at, kmap, bar, 0, part * kTile, 0, head, at);
-                    tma_load_5d(dst + a.v_at, vmap, bar, 0, part * kTile, 0, head, at);
+                    tma_load_5d(dst + a.k_at, kmap, bar, 0, from, 0, head, at);
+                    tma_load_5d(dst + a.v_at, vmap, bar, 0, from, 0, head, at);
                 }
             }
             __syncwarp();
             if constexpr (E4M3) {
-                const int64_t src = ((int64_t)sc_page * a.c.Hkv + head) * a.c.Bp + part * kTile + sc_part;
-                if (sc_mine && UP_IN(src, a.c.scale_limit - 15, a.status)) {
-                    copy16(sc, a.c.ks + src);
-                    copy16(sc + kScaleBytes, a.c.vs + src);
+                const int64_t src = ((int64_t)sc_page * a.c.Hkv + head) * a.c.Bp + sc_from;
+                if (sc_mine && UP_IN(src, a.c.scale_limit - c.sc + 1, a.status)) {
+                    if (c.sc == 16) {
+                        copy16(sc, a.c.ks + src);
+                        copy16(sc + kScaleBytes, a.c.vs + src);
+                    } else {
+                        copy8(sc, a.c.ks + src);
+                        copy8(sc + kScaleBytes, a.c.vs + src);
+                    }
                 }
                 arrive_after_copies(bar);
             }
@@ -555,8 +571,8 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     };
     const uint32_t krow = row_at(my_row), vrow = E4M3 ? krow : row_at(16 * warp + (lane & 7) + ((lane >> 4) << 3));
     const uint32_t panel = c.seg * PB;
-    const bool whole = c.spt * c.segp == kTile && c.segp == c.seg && (c.spp == 1 || c.B % kTile == 0);
-    const int scs = (c.seg + 15) & ~15;
+    const bool whole = c.spt * c.segp == kTile && c.segp == c.seg && (c.spp == 1 || c.B % c.seg == 0);
+    const int scs = (c.seg + c.sc - 1) & -c.sc;
     // scale bytes of the keys g and g + 8 of the warp
     uint32_t sc_at[2];
 #pragma unroll
@@ -666,7 +682,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 uint32_t counts = 0xffffu;
                 if (!whole || t0 + i == 0 || t0 + i == it.tiles - 1) {
                     const int s = it.seg0 + (t0 + i) * c.spt + my_seg;
-                    const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * kTile + my_off;
+                    const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * c.seg + my_off;
                     const int64_t pos = (int64_t)page * c.B + tok;
                     counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= it.lo &&
                                                             pos < it.len);
@@ -1158,6 +1174,15 @@ static int ctas_of(bool e4m3, int group) {
     return e4m3 ? Shape<DK, true, 16>::kCtas : Shape<DK, false, 16>::kCtas;
 }
 
+// Whole pages, or kTile rows of longer ones, leave part of a tile empty where one is no multiple of the other, and an
+// e4m3 call takes its time by the tile.  There a page goes by its largest part of 8, 16 or 32 rows: it takes more
+// copies, and every tile is full (32 requests of 0-16K, 8 heads of 128, pages of 24, 40 and 200: e4m3 112 -> 92,
+// 131 -> 89 and 103 -> 85 us, bf16 142 -> 140, 148 -> 139 and 141 -> 138 us).
+static int segment_of(int B) {
+    if (kTile % B == 0 || B % kTile == 0 || B % 8) return B < kTile ? B : kTile;
+    return B % 32 == 0 ? 32 : B % 16 == 0 ? 16 : 8;
+}
+
 // 0 for arguments that the call refuses
 static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int window, bool e4m3, Cut* c) {
     if (R <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || B <= 0 || B > (1 << 20)) return 0;
@@ -1165,10 +1190,11 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
     if (dk != 64 && dk != 128 && dk != 256) return 0;
     if ((int64_t)max_blocks * B > 0x7fffffff - 2 * kTile) return 0;
     c->B = B;
-    c->seg = B < kTile ? B : kTile;
+    c->seg = segment_of(B);
     c->segp = (c->seg + 1) & ~1;               // 64-byte rows: a segment starts on a 128-byte boundary
-    c->spp = static_cast<int>(cdiv(B, kTile));
+    c->spp = static_cast<int>(cdiv(B, c->seg));
     c->spt = kTile / c->segp;
+    c->sc = c->seg == 8 && B > 8 ? 8 : 16;
     c->window = window;
     c->by_b = kv::fast_div(B);
     c->by_spt = kv::fast_div(c->spt);
@@ -1196,9 +1222,9 @@ static int make_cut(int R, int Hq, int Hkv, int dk, int B, int max_blocks, int w
 // Maps of (columns of a panel, tokens, panels, heads, pages): a box is every panel of a segment's rows.  Where a
 // page's heads follow one another at the same stride as pages do, heads and pages can be one axis, and the axis that
 // frees holds keys and values, |v - k| bytes apart: one box brings both, and the producer, which issues one in 85 cycles,
-// needs half as many.  That counts where a tile is many pages (32 requests of 0-16K in e4m3: pages of 8 tokens, 8 heads of
-// 128, 101 -> 92 us; pages of 16, heads of 64, 68 -> 59 us; one request of 4K, 9.2 -> 8.8 us); from pages of 24 tokens
-// on nothing is left of it.
+// needs half as many.  That counts where a tile is many segments (32 requests of 0-16K in e4m3: pages of 8 tokens, 8
+// heads of 128, 101 -> 92 us; pages of 16, heads of 64, 68 -> 59 us; one request of 4K, 9.2 -> 8.8 us); of two in a
+// tile, or one, nothing is left of it.
 static bool make_maps(CUtensorMap* km, CUtensorMap* vm, Args* a, int dk, bool e4m3) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;

@@ -427,6 +427,15 @@ def test_decode_of_short_requests_over_and_over(Hq, Hkv, dk, B, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 1, 100, 333])
+@pytest.mark.parametrize("Hq,Hkv,dk,B", [(8, 2, 128, 24), (4, 1, 64, 40), (16, 2, 256, 48), (8, 2, 128, 72), (9, 1, 128, 96),
+                                         (2, 2, 256, 112), (8, 2, 64, 120), (8, 2, 128, 200)])
+def test_decode_pages_that_do_not_fill_tiles(Hq, Hkv, dk, B, window, e4m3):
+    c, table, rows, q = _decode_case(B + dk, Hq, Hkv, dk, B, LENS, e4m3, window=window)
+    _check(c, table, rows, q, LENS, window)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("Hkv,dk", [(1, 64), (2, 128), (3, 256)])
 @pytest.mark.parametrize("B", [2, 8, 16, 32])
 def test_decode_wherever_keys_and_values_lie(B, Hkv, dk, e4m3):
