@@ -15,7 +15,7 @@
 // dk / 8 neighbouring lanes, 16 bytes of bf16 each, so that its maximum is a few shuffles; the warps of a CTA
 // take the heads of the same tokens, so that they read or write whole tokens of the stream together.
 // At 32K tokens of 8 heads of 128 in e4m3 the write takes 32.5 us (6.2 TB/s of what it must move, 0.92 of the
-// measured copy rate) and the read 36.3 us (5.6 TB/s); with bf16 rows both run at the copy rate (685K tokens written
+// measured copy rate) and the read 33.9 us (6.0 TB/s, 0.89); with bf16 rows both run at the copy rate (685K tokens written
 // in 811 us, 6.9 TB/s).  What the e4m3 forms lack is issue slots: the write's instructions filled 65% of them before
 // two rows' maxima shared a shuffle and the scaling moved to pairs of bf16 (35.4 us).
 #include <stdint.h>
@@ -35,7 +35,7 @@ namespace kv {
 constexpr int kThreads = 128, kCtas = 8;
 constexpr int kChunk = 16, kSmallChunk = 4;      // tokens of a warp's unit
 constexpr int kSmallWarps = 4;                   // warps of an SM below which units are small
-constexpr int kGridPerSm = 32;                   // most CTAs of a side
+constexpr int kGridPerSm = 32;                   // most CTAs of a side on an SM, where they come in waves
 constexpr int kUnroll = 8;
 
 struct Side {              // keys or values of a call
@@ -291,7 +291,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const __grid_cons
 template <int DK, bool E4M3, int CHUNK>
 static cudaError_t launch_one(const Args& a, bool write, cudaStream_t st) {
     const int64_t units = cdiv(a.T, CHUNK) * a.c.Hkv;
-    const dim3 g(static_cast<unsigned>(std::min<int64_t>(cdiv(units, kThreads / 32), kGridPerSm * num_sms())), 2);
+    // Reads of e4m3 rows of up to 128, whose units are one batch of loads, go by CTAs that stay: no start and no last wave
+    // (32K tokens of 8 heads of 128: 36.3 -> 33.9 us, 131K 129 -> 124).  With two batches a unit (heads of 256: 215 -> 233),
+    // and with bf16 rows (32K: 41.5 -> 45.0) or a write's maxima (131K: 117 -> 132), waves keep more loads in flight.
+    const int sides = (a.side[0].dst != nullptr) + (a.side[1].dst != nullptr);
+    const int per_sm = !write && E4M3 && DK <= 128 ? kCtas / sides : kGridPerSm;
+    const dim3 g(static_cast<unsigned>(std::min<int64_t>(cdiv(units, kThreads / 32), per_sm * num_sms())), 2);
     return write ? launch_pdl(write_kernel<DK, E4M3, CHUNK>, g, dim3(kThreads), 0, st, a)
                  : launch_pdl(read_kernel<DK, E4M3, CHUNK>, g, dim3(kThreads), 0, st, a);
 }

@@ -21,6 +21,10 @@ def _bits(t):
     return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
 
 
+def _as_bits(t):
+    return t.view(torch.int16)
+
+
 def _from_bits(bits):
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
 
@@ -126,6 +130,38 @@ def test_write_and_read_are_exact(T, e4m3, Hkv, dk, B, order):
                 want = kv_ref.bf16_bits(kv_ref.dequantise(codes, b).astype(np.float32))
         want[~live] = 0
         assert np.array_equal(_bits(got), want[perm])
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hkv,dk", [(8, 64), (4, 128), (2, 256)])
+def test_a_long_read_is_that_of_its_pieces(Hkv, dk, e4m3):
+    """more tokens than the CTAs of one wave take at once; both sides, and each alone"""
+    rng = np.random.default_rng(dk)
+    T, B = 50021, 16
+    nb = -(-T // B)
+    c = Pages(nb, Hkv, B, dk, e4m3)
+    slots = rng.permutation(nb * B)[:T].astype(np.int64)
+    slots[rng.integers(0, T, 50)] = -1
+    kb, vb = (kv_ref.bf16_bits(rng.standard_normal((T, Hkv, dk)).astype(np.float32)) for _ in "kv")
+    assert _write(c, kb, vb, slots) == 0
+    sl = torch.from_numpy(slots).cuda()
+    st = _status()
+    new = lambda n: torch.full((n, Hkv, dk), 7.0, dtype=torch.bfloat16, device="cuda")
+    k, v, k1, v1 = new(T), new(T), new(T), new(T)
+    up.up_kv_read(c.k, c.v, sl, k, v, st, **c.scales())
+    up.up_kv_read(c.k, c.v, sl, k1, None, st, **c.scales())
+    up.up_kv_read(c.k, c.v, sl, None, v1, st, **c.scales())
+    assert torch.equal(_as_bits(k), _as_bits(k1)) and torch.equal(_as_bits(v), _as_bits(v1))
+    for t0 in range(0, T, 7000):
+        n = min(7000, T - t0)
+        kk, vv = new(n), new(n)
+        up.up_kv_read(c.k, c.v, sl[t0:t0 + n], kk, vv, st, **c.scales())
+        assert torch.equal(_as_bits(kk), _as_bits(k[t0:t0 + n])) and torch.equal(_as_bits(vv), _as_bits(v[t0:t0 + n]))
+    assert up.up_read_status(st) == 0
+    if not e4m3:
+        live = slots >= 0
+        assert np.array_equal(_bits(k)[live], kb[live]) and np.array_equal(_bits(v)[live], vb[live])
+        assert (_bits(k)[~live] == 0).all()
 
 
 def test_nonfinite_numbers_become_nan_codes_and_leave_the_rest_of_the_row():
