@@ -549,6 +549,31 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     }
 }
 
+// bit i: row i of a warp's 16 value rows has a code other than +0 and -0.  Lanes i and i + 16 read half of row i, which
+// starts at byte `row` (a lane's own), panels `panel` bytes apart.  The order of a row's columns does not matter here, so
+// eight neighbouring lanes take eight different ones.  Not inline: the loop around it keeps its registers (32 query heads
+// on one key head of 128: 105.8 us inline, 103.2 so).
+template <int DK, int PB>
+__device__ __noinline__ uint32_t nonzero_rows(uint32_t row, uint32_t panel) {
+    constexpr int N = PB / 16, HALF = DK / 32;         // 16-byte columns of a panel, and of half a row
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int first = (N == 8 ? lane : lane >> 1) + (DK > PB ? 0 : half * HALF);
+    const uint32_t at = row + (DK > PB ? half * panel : 0);
+    uint32_t any = 0;
+#pragma unroll 4
+    for (int i = 0; i < HALF; ++i) {
+        uint32_t x, y, z, w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                     : "r"(at + 16 * ((first + i) & (N - 1)))
+                     : "memory");
+        any |= x | y | z | w;
+    }
+    any &= 0x7f7f7f7fu;
+    any |= __shfl_xor_sync(0xffffffffu, any, 16);
+    return __ballot_sync(0xffffffffu, any != 0);
+}
+
 template <int DK, bool E4M3, int HT, bool TEAM>
 __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control<Shape<DK, E4M3, HT>::kLdq, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
     using S = Shape<DK, E4M3, HT>;
@@ -656,8 +681,8 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
         float o[NH][KS][4];
         // References: rs near the running maximum of the scores (of the sums l) and, with scaled values, rt near that of
-        // score + the value's exponent (of the sums o): a token may have nearly all the weight and values 2^-100 of
-        // another's.  -inf before the first score.  rf = 2^(rs - rt).
+        // score + the value's exponent over the rows that are not all zeros (of the sums o): a token may have nearly all the
+        // weight and values 2^-100 of another's, or none.  -inf before the first score.  rf = 2^(rs - rt).
         float rs[NH][2], rt[NH][2], rf[NH][2], l[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -758,6 +783,13 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                     return good;
                 };
                 if (!__all_sync(0xffffffffu, weigh())) {
+                    if constexpr (E4M3) {
+                        // A row of zeros adds nothing whatever its weight and scale, so it must not raise the outputs'
+                        // reference: the other rows' weights would lose their bits, or all of them, in f16.
+                        const uint32_t live = nonzero_rows<DK, PB>(sv + vrow, panel);
+                        vf[0] = (live >> g) & 1 ? vf[0] : 0.f;
+                        vf[1] = (live >> (g + 8)) & 1 ? vf[1] : 0.f;
+                    }
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -768,7 +800,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                                 const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
                                 p[j] = masked && !ok[j] ? -INFINITY : __fmul_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f);
                                 top = fmaxf(top, p[j]);
-                                if constexpr (E4M3) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
+                                if (E4M3 && vf[j] != 0.f) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
                             }
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -781,11 +813,13 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                             if constexpr (E4M3) {
 #pragma unroll
                                 for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-                                const float nt = fmaxf(rt[h][x], topv);
+                                // 126 below the scores' at least, which 2^-126 and its inverse reach: a row that could
+                                // need more has no weight left in 32 bits
+                                const float nt = fmaxf(fmaxf(rt[h][x], topv), ns - 126.f);
                                 f = weight(rt[h][x], nt);
                                 rt[h][x] = nt;
                                 ut = nt == -INFINITY ? 0.f : nt;
-                                rf[h][x] = ex2(fminf(us - ut, 126.f));
+                                rf[h][x] = ex2(us - ut);
                             }
 #pragma unroll
                             for (int k = 0; k < KS; ++k) {
