@@ -303,7 +303,10 @@ size_t up_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int dk, int B, in
  * A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a table entry outside
  * [0, num_blocks) sets UP_DEV_BAD_PAGE and its keys and values count as zeros.
  * Hq % Hkv == 0; R * Hq below 2^31; max_blocks * B at most 2^31 - 129 (UP_ERR_SHAPE otherwise).
- * Arithmetic: products of the cache's numbers with q in full, fp32 accumulation and softmax.  The range
+ * Arithmetic: products of the cache's numbers with q in full, fp32 sums, maxima and exponentials.  The weights enter
+ * the product with the values rounded: for UP_KV_BF16 to 16 bits (two bf16 parts); for UP_KV_E4M3 to 11 bits where
+ * weight * value scale is at least 2^-21 of the largest such product of the row, and with an absolute error of up
+ * to 2^-32 of that largest one below (rows of zeros do not count for it).  The range
  * of a request is split by its own length alone, so a request's result does not depend on the others.
  * ws: device workspace of up_paged_decode_workspace_bytes(...) bytes, 16-byte aligned, no initialisation. */
 up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const up_kv_cache* cache,

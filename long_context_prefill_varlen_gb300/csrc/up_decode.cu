@@ -57,7 +57,11 @@ constexpr int kScaleBytes = 512;     // room of a tile's scale bytes (keys or va
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // a running maximum moves once a score passes it by this much (log2)
-constexpr float kTop = 256.f;        // 2^kSlack
+// The weights of e4m3 values go to the second product in f16: an eighth of the output's own rounding (two f16 parts cost 2
+// to 8% of a call).  Their reference lies kLift below the largest, so that they reach 2^kLift, and
+// 2^(kLift + kSlack) before it moves, of f16's 2^16: a weight keeps its 11 bits down to 2^(-14 - kLift) of the
+// largest and has an error of 2^(-25 - kLift) below.
+constexpr float kLift = 7.f, kTop = 32768.f;
 
 // How the positions of a request fall into segments (a page, or seg rows of one), tiles of spt segments, and chunks
 // of tiles.
@@ -815,7 +819,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                                 for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
                                 // 126 below the scores' at least, which 2^-126 and its inverse reach: a row that could
                                 // need more has no weight left in 32 bits
-                                const float nt = fmaxf(fmaxf(rt[h][x], topv), ns - 126.f);
+                                const float nt = fmaxf(fmaxf(rt[h][x], topv - kLift), ns - 126.f);
                                 f = weight(rt[h][x], nt);
                                 rt[h][x] = nt;
                                 ut = nt == -INFINITY ? 0.f : nt;
@@ -842,7 +846,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         if constexpr (E4M3) {
-                            pb[h][j] = transposed(f16x2(pw[h][j][0], pw[h][j][1]));        // 11 bits: a weight's one rounding
+                            pb[h][j] = transposed(f16x2(pw[h][j][0], pw[h][j][1]));        // a weight's one rounding: see kLift
                         } else {
                             // bf16 values want bf16 weights: high and low part, 16 bits together
                             const uint32_t hi = bf16x2(pw[h][j][0], pw[h][j][1]);

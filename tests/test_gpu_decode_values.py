@@ -90,3 +90,23 @@ def test_a_page_out_of_range_counts_as_zeros_among_small_values(size, e4m3):
     k[32:48] = v[32:48] = 0
     o, _, tol, _ = kv_ref.decode(kv_ref.bf16_value(qb), [k], [v], 64 ** -0.5)
     assert (np.abs(kv_ref.bf16_value(_bits(out)) - o) <= tol).all()
+
+
+@pytest.mark.parametrize("nats", [13, 16, 20, 30])
+@pytest.mark.parametrize("n", [16, 100, 1000])
+def test_the_last_bits_of_light_rows_beside_a_heavy_one(n, nats):
+    """An e4m3 cache's weights are f16 numbers whose reference lies 2^-7 below the largest weight * value scale W: to half a
+    step of f16's subnormals, 2^-25, an error is 2^-32 W and a code's size that of the row's number."""
+    c, table, qb = _case(n + nats, n, [7], nats, 1.0, True, _every_other_column)
+    status, out, _ = _run_decode(c, table, [n], _from_bits(qb))
+    assert status == 0
+    rows = np.arange(n)
+    k, v, q = c.rows("k", rows), c.rows("v", rows), kv_ref.bf16_value(qb)
+    o, _, tol, _ = kv_ref.decode(q, [k], [v], 64 ** -0.5)
+    scale = 2.0 ** (c.vs.cpu().numpy()[rows // 16, 0, rows % 16].astype(float) - 127)
+    s = q[0] @ k[:, 0].T * 64 ** -0.5
+    p = np.exp(s - s.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    largest = (p * scale).max(1)[:, None]                      # W of each head
+    tol[0] += (1 + kv_ref.BF16) * 2.0 ** -32 * largest * (np.abs(v[:, 0]) / scale[:, None]).sum(0)
+    assert (np.abs(kv_ref.bf16_value(_bits(out)) - o) <= tol).all()
