@@ -399,6 +399,7 @@ struct Control {
     float m[kWarps][16], f[kWarps][16], l[kWarps][16];
     float lse[16];                             // of a cluster's chunk; its sums take the queries' place
     uint64_t full[NS], empty[NS], qfull[2], qempty[2], ifull[kItems], iempty[kItems], joined;
+    int64_t tiles, queries;                    // copies that the producer issued: to the ring, to the two query slots
     int abort;
 };
 
@@ -414,6 +415,31 @@ struct Sizes {
 
 // ------------------------------------------------------------------------------------------------
 
+// mbar_wait for a converged warp: one answer for all of its lanes.  Where one lane's time ran out no lane goes on, so that
+// the warp's shuffles and votes stay whole.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
+}
+
+// A role whose wait runs out reports it, raises the CTA's flag and leaves at once, without another arrival: what it has
+// not read must not be overwritten, and no barrier is armed twice.  The others follow at their next wait.
+__device__ __forceinline__ void give_up(const Args& a) {
+    if ((threadIdx.x & 31) == 0) set_status(a.status, UP_DEV_WAIT_TIMEOUT);
+}
+
+// Before the CTA of an aborted run goes: the copies in flight write its shared memory, so wait for them (again with a limit).
+template <int LDQ, int HT, int NS>
+__device__ __noinline__ void drain(Control<LDQ, HT, NS>& sh) {
+    const uint64_t t0 = globaltimer_ns();
+    const int64_t tiles = sh.tiles, queries = sh.queries;
+    for (int64_t k = tiles < NS ? 0 : tiles - NS; k < tiles; ++k)
+        while (!mbar_try_wait(smem_u32(&sh.full[k % NS]), (k / NS) & 1))
+            if (globaltimer_ns() - t0 > kDrainLimitNs) return;
+    for (int64_t k = queries < 2 ? 0 : queries - 2; k < queries; ++k)
+        while (!mbar_try_wait(smem_u32(&sh.qfull[k % 2]), (k / 2) & 1))
+            if (globaltimer_ns() - t0 > kDrainLimitNs) return;
+}
+
 template <int DK, bool E4M3, int HT, bool TEAM>
 __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMap* vmap, uint32_t ring,
                         Control<Shape<DK, E4M3, HT>::kLdq, HT, Shape<DK, E4M3, HT>::kStages>& sh) {
@@ -422,8 +448,11 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     const Cut& c = a.cut;
     int slot = 0, qslot = 0, islot = 0;
     uint32_t phase = 0, qphase = 0, iphase = 0;
-    int64_t issued = 0;
-    bool dead = false;
+    int64_t tiles = 0, queries = 0;
+    auto leave = [&](bool in_order) {
+        if (!in_order) give_up(a);
+        if (lane == 0) sh.tiles = tiles, sh.queries = queries;
+    };
     const int per = (32 / c.spt) * c.spt, tiles_per = 32 / c.spt;      // table entries and tiles of a batch
     // the scale bytes that this lane copies: of which segment of the tile, and from which byte of its part of a page
     const int per_seg = (c.seg + 15) / 16, sc_seg = lane / per_seg, sc_part = (lane - sc_seg * per_seg) * 16;
@@ -443,13 +472,14 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
     };
     int first_pages = fetch(w, 0);
     int q_r = -1, q_head = -1, q_ht = -1;                               // whose queries were sent last
-    while (w.live(a) && !dead) {
+    while (w.live(a)) {
         const int head = w.head, h0 = w.ht * HT;
         const bool fresh_q = w.r != q_r || head != q_head || w.ht != q_ht;
         if (fresh_q) {
             q_r = w.r, q_head = head, q_ht = w.ht;
             const int heads = min(HT, a.group - h0);
-            if (!mbar_wait(smem_u32(&sh.qempty[qslot]), qphase ^ 1, &sh.abort)) break;
+            if (!warp_wait(&sh.qempty[qslot], qphase ^ 1, &sh.abort)) return leave(false);
+            ++queries;
             const uint32_t bar = smem_u32(&sh.qfull[qslot]), dst = smem_u32(sh.q[qslot]);
             const uint8_t* src = a.q + w.r * a.q_stride + (int64_t)(head * a.group + h0) * DK * 2;
             if (lane == 0) mbar_arrive_expect_tx(bar, heads * DK * 2);
@@ -463,7 +493,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
             }
             if (++qslot == 2) qslot = 0, qphase ^= 1;
         }
-        if (!mbar_wait(smem_u32(&sh.iempty[islot]), iphase ^ 1, &sh.abort)) break;
+        if (!warp_wait(&sh.iempty[islot], iphase ^ 1, &sh.abort)) return leave(false);
         if (lane == 0) {
             sh.item[islot] = Item{w.r, head, w.ch, h0, w.t0, w.n, w.g.tiles, w.g.seg0, w.g.lo, w.g.len, fresh_q, 0};
             mbar_arrive(smem_u32(&sh.ifull[islot]));
@@ -476,10 +506,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                 j = 0;
                 pages = pages_next;
             }
-            if (!mbar_wait(smem_u32(&sh.empty[slot]), phase ^ 1, &sh.abort)) {
-                dead = true;
-                break;
-            }
+            if (!warp_wait(&sh.empty[slot], phase ^ 1, &sh.abort)) return leave(false);
             // segments s0 .. s0 + ns - 1 of the request
             const int s0 = seg0 + (t0 + i) * c.spt, ns = min(c.spt, seg1 - s0 + 1);
             const uint32_t stage = ring + slot * S::kStage, bar = smem_u32(&sh.full[slot]);
@@ -531,7 +558,7 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
                 }
                 arrive_after_copies(bar);
             }
-            ++issued;
+            ++tiles;
             if (++slot == S::kStages) slot = 0, phase ^= 1;
             if (j == 0) pages_next = fetch(w, i + tiles_per);           // the batch after this one
         }
@@ -539,18 +566,12 @@ __device__ void produce(const Args& a, const CUtensorMap* kmap, const CUtensorMa
         w.next(a);
         first_pages = fetch(w, 0);
     }
-    if (!dead && mbar_wait(smem_u32(&sh.iempty[islot]), iphase ^ 1, &sh.abort) && lane == 0) {
+    if (!warp_wait(&sh.iempty[islot], iphase ^ 1, &sh.abort)) return leave(false);
+    if (lane == 0) {
         sh.item[islot].n = 0;
         mbar_arrive(smem_u32(&sh.ifull[islot]));
     }
-    if (dead || sh.abort) {
-        // let the copies in flight land before the CTA goes (they write its shared memory)
-        const uint64_t t0 = globaltimer_ns();
-        const int64_t last = issued < S::kStages ? issued : S::kStages;
-        for (int64_t k = issued - last; k < issued; ++k)
-            while (!mbar_try_wait(smem_u32(&sh.full[k % S::kStages]), (k / S::kStages) & 1))
-                if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-    }
+    leave(true);
 }
 
 // bit i: row i of a warp's 16 value rows has a code other than +0 and -0.  Lanes i and i + 16 read half of row i, which
@@ -587,7 +608,6 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     const Cut& c = a.cut;
     int slot = 0, qslot = 0;
     uint32_t phase = 0, qphase = 0;
-    bool dead = false;
 
     // tile row 16 warp + (lane & 15): its segment of the tile and its token there
     const int my_row = 16 * warp + (lane & 15);
@@ -615,7 +635,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
     // queries to registers, as the products' second operand: head g (of each tile of 8), columns
     // 16k + {2t, 2t+1, 2t+8, 2t+9}; for e4m3 16k + 4t .. 4t+3, the order that the key bytes come in
     auto load_queries = [&](int heads) {
-        if (!dead && !mbar_wait(smem_u32(&sh.qfull[qslot]), qphase, &sh.abort)) dead = true;
+        if (!warp_wait(&sh.qfull[qslot], qphase, &sh.abort)) return false;
         const uint32_t* qs = reinterpret_cast<const uint32_t*>(sh.q[qslot]);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -655,31 +675,30 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.qempty[qslot]));
         if (++qslot == 2) qslot = 0, qphase ^= 1;
+        return true;
     };
 
-    // the consumer warps meet: a bounded wait like the others (a warp that has given up may have left)
+    // the consumer warps meet: a bounded wait like the others (a warp that has given up has left)
     uint32_t jphase = 0;
     auto meet = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.joined));
-        if (!dead && !mbar_wait(smem_u32(&sh.joined), jphase, &sh.abort)) dead = true;
+        const bool all = warp_wait(&sh.joined, jphase, &sh.abort);
         jphase ^= 1;
+        return all;
     };
 
     int islot = 0;
     uint32_t iphase = 0;
     for (;;) {
-        if (!mbar_wait(smem_u32(&sh.ifull[islot]), iphase, &sh.abort)) {
-            dead = true;
-            break;
-        }
+        if (!warp_wait(&sh.ifull[islot], iphase, &sh.abort)) return give_up(a);
         const Item it = sh.item[islot];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.iempty[islot]));
         if (++islot == kItems) islot = 0, iphase ^= 1;
-        if (it.n == 0) break;
+        if (it.n == 0) return;
         const int heads = min(HT, a.group - it.h0);
-        if (it.fresh) load_queries(heads);
+        if (it.fresh && !load_queries(heads)) return give_up(a);
 
         // sums of the warp's keys, heads 2t and 2t + 1 (of each tile of 8).  o[h][k]: columns 16k + g (0, 1) and
         // 16k + g + 8 (2, 3); for e4m3 16k + 2g and 16k + 2g + 1.
@@ -703,197 +722,195 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         const int n = it.n, t0 = it.t0;
         int last_slot = 0;
         for (int i = 0; i < n; ++i) {
-            if (!dead && !mbar_wait(smem_u32(&sh.full[slot]), phase, &sh.abort)) dead = true;
+            if (!warp_wait(&sh.full[slot], phase, &sh.abort)) return give_up(a);
             last_slot = slot;
-            if (!dead) {
-                const uint32_t st = ring + slot * S::kStage, sk = st + a.k_at, sv = st + a.v_at, sb = st + 2 * S::kTileBytes;
-                // bit i: the warp's i-th key counts
-                uint32_t counts = 0xffffu;
-                if (!whole || t0 + i == 0 || t0 + i == it.tiles - 1) {
-                    const int s = it.seg0 + (t0 + i) * c.spt + my_seg;
-                    const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * c.seg + my_off;
-                    const int64_t pos = (int64_t)page * c.B + tok;
-                    counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= it.lo &&
-                                                            pos < it.len);
+            const uint32_t st = ring + slot * S::kStage, sk = st + a.k_at, sv = st + a.v_at, sb = st + 2 * S::kTileBytes;
+            // bit i: the warp's i-th key counts
+            uint32_t counts = 0xffffu;
+            if (!whole || t0 + i == 0 || t0 + i == it.tiles - 1) {
+                const int s = it.seg0 + (t0 + i) * c.spt + my_seg;
+                const int page = div_of(s, c.by_spp), tok = (s - page * c.spp) * c.seg + my_off;
+                const int64_t pos = (int64_t)page * c.B + tok;
+                counts = __ballot_sync(0xffffffffu, my_seg < c.spt && my_off < c.seg && tok < c.B && pos >= it.lo &&
+                                                        pos < it.len);
+            }
+            const bool masked = counts != 0xffffu;
+            if (counts != 0) {                     // else nothing for this warp (rows that odd pages leave unused)
+            // scores, keys in the rows: s[h] = (key g: heads 2t, 2t + 1; key g + 8: the same), in two parts so
+            // that a product need not wait for the one before
+            float s[NH][2][4];
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[h][0][x] = s[h][1][x] = 0.f;
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int k = 0; k < KS; k += 2) {
+                    uint32_t b[4];                 // (keys 0-7, 8-15) of 16 bytes, then of the next 16
+                    ldsm4(b, sk + swizzled<PB>(krow + (k >> 3) * panel, k + (lane >> 4)));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t a0, a1, a2, a3;
+                        kv::e4m3x4_to_f16x4(b[2 * x], a0, a2);
+                        kv::e4m3x4_to_f16x4(b[2 * x + 1], a1, a3);
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) mma<true>(s[h][x], a0, a1, a2, a3, qb[h][k + x][0], qb[h][k + x][1]);
+                    }
                 }
-                const bool masked = counts != 0xffffu;
-                if (counts != 0) {                     // else nothing for this warp (rows that odd pages leave unused)
-                // scores, keys in the rows: s[h] = (key g: heads 2t, 2t + 1; key g + 8: the same), in two parts so
-                // that a product need not wait for the one before
-                float s[NH][2][4];
+            } else {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];                 // (keys 0-7, 8-15) of 8 columns, then of the next 8
+                    ldsm4(b, sk + swizzled<PB>(krow + (k >> 2) * panel, 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
+                }
+            }
+            float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f};      // scales of the keys' and values' rows g, g + 8
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    kf[j] = __uint_as_float(max(lds_u8(sb + sc_at[j]) << 23, 0x00400000u));    // 2^(b - 127)
+                    vf[j] = __uint_as_float(max(lds_u8(sb + kScaleBytes + sc_at[j]) << 23, 0x00400000u));
+                }
+            }
+            const bool ok[2] = {((counts >> g) & 1) != 0, ((counts >> (g + 8)) & 1) != 0};
+            if (E4M3 && masked) {                  // bytes that nobody wrote may stand for infinity
+                vf[0] = ok[0] ? vf[0] : 0.f;
+                vf[1] = ok[1] ? vf[1] : 0.f;
+            }
+            // Of key g + 8j and head 2t + x: y[h][j][x] = 2^(score - rs), and pw the same times the value's scale over
+            // 2^(rt - rs).  The references stay while no weight passes 2^kSlack: a weight that does, or is NaN (also
+            // before the first score), has all the warp's moved.
+            float y[NH][2][2], pw[NH][2][2];
+            auto weigh = [&]() {
+                bool good = true;
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) s[h][0][x] = s[h][1][x] = 0.f;
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
+                            float d = __fmaf_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f, -rs[h][x]);
+                            if (masked && !ok[j]) d = -INFINITY;
+                            good &= d <= kSlack;
+                            y[h][j][x] = ex2(d);
+                            pw[h][j][x] = y[h][j][x];
+                            if constexpr (E4M3) {
+                                pw[h][j][x] = y[h][j][x] * vf[j] * rf[h][x];
+                                good &= pw[h][j][x] <= kTop;
+                            }
+                        }
+                return good;
+            };
+            if (!__all_sync(0xffffffffu, weigh())) {
+                if constexpr (E4M3) {
+                    // A row of zeros adds nothing whatever its weight and scale, so it must not raise the outputs'
+                    // reference: the other rows' weights would lose their bits, or all of them, in f16.
+                    const uint32_t live = nonzero_rows<DK, PB>(sv + vrow, panel);
+                    vf[0] = (live >> g) & 1 ? vf[0] : 0.f;
+                    vf[1] = (live >> (g + 8)) & 1 ? vf[1] : 0.f;
+                }
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float p[2], top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
+                            p[j] = masked && !ok[j] ? -INFINITY : __fmul_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f);
+                            top = fmaxf(top, p[j]);
+                            if (E4M3 && vf[j] != 0.f) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
+                        }
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float ns = fmaxf(rs[h][x], top);
+                        float f = weight(rs[h][x], ns);
+                        l[h][x] *= f;
+                        rs[h][x] = ns;
+                        const float us = ns == -INFINITY ? 0.f : ns;       // 0 stands in for a reference of -inf
+                        float ut = 0.f;
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
+                            // 126 below the scores' at least, which 2^-126 and its inverse reach: a row that could
+                            // need more has no weight left in 32 bits
+                            const float nt = fmaxf(fmaxf(rt[h][x], topv - kLift), ns - 126.f);
+                            f = weight(rt[h][x], nt);
+                            rt[h][x] = nt;
+                            ut = nt == -INFINITY ? 0.f : nt;
+                            rf[h][x] = ex2(us - ut);
+                        }
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            o[h][k][x] *= f;
+                            o[h][k][2 + x] *= f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            y[h][j][x] = ex2(__fsub_rn(p[j], us));
+                            pw[h][j][x] = E4M3 ? y[h][j][x] * vf[j] * rf[h][x] : y[h][j][x];
+                        }
+                    }
+            }
+            // weights, transposed to the second operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of head g)
+            uint32_t pb[NH][2], lo[NH][2];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) l[h][x] += y[h][0][x] + y[h][1][x];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (E4M3) {
+                        pb[h][j] = transposed(f16x2(pw[h][j][0], pw[h][j][1]));        // a weight's one rounding: see kLift
+                    } else {
+                        // bf16 values want bf16 weights: high and low part, 16 bits together
+                        const uint32_t hi = bf16x2(pw[h][j][0], pw[h][j][1]);
+                        pb[h][j] = transposed(hi);
+                        lo[h][j] = transposed(bf16x2(pw[h][j][0] - low_of(hi), pw[h][j][1] - high_of(hi)));
+                    }
+                }
+            }
+            // values, columns in the rows; a key that does not count is zero, whatever its row holds
+            const uint32_t c0 = counts >> (2 * t), c1 = counts >> (2 * t + 8);
+            const uint32_t z0 = (c0 & 1 ? 0xffffu : 0u) | (c0 & 2 ? 0xffff0000u : 0u);
+            const uint32_t z1 = (c1 & 1 ? 0xffffu : 0u) | (c1 & 2 ? 0xffff0000u : 0u);
+            auto values = [&](auto with_mask) {
+                constexpr bool M = decltype(with_mask)::value;
                 if constexpr (E4M3) {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
-                        uint32_t b[4];                 // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                        ldsm4(b, sk + swizzled<PB>(krow + (k >> 3) * panel, k + (lane >> 4)));
+                        uint32_t b[4];             // (keys 0-7, 8-15) of 16 bytes, then of the next 16
+                        ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 3) * panel, k + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            uint32_t a0, a1, a2, a3;
-                            kv::e4m3x4_to_f16x4(b[2 * x], a0, a2);
-                            kv::e4m3x4_to_f16x4(b[2 * x + 1], a1, a3);
+                            // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
+                            const uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
+                            uint32_t e0, e1, d0, d1;
+                            kv::e4m3x4_to_f16x4(b0, e0, d0);
+                            kv::e4m3x4_to_f16x4(b1, e1, d1);
+                            if constexpr (M) e0 &= z0, d0 &= z0, e1 &= z1, d1 &= z1;
 #pragma unroll
-                            for (int h = 0; h < NH; ++h) mma<true>(s[h][x], a0, a1, a2, a3, qb[h][k + x][0], qb[h][k + x][1]);
+                            for (int h = 0; h < NH; ++h) mma<true>(o[h][k + x], e0, d0, e1, d1, pb[h][0], pb[h][1]);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        uint32_t b[4];                 // (keys 0-7, 8-15) of 8 columns, then of the next 8
-                        ldsm4(b, sk + swizzled<PB>(krow + (k >> 2) * panel, 2 * k + (lane >> 4)));
+                        uint32_t b[4];             // keys 0-7 of 8 columns and the next 8, then keys 8-15
+                        ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 2) * panel, 2 * k + ((lane >> 3) & 1)));
+                        if constexpr (M) b[0] &= z0, b[1] &= z0, b[2] &= z1, b[3] &= z1;
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) mma<false>(s[h][k & 1], b[0], b[1], b[2], b[3], qb[h][k][0], qb[h][k][1]);
-                    }
-                }
-                float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f};      // scales of the keys' and values' rows g, g + 8
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        kf[j] = __uint_as_float(max(lds_u8(sb + sc_at[j]) << 23, 0x00400000u));    // 2^(b - 127)
-                        vf[j] = __uint_as_float(max(lds_u8(sb + kScaleBytes + sc_at[j]) << 23, 0x00400000u));
-                    }
-                }
-                const bool ok[2] = {((counts >> g) & 1) != 0, ((counts >> (g + 8)) & 1) != 0};
-                if (E4M3 && masked) {                  // bytes that nobody wrote may stand for infinity
-                    vf[0] = ok[0] ? vf[0] : 0.f;
-                    vf[1] = ok[1] ? vf[1] : 0.f;
-                }
-                // Of key g + 8j and head 2t + x: y[h][j][x] = 2^(score - rs), and pw the same times the value's scale over
-                // 2^(rt - rs).  The references stay while no weight passes 2^kSlack: a weight that does, or is NaN (also
-                // before the first score), has all the warp's moved.
-                float y[NH][2][2], pw[NH][2][2];
-                auto weigh = [&]() {
-                    bool good = true;
-#pragma unroll
-                    for (int h = 0; h < NH; ++h)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
-                                float d = __fmaf_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f, -rs[h][x]);
-                                if (masked && !ok[j]) d = -INFINITY;
-                                good &= d <= kSlack;
-                                y[h][j][x] = ex2(d);
-                                pw[h][j][x] = y[h][j][x];
-                                if constexpr (E4M3) {
-                                    pw[h][j][x] = y[h][j][x] * vf[j] * rf[h][x];
-                                    good &= pw[h][j][x] <= kTop;
-                                }
-                            }
-                    return good;
-                };
-                if (!__all_sync(0xffffffffu, weigh())) {
-                    if constexpr (E4M3) {
-                        // A row of zeros adds nothing whatever its weight and scale, so it must not raise the outputs'
-                        // reference: the other rows' weights would lose their bits, or all of them, in f16.
-                        const uint32_t live = nonzero_rows<DK, PB>(sv + vrow, panel);
-                        vf[0] = (live >> g) & 1 ? vf[0] : 0.f;
-                        vf[1] = (live >> (g + 8)) & 1 ? vf[1] : 0.f;
-                    }
-#pragma unroll
-                    for (int h = 0; h < NH; ++h)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float p[2], top = -INFINITY, topv = -INFINITY;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float f = E4M3 ? kf[j] * qf[h][x] : qf[h][x];
-                                p[j] = masked && !ok[j] ? -INFINITY : __fmul_rn(s[h][0][2 * j + x] + s[h][1][2 * j + x], f);
-                                top = fmaxf(top, p[j]);
-                                if (E4M3 && vf[j] != 0.f) topv = fmaxf(topv, p[j] + static_cast<float>(static_cast<int>(__float_as_uint(vf[j]) >> 23) - 127));
-                            }
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                            const float ns = fmaxf(rs[h][x], top);
-                            float f = weight(rs[h][x], ns);
-                            l[h][x] *= f;
-                            rs[h][x] = ns;
-                            const float us = ns == -INFINITY ? 0.f : ns;       // 0 stands in for a reference of -inf
-                            float ut = 0.f;
-                            if constexpr (E4M3) {
-#pragma unroll
-                                for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-                                // 126 below the scores' at least, which 2^-126 and its inverse reach: a row that could
-                                // need more has no weight left in 32 bits
-                                const float nt = fmaxf(fmaxf(rt[h][x], topv - kLift), ns - 126.f);
-                                f = weight(rt[h][x], nt);
-                                rt[h][x] = nt;
-                                ut = nt == -INFINITY ? 0.f : nt;
-                                rf[h][x] = ex2(us - ut);
-                            }
-#pragma unroll
-                            for (int k = 0; k < KS; ++k) {
-                                o[h][k][x] *= f;
-                                o[h][k][2 + x] *= f;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                y[h][j][x] = ex2(__fsub_rn(p[j], us));
-                                pw[h][j][x] = E4M3 ? y[h][j][x] * vf[j] * rf[h][x] : y[h][j][x];
-                            }
-                        }
-                }
-                // weights, transposed to the second operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of head g)
-                uint32_t pb[NH][2], lo[NH][2];
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) l[h][x] += y[h][0][x] + y[h][1][x];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if constexpr (E4M3) {
-                            pb[h][j] = transposed(f16x2(pw[h][j][0], pw[h][j][1]));        // a weight's one rounding: see kLift
-                        } else {
-                            // bf16 values want bf16 weights: high and low part, 16 bits together
-                            const uint32_t hi = bf16x2(pw[h][j][0], pw[h][j][1]);
-                            pb[h][j] = transposed(hi);
-                            lo[h][j] = transposed(bf16x2(pw[h][j][0] - low_of(hi), pw[h][j][1] - high_of(hi)));
+                        for (int h = 0; h < NH; ++h) {
+                            mma<false>(o[h][k], b[0], b[1], b[2], b[3], pb[h][0], pb[h][1]);
+                            mma<false>(o[h][k], b[0], b[1], b[2], b[3], lo[h][0], lo[h][1]);
                         }
                     }
                 }
-                // values, columns in the rows; a key that does not count is zero, whatever its row holds
-                const uint32_t c0 = counts >> (2 * t), c1 = counts >> (2 * t + 8);
-                const uint32_t z0 = (c0 & 1 ? 0xffffu : 0u) | (c0 & 2 ? 0xffff0000u : 0u);
-                const uint32_t z1 = (c1 & 1 ? 0xffffu : 0u) | (c1 & 2 ? 0xffff0000u : 0u);
-                auto values = [&](auto with_mask) {
-                    constexpr bool M = decltype(with_mask)::value;
-                    if constexpr (E4M3) {
-#pragma unroll
-                        for (int k = 0; k < KS; k += 2) {
-                            uint32_t b[4];             // (keys 0-7, 8-15) of 16 bytes, then of the next 16
-                            ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 3) * panel, k + (lane >> 4)));
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                // bytes (key, column): (2t, 2g) (2t, 2g+1) (2t+1, 2g) (2t+1, 2g+1)
-                                const uint32_t b0 = __byte_perm(b[2 * x], 0, 0x3120), b1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
-                                uint32_t e0, e1, d0, d1;
-                                kv::e4m3x4_to_f16x4(b0, e0, d0);
-                                kv::e4m3x4_to_f16x4(b1, e1, d1);
-                                if constexpr (M) e0 &= z0, d0 &= z0, e1 &= z1, d1 &= z1;
-#pragma unroll
-                                for (int h = 0; h < NH; ++h) mma<true>(o[h][k + x], e0, d0, e1, d1, pb[h][0], pb[h][1]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            uint32_t b[4];             // keys 0-7 of 8 columns and the next 8, then keys 8-15
-                            ldsm4t(b, sv + swizzled<PB>(vrow + (k >> 2) * panel, 2 * k + ((lane >> 3) & 1)));
-                            if constexpr (M) b[0] &= z0, b[1] &= z0, b[2] &= z1, b[3] &= z1;
-#pragma unroll
-                            for (int h = 0; h < NH; ++h) {
-                                mma<false>(o[h][k], b[0], b[1], b[2], b[3], pb[h][0], pb[h][1]);
-                                mma<false>(o[h][k], b[0], b[1], b[2], b[3], lo[h][0], lo[h][1]);
-                            }
-                        }
-                    }
-                };
-                if (masked) values(std::true_type{}); else values(std::false_type{});
-                }
+            };
+            if (masked) values(std::true_type{}); else values(std::false_type{});
             }
             if (i + 1 < n) {                           // the last stage is kept for the join of the warps
                 fence_proxy_async_smem();              // its next content comes by the async proxy
@@ -911,7 +928,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[h][x] += __shfl_xor_sync(0xffffffffu, l[h][x], d);
-        meet();                                        // every warp is done with the stage, and with sh.m of the last item
+        if (!meet()) return give_up(a);                // every warp is done with the stage, and with sh.m of the last item
         if (g == 0) {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
@@ -924,7 +941,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            if (h) meet();
+            if (h && !meet()) return give_up(a);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float* row = scratch + (warp * 8 + 2 * t + x) * kLd<DK>;
@@ -938,7 +955,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                     }
                 }
             }
-            meet();
+            if (!meet()) return give_up(a);
             constexpr int TPH = 4 * kWarps;            // threads of a head
             const int hh = threadIdx.x / TPH, x = threadIdx.x % TPH, hr = 8 * h + hh;
             float M = sh.m[0][hr];
@@ -967,7 +984,7 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[last_slot]));
             }
             const int64_t part = ((int64_t)it.r * a.Hq + it.head * a.group + it.h0 + hr) * c.max_splits + it.ch;
-            if (hr < heads && !dead && (TEAM || UP_IN(part, a.parts, a.status))) {
+            if (hr < heads && (TEAM || UP_IN(part, a.parts, a.status))) {
                 float* sums = TEAM ? reinterpret_cast<float*>(sh.q) + hr * DK : a.part_o + part * DK;
                 // L = 0: no score above -inf.  NaN goes through.
                 const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -979,7 +996,6 @@ __device__ void consume(const Args& a, uint32_t ring, uint8_t* ring_ptr, Control
             }
         }
     }
-    if (dead && threadIdx.x == 0) set_status(a.status, UP_DEV_WAIT_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1088,7 +1104,10 @@ split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         if (warp < kWarps) join_team<DK>(a, sh);
         __syncwarp();
         cluster_meet();        // no CTA leaves while another reads its sums
+    } else {
+        __syncthreads();
     }
+    if (warp == kWarps && sh.abort) drain(sh);
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -78,8 +78,16 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // Every pipeline wait in this library gives up after this long, records
-// UP_DEV_WAIT_TIMEOUT and lets the kernel wind down instead of hanging.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// UP_DEV_WAIT_TIMEOUT and lets the kernel wind down instead of hanging.  UP_WAIT_LIMIT_NS makes a build whose
+// waits do run out, to test that: it looks at the clock at every poll, and polls without suspending.
+constexpr uint64_t kDrainLimitNs = 2000000000ull;      // for copies in flight when a kernel has given up
+#ifdef UP_WAIT_LIMIT_NS
+constexpr uint64_t kWaitLimitNs = UP_WAIT_LIMIT_NS;
+constexpr uint32_t kWaitPolls = 1;
+#else
+constexpr uint64_t kWaitLimitNs = kDrainLimitNs;
+constexpr uint32_t kWaitPolls = 32;                    // polls from one look at the clock to the next
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -107,7 +115,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+#ifdef UP_WAIT_LIMIT_NS
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+#else
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+#endif
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -122,7 +134,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 31u) == 0) {
+        if (i % kWaitPolls == 0) {
             if (*abort_flag) return false;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
                 *abort_flag = 1;
