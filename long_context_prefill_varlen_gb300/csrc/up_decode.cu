@@ -34,7 +34,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "up_kv.cuh"
@@ -1333,14 +1332,13 @@ static cudaError_t prepare_split() {
     constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     static_assert(Shape<DK, E4M3, HT>::kStage >= 8 * kWarps * kLd<DK> * 4, "the join of the warps fits a stage");
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (TEAM && attr == cudaSuccess)
-            attr = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static DeviceSet done{0};
+    return once_per_device(done, [] {
+        const cudaError_t e = cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return TEAM && e == cudaSuccess
+                   ? cudaFuncSetAttribute(split_kernel<DK, E4M3, HT, TEAM>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
+                   : e;
     });
-    return attr;
 }
 
 template <int DK, bool E4M3, int HT>
@@ -1373,13 +1371,11 @@ static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, cons
 // would have to run empty between the two.
 template <int DK, int W>
 static cudaError_t launch_join(const Args& a, int64_t ctas, cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(join_kernel<DK, W>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                    cudaSharedmemCarveoutMaxShared);
+    static DeviceSet done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(join_kernel<DK, W>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     });
-    if (attr != cudaSuccess) return attr;
+    if (e != cudaSuccess) return e;
     return launch_pdl(join_kernel<DK, W>, dim3(static_cast<unsigned>(ctas)), dim3(W == 16 ? 512 : 128), 0, st, a);
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/uniprefill.h"
 
 namespace up {
@@ -23,6 +25,21 @@ EncodeTiledFn encode_tiled_fn();       // cuTensorMapEncodeTiled of the loaded d
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Runs set_up once on each device, before a kernel's first launch there: function attributes belong to the current
+// device's copy of the kernel.  A set-up that failed is tried again by the next call; two threads may both run it.
+typedef std::atomic<uint64_t> DeviceSet;           // bit d: device d is set up
+template <typename F>
+inline cudaError_t once_per_device(DeviceSet& done, F set_up) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = set_up();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Every kernel of the library is launched with programmatic dependent launch: its CTAs may become
 // resident (and set up shared memory, barriers and TMEM) while the previous kernel in the stream is

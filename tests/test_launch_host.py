@@ -1,0 +1,65 @@
+"""The host side of the library's launches (no GPU): its objects linked with a stand-in for the CUDA runtime, which keeps
+attributes per device, refuses what they do not allow and can be told to fail."""
+import ctypes
+import itertools
+import os
+import subprocess
+
+import pytest
+
+from long_context_prefill_varlen_gb300 import _build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+A = 0x1000                     # never dereferenced
+# the stand-in's second GPU and further ones: a test takes one that no test had before
+fresh_device = itertools.count(1).__next__
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    import long_context_prefill_varlen_gb300 as up
+    _build.build()
+    objects = [os.path.join(_build.PKG, "_build", s.replace(".cu", ".o")) for s in _build.SOURCES]
+    out = str(tmp_path_factory.mktemp("fake") / "libuniprefill_fake.so")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc())))
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", os.path.join(cuda, "include"),
+                        "-o", out, os.path.join(HERE, "fake_cudart.cpp")] + objects, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    m = ctypes.CDLL(out)
+    for name, (res, args) in up._SIGNATURES.items():
+        getattr(m, name).restype, getattr(m, name).argtypes = res, args
+    m.fake_launch_name.restype = ctypes.c_char_p
+    return m
+
+
+def _decode(lib, Hq=32, Hkv=8, dk=128, e4m3=False, R=1, max_blocks=256, B=16):
+    import long_context_prefill_varlen_gb300 as up
+    cache = up._KvCache(A, A, A, A, 8, Hkv * B * dk, B * dk, dk, Hkv, B, dk, up.KV_E4M3 if e4m3 else up.KV_BF16)
+    return lib.up_paged_decode(A, Hq * dk, ctypes.byref(cache), A, A, R, max_blocks, Hq, 0.1, 0, A, None, A, 1 << 50, A, None)
+
+
+def _launched(lib):
+    return [(lib.fake_launch_name(i).decode(), lib.fake_launch_cluster(i)) for i in range(lib.fake_launches())]
+
+
+SHAPES = [(Hq, dk, e4m3) for Hq in (8, 16) for dk in (64, 128, 256) for e4m3 in (False, True)]
+
+
+@pytest.mark.parametrize("R", [1, 300], ids=["one_launch", "two_launches"])
+@pytest.mark.parametrize("Hq,dk,e4m3", SHAPES)
+def test_decode_sets_its_kernels_up_on_every_device(lib, Hq, dk, e4m3, R):
+    for device in (0, fresh_device()):
+        for _ in range(2):
+            lib.fake_reset(device, 16)
+            assert _decode(lib, Hq, 1, dk, e4m3, R) == 0, device
+            launched = _launched(lib)
+            assert len(launched) == (1 if R == 1 else 2) and "split_kernel" in launched[0][0]
+
+
+def test_a_set_up_that_failed_is_tried_again(lib):
+    device = fresh_device()
+    lib.fake_reset(device, 16)
+    lib.fake_fail(1, 0)
+    assert _decode(lib) != 0 and lib.fake_launches() == 0
+    lib.fake_reset(device, 16)
+    assert _decode(lib) == 0 and lib.fake_launches() == 1
