@@ -32,7 +32,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "up_internal.cuh"
 
@@ -1754,10 +1753,9 @@ static bool make_map(CUtensorMap* m, const void* ptr, int64_t T, int heads, int 
 template <int PASS, int NC>
 static cudaError_t launch_pass(const CUtensorMap& q, const CUtensorMap& k, const Params& P, int grid,
                                cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(score_pass_kernel<PASS, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    static DeviceSet done{0};
+    const cudaError_t attr = once_per_device(done, [] {
+        return cudaFuncSetAttribute(score_pass_kernel<PASS, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemBytes);
     });
     if (attr != cudaSuccess) return attr;
@@ -1791,10 +1789,9 @@ static cudaError_t launch_one(const CUtensorMap& q, const CUtensorMap& k, const 
                               int64_t merge_rows, int64_t req_tiles, cudaStream_t st, bool plan_inside = false) {
     cudaError_t e;
     if (plan_inside) {
-        static std::once_flag once;
-        static cudaError_t attr = cudaSuccess;
-        std::call_once(once, [] {
-            attr = cudaFuncSetAttribute(score_pass_kernel<3, NC, true>,
+        static DeviceSet done{0};
+        const cudaError_t attr = once_per_device(done, [] {
+            return cudaFuncSetAttribute(score_pass_kernel<3, NC, true>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         });
         if (attr != cudaSuccess) return attr;

@@ -63,3 +63,15 @@ def test_a_set_up_that_failed_is_tried_again(lib):
     assert _decode(lib) != 0 and lib.fake_launches() == 0
     lib.fake_reset(device, 16)
     assert _decode(lib) == 0 and lib.fake_launches() == 1
+
+
+@pytest.mark.parametrize("tokens", [None, A], ids=["one_pass", "two_pass"])
+@pytest.mark.parametrize("R", [1, 5000])
+@pytest.mark.parametrize("Hq,Hkv,dk", [(8, 2, 64), (8, 2, 128), (4, 2, 256)])
+def test_the_score_sets_its_kernels_up_on_every_device(lib, Hq, Hkv, dk, R, tokens):
+    T, G, n = 10000, 64, 128
+    nb = lib.up_max_blocks(R, T, G)
+    for device in (0, fresh_device()):
+        lib.fake_reset(device, 16)
+        assert lib.up_score_blocks(A, A, A, R, T, Hq, Hkv, dk, G, n, 0.1, A, nb, A, tokens, A, 1 << 50, A, None) == 0, device
+        assert any("score_pass_kernel" in name for name, _ in _launched(lib))
