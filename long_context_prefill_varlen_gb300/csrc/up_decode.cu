@@ -1318,7 +1318,7 @@ static bool make_maps(CUtensorMap* km, CUtensorMap* vm, Args* a, int dk, bool e4
     return encode(km, c.k, dims, strides, box) && encode(vm, c.v, dims, strides, box);
 }
 
-// the cluster that holds a row's chunks, 0 where they do not all run at once
+// the cluster that would hold a row's chunks, 0 where they do not all run at once
 template <int DK, bool E4M3, int HT>
 static int team_of(const Args& a) {
     int team = 1;
@@ -1341,30 +1341,61 @@ static cudaError_t prepare_split() {
     });
 }
 
-template <int DK, bool E4M3, int HT>
-static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, int team, cudaStream_t st) {
-    constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
-    if (team == 0) {
-        const cudaError_t e = prepare_split<DK, E4M3, HT, false>();
-        if (e != cudaSuccess) return e;
-        return launch_pdl(split_kernel<DK, E4M3, HT, false>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
-    }
-    const cudaError_t e = prepare_split<DK, E4M3, HT, true>();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(team, a.c.Hkv * a.head_tiles, a.R);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
+// a launch in clusters of `team` CTAs
+struct TeamLaunch {
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = team;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, split_kernel<DK, E4M3, HT, true>, k, v, a);
+    TeamLaunch(int team, const Args& a, int smem, cudaStream_t st) : cfg{} {
+        cfg.gridDim = dim3(team, a.c.Hkv * a.head_tiles, a.R);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = team;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+    TeamLaunch(const TeamLaunch&) = delete;
+};
+
+// Whether the current device has room for a cluster of `team` CTAs (a partition with small processing clusters may not
+// have it for 16): asked once on each device and for each size.
+template <int DK, bool E4M3, int HT>
+static bool placed(int team, const Args& a) {
+    static std::atomic<uint64_t> yes[5], no[5];        // bit d: device d; sizes 1, 2, 4, 8, 16
+    int dev = 0, i = 0;
+    while ((1 << i) < team) ++i;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if (yes[i].load(std::memory_order_relaxed) & bit) return true;
+    if (no[i].load(std::memory_order_relaxed) & bit) return false;
+    const TeamLaunch l(team, a, Sizes<DK, E4M3, HT>::kSmem, nullptr);
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, split_kernel<DK, E4M3, HT, true>, &l.cfg);
+    if (e != cudaSuccess) cudaGetLastError();          // an answer, too: the next call's check must not find it
+    const bool fits = e == cudaSuccess && n > 0;
+    (fits ? yes : no)[i].fetch_or(bit, std::memory_order_relaxed);
+    return fits;
+}
+
+template <int DK, bool E4M3, int HT>
+static cudaError_t launch_split(const CUtensorMap& k, const CUtensorMap& v, const Args& a, int* team, cudaStream_t st) {
+    constexpr int smem = Sizes<DK, E4M3, HT>::kSmem;
+    if (*team != 0) {
+        const cudaError_t e = prepare_split<DK, E4M3, HT, true>();
+        if (e != cudaSuccess) return e;
+        if (placed<DK, E4M3, HT>(*team, a)) {
+            const TeamLaunch l(*team, a, smem, st);
+            return cudaLaunchKernelEx(&l.cfg, split_kernel<DK, E4M3, HT, true>, k, v, a);
+        }
+        *team = 0;                                     // the same bits by two launches
+    }
+    const cudaError_t e = prepare_split<DK, E4M3, HT, false>();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(split_kernel<DK, E4M3, HT, false>, dim3(Shape<DK, E4M3, HT>::kCtas * num_sms()), dim3(kThreads), smem, st, k, v, a);
 }
 
 // The join asks for the split's division of an SM's memory (nearly all of it shared): with the default one an SM
@@ -1381,8 +1412,8 @@ static cudaError_t launch_join(const Args& a, int64_t ctas, cudaStream_t st) {
 
 template <int DK, bool E4M3, int HT>
 static cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const Args& a, cudaStream_t st) {
-    const int team = team_of<DK, E4M3, HT>(a);
-    const cudaError_t e = launch_split<DK, E4M3, HT>(k, v, a, team, st);
+    int team = team_of<DK, E4M3, HT>(a);
+    const cudaError_t e = launch_split<DK, E4M3, HT>(k, v, a, &team, st);
     count_launch(team ? 1 : 2);
     if (e != cudaSuccess || team) return e;
     const int64_t rows = (int64_t)a.Hq * a.R;

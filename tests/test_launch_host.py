@@ -75,3 +75,20 @@ def test_the_score_sets_its_kernels_up_on_every_device(lib, Hq, Hkv, dk, R, toke
         lib.fake_reset(device, 16)
         assert lib.up_score_blocks(A, A, A, R, T, Hq, Hkv, dk, G, n, 0.1, A, nb, A, tokens, A, 1 << 50, A, None) == 0, device
         assert any("score_pass_kernel" in name for name, _ in _launched(lib))
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("largest", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("Hq,Hkv,dk,max_blocks,wants", [(32, 8, 128, 16, 1), (32, 8, 128, 32, 2), (32, 8, 128, 64, 4), (32, 8, 128, 128, 8),
+                                                        (32, 8, 128, 256, 16), (4, 1, 256, 256, 16)])
+def test_a_cluster_that_the_device_cannot_place_gives_two_launches(lib, Hq, Hkv, dk, max_blocks, wants, largest, e4m3):
+    """(a partition of a GPU may have room for smaller clusters only)"""
+    device = fresh_device()
+    for _ in range(2):
+        lib.fake_reset(device, largest)
+        assert _decode(lib, Hq, Hkv, dk, e4m3, 1, max_blocks) == 0
+        launched = _launched(lib)
+        assert [c for _, c in launched] == ([wants] if wants <= largest else [1, 1])
+        assert "split_kernel" in launched[0][0] and (wants <= largest or "join_kernel" in launched[1][0])
+    lib.fake_reset(device, largest)
+    assert _decode(lib, Hq, Hkv, dk, e4m3, 1, 16) == 0 and lib.fake_launches() == 1      # no error is left behind
