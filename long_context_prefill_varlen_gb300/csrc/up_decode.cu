@@ -1481,6 +1481,6 @@ extern "C" up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const 
     const cudaError_t e = cache->dk == 64    ? launch_dk<64>(km, vm, a, e4m3, st)
                           : cache->dk == 128 ? launch_dk<128>(km, vm, a, e4m3, st)
                                              : launch_dk<256>(km, vm, a, e4m3, st);
-    if (e != cudaSuccess) return UP_ERR_CUDA;
+    if (e != cudaSuccess) return failed_launch();
     return check_launch();
 }

@@ -18,6 +18,7 @@ namespace up {
 void count_launch(int n = 1);          // launch accounting behind up_kernel_launches()
 int num_sms();                         // SM count of the current device (cached per device)
 up_status check_launch();              // UP_ERR_CUDA if the last launch failed
+up_status failed_launch();             // UP_ERR_CUDA of a call that has seen its own error, which the next one's check must not find
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

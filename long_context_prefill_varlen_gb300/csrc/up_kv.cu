@@ -312,7 +312,7 @@ static up_status launch(const Args& a, bool write, int dk, int format, cudaStrea
     const bool e4m3 = format == UP_KV_E4M3;
     const cudaError_t e = dk == 64 ? launch_dk<64>(a, write, e4m3, st) : dk == 128 ? launch_dk<128>(a, write, e4m3, st)
                                                                                     : launch_dk<256>(a, write, e4m3, st);
-    if (e != cudaSuccess) return UP_ERR_CUDA;
+    if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();
 }

@@ -42,6 +42,10 @@ EncodeTiledFn encode_tiled_fn() {
     return fn;
 }
 
+up_status failed_launch() {
+    cudaGetLastError();
+    return UP_ERR_CUDA;
+}
 up_status check_launch() { return cudaGetLastError() == cudaSuccess ? UP_OK : UP_ERR_CUDA; }
 
 namespace meta {

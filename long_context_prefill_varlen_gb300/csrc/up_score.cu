@@ -1910,7 +1910,7 @@ extern "C" up_status up_score_blocks(const uint16_t* Q, const uint16_t* K, const
             case 2: e = launch_one<2>(tq, tk, P, grid, merge_rows, req_tiles, st, true); break;
             default: e = launch_one<4>(tq, tk, P, grid, merge_rows, req_tiles, st, true); break;
         }
-        return e == cudaSuccess ? UP_OK : UP_ERR_CUDA;
+        return e == cudaSuccess ? UP_OK : failed_launch();
     }
     // the item list by a grid of CTAs (one while the requests' offsets do not fit their shared memory)
     const int pgrid = R <= kPlanSmemReqs
@@ -1918,7 +1918,7 @@ extern "C" up_status up_score_blocks(const uint16_t* Q, const uint16_t* K, const
                           : 1;
     cudaError_t le = launch_pdl(plan_kernel, dim3(pgrid), dim3(kPlanThreads), 0, st, P);
     count_launch();
-    if (le != cudaSuccess) return UP_ERR_CUDA;
+    if (le != cudaSuccess) return failed_launch();
     if (T > 0) {
         CUtensorMap tq, tk;
         if (!make_map(&tq, Q, T, Hq, dk, g.box_rows) || !make_map(&tk, K, T, Hkv, dk, kTileKeys)) return UP_ERR_CUDA;
@@ -1933,17 +1933,17 @@ extern "C" up_status up_score_blocks(const uint16_t* Q, const uint16_t* K, const
                 case 2: e = launch_one<2>(tq, tk, P, grid, merge_rows, req_tiles, st); break;
                 default: e = launch_one<4>(tq, tk, P, grid, merge_rows, req_tiles, st); break;
             }
-            return e == cudaSuccess ? UP_OK : UP_ERR_CUDA;
+            return e == cudaSuccess ? UP_OK : failed_launch();
         }
         switch (g.nc) {
             case 1: e = launch_both<1>(tq, tk, P, grid, merge_rows, st); break;
             case 2: e = launch_both<2>(tq, tk, P, grid, merge_rows, st); break;
             default: e = launch_both<4>(tq, tk, P, grid, merge_rows, st); break;
         }
-        if (e != cudaSuccess) return UP_ERR_CUDA;
+        if (e != cudaSuccess) return failed_launch();
     }
     const int fgrid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4 * num_sms(), cdiv(std::max<int64_t>(nb_cap, T), 256))));
     le = launch_pdl(finalize_kernel, dim3(fgrid), dim3(256), 0, st, P);
     count_launch();
-    return le == cudaSuccess ? UP_OK : UP_ERR_CUDA;
+    return le == cudaSuccess ? UP_OK : failed_launch();
 }

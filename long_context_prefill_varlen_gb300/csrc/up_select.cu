@@ -494,7 +494,7 @@ extern "C" up_status up_select_topp(const float* block_scores, const int32_t* cu
     if (dev < 64 && !attr_done[dev]) {
         if (cudaFuncSetAttribute(select::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  select::kSmemBytes) != cudaSuccess)
-            return UP_ERR_CUDA;
+            return failed_launch();
         attr_done[dev] = 1;
     }
     launch_pdl(select::select_kernel, dim3(R), dim3(select::kThreads), select::kSmemBytes,

@@ -11,8 +11,9 @@ from long_context_prefill_varlen_gb300 import _build
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 A = 0x1000                     # never dereferenced
-# the stand-in's second GPU and further ones: a test takes one that no test had before
-fresh_device = itertools.count(1).__next__
+# the stand-in's devices (the library tells 64 apart): 0, 1, one for each size of cluster, then one that no test had before
+CLUSTERS = {1: 2, 2: 3, 4: 4, 8: 5, 16: 6}
+fresh_device = itertools.count(7).__next__
 
 
 @pytest.fixture(scope="module")
@@ -48,7 +49,7 @@ SHAPES = [(Hq, dk, e4m3) for Hq in (8, 16) for dk in (64, 128, 256) for e4m3 in 
 @pytest.mark.parametrize("R", [1, 300], ids=["one_launch", "two_launches"])
 @pytest.mark.parametrize("Hq,dk,e4m3", SHAPES)
 def test_decode_sets_its_kernels_up_on_every_device(lib, Hq, dk, e4m3, R):
-    for device in (0, fresh_device()):
+    for device in (0, 1):
         for _ in range(2):
             lib.fake_reset(device, 16)
             assert _decode(lib, Hq, 1, dk, e4m3, R) == 0, device
@@ -71,7 +72,7 @@ def test_a_set_up_that_failed_is_tried_again(lib):
 def test_the_score_sets_its_kernels_up_on_every_device(lib, Hq, Hkv, dk, R, tokens):
     T, G, n = 10000, 64, 128
     nb = lib.up_max_blocks(R, T, G)
-    for device in (0, fresh_device()):
+    for device in (0, 1):
         lib.fake_reset(device, 16)
         assert lib.up_score_blocks(A, A, A, R, T, Hq, Hkv, dk, G, n, 0.1, A, nb, A, tokens, A, 1 << 50, A, None) == 0, device
         assert any("score_pass_kernel" in name for name, _ in _launched(lib))
@@ -83,7 +84,7 @@ def test_the_score_sets_its_kernels_up_on_every_device(lib, Hq, Hkv, dk, R, toke
                                                         (32, 8, 128, 256, 16), (4, 1, 256, 256, 16)])
 def test_a_cluster_that_the_device_cannot_place_gives_two_launches(lib, Hq, Hkv, dk, max_blocks, wants, largest, e4m3):
     """(a partition of a GPU may have room for smaller clusters only)"""
-    device = fresh_device()
+    device = CLUSTERS[largest]
     for _ in range(2):
         lib.fake_reset(device, largest)
         assert _decode(lib, Hq, Hkv, dk, e4m3, 1, max_blocks) == 0
@@ -92,3 +93,32 @@ def test_a_cluster_that_the_device_cannot_place_gives_two_launches(lib, Hq, Hkv,
         assert "split_kernel" in launched[0][0] and (wants <= largest or "join_kernel" in launched[1][0])
     lib.fake_reset(device, largest)
     assert _decode(lib, Hq, Hkv, dk, e4m3, 1, 16) == 0 and lib.fake_launches() == 1      # no error is left behind
+
+
+@pytest.mark.parametrize("R", [1, 300], ids=["one_launch", "two_launches"])
+@pytest.mark.parametrize("attributes,launches", [(1, 0), (0, 1)], ids=["attribute", "launch"])
+def test_an_error_of_a_decode_call_is_that_calls_alone(lib, attributes, launches, R):
+    device = fresh_device()
+    lib.fake_reset(device, 16)
+    lib.fake_fail(attributes, launches)
+    assert _decode(lib, R=R) == 4                                # UP_ERR_CUDA
+    assert _decode(lib, R=R) == 0
+
+
+def test_an_error_of_a_cache_call_is_that_calls_alone(lib):
+    import long_context_prefill_varlen_gb300 as up
+    cache = ctypes.byref(up._KvCache(A, A, A, A, 8, 2 * 16 * 128, 16 * 128, 128, 2, 16, 128, up.KV_E4M3))
+    for call in (lambda: lib.up_kv_write(cache, A, 256, A, 256, A, 4, None, A, None), lambda: lib.up_kv_read(cache, A, 4, None, A, A, A, None)):
+        lib.fake_reset(0, 16)
+        lib.fake_fail(0, 1)
+        assert call() == 4 and call() == 0
+
+
+@pytest.mark.parametrize("attributes,launches", [(1, 0), (0, 1)], ids=["attribute", "launch"])
+def test_an_error_of_a_drop_step_call_is_that_calls_alone(lib, attributes, launches):
+    lib.fake_reset(fresh_device(), 16)
+    for call in (lambda: lib.up_score_blocks(A, A, A, 1, 1000, 8, 2, 128, 64, 128, 0.1, A, 100, A, None, A, 1 << 50, A, None),
+                 lambda: lib.up_select_topp(A, A, A, 1, 1000, 100, 64, 128, 128, 0.9, A, A, A, None, 0, A, None)):
+        lib.fake_fail(attributes, launches)
+        assert call() == 4
+        assert lib.up_seqused(A, A, 2, 3, 1, A, A, A, None) == 0 and call() == 0
