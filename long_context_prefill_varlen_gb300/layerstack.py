@@ -132,7 +132,8 @@ class StackCache:
         self.ws = None
 
     def start(self, cu_seqlens):
-        """Forget what was cached; the coming prefill's requests have these lengths."""
+        """Forget what was cached, an error that it ran into included; the coming prefill's requests have these lengths."""
+        self.status.zero_()
         self.drop_layer.zero_()
         self.orig_len.copy_(cu_seqlens.diff())
         self.kv_len.copy_(self.orig_len)
@@ -312,7 +313,8 @@ class RandomLlamaStack:
     def decode(self, hidden, positions, cache):
         """One new token per request through all layers: hidden [R, d] bf16, positions [R] int64 (rotary: the
         tokens the request has had so far, dropped ones included).  Each layer appends the token's key and value to
-        its part of the cache and attends over the tokens it holds.  Returns the token's output [R, d]."""
+        its part of the cache and attends over the tokens it holds.  Returns the token's output [R, d].  The host does not
+        wait: cache.check() tells of a request that has outgrown the cache, whose output is then none."""
         g = self.g
         R = hidden.shape[0]
         cache.kv_len.add_(1)
