@@ -269,7 +269,8 @@ class RandomLlamaStack:
         count and (keep_scored) the rotated q and k it was scored on, and the stream x and positions it
         compacted.  Each drop synchronises the host
         once, to learn the compacted stream's length.  With a StackCache, every layer's keys and values are
-        written to it as the layer's stream holds them, and the drops to its history, for decode()."""
+        written to it as the layer's stream holds them, and the drops to its history, for decode(); the host waits for
+        the end and a request that is longer than the cache raises."""
         upto = self.L if upto is None else upto
         drops = list(drops)
         h = hidden.clone()
@@ -308,6 +309,8 @@ class RandomLlamaStack:
             h = block_in
         for _, step in stack_of_blocks:
             step.check()
+        if cache is not None:
+            cache.check()                                  # a request longer than the cache has lost its last rows
         return h, info
 
     def decode(self, hidden, positions, cache):

@@ -33,3 +33,11 @@ def test_a_cache_that_ran_full_takes_the_next_prefill(e4m3):
         outs.append(stack.decode(token, torch.tensor([20, 30], device="cuda"), c))
         c.check()
     assert torch.equal(outs[0], outs[1])
+
+
+def test_a_prefill_longer_than_its_cache_raises():
+    stack = ls.RandomLlamaStack(L, GEOM, seed=3, device="cuda", init_device="cpu")
+    cache = ls.StackCache(L, 2, GEOM.Hkv, GEOM.dk, 32)
+    with pytest.raises(RuntimeError):
+        _prefill(stack, cache, (40, 7))
+    _prefill(stack, cache, (32, 7))
