@@ -272,6 +272,8 @@ class RandomLlamaStack:
         written to it as the layer's stream holds them, and the drops to its history, for decode(); the host waits for
         the end and a request that is longer than the cache raises."""
         upto = self.L if upto is None else upto
+        if cache is not None and upto != self.L:
+            raise ValueError("upto: a prefill with a cache runs all layers, as decode() does")
         drops = list(drops)
         h = hidden.clone()
         pos, cu, T = positions, cu_seqlens, hidden.shape[0]
