@@ -131,8 +131,14 @@ class StackCache:
         self.one_each = torch.arange(R + 1, **i32)
         self.ws = None
 
+    def fit(self, L, R):
+        """Refuse a stack or a batch of another size: the cache's buffers, and the kernels' writes, are L and R long."""
+        if (L, R) != (self.L, self.R):
+            raise ValueError(f"a cache of {self.L} layers and {self.R} requests for {L} layers and {R} requests")
+
     def start(self, cu_seqlens):
         """Forget what was cached, an error that it ran into included; the coming prefill's requests have these lengths."""
+        self.fit(self.L, cu_seqlens.numel() - 1)
         self.status.zero_()
         self.drop_layer.zero_()
         self.orig_len.copy_(cu_seqlens.diff())
@@ -274,6 +280,8 @@ class RandomLlamaStack:
         upto = self.L if upto is None else upto
         if cache is not None and upto != self.L:
             raise ValueError("upto: a prefill with a cache runs all layers, as decode() does")
+        if cache is not None:
+            cache.fit(self.L, cu_seqlens.numel() - 1)
         drops = list(drops)
         h = hidden.clone()
         pos, cu, T = positions, cu_seqlens, hidden.shape[0]
@@ -322,6 +330,9 @@ class RandomLlamaStack:
         wait: cache.check() tells of a request that has outgrown the cache, whose output is then none."""
         g = self.g
         R = hidden.shape[0]
+        cache.fit(self.L, R)
+        if positions.numel() != R:
+            raise ValueError(f"{positions.numel()} positions for {R} tokens")
         cache.kv_len.add_(1)
         h = hidden
         for layer in range(self.L):

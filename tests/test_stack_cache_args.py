@@ -30,3 +30,32 @@ def test_a_prefill_of_the_first_layers_alone(stack):
     for upto in (0, 1, L - 1):
         with pytest.raises(ValueError, match="upto"):
             _forward(stack, _cache(), upto=upto)
+
+
+def _decode(stack, cache, rows, positions=None):
+    return stack.decode(torch.zeros(rows, GEOM.d, dtype=torch.bfloat16), torch.zeros(positions or rows, dtype=torch.int64), cache)
+
+
+@pytest.mark.parametrize("lengths", [(5,), (5, 0, 1)])
+def test_a_batch_or_a_stack_of_another_size(stack, lengths):
+    """one request's lengths would stand for every request's, and a step's slots run past their buffer"""
+    cu = torch.tensor((0,) + lengths).cumsum(0).to(torch.int32)
+    with pytest.raises(ValueError, match="requests"):
+        _cache().start(cu)
+    with pytest.raises(ValueError, match="requests"):
+        _forward(stack, _cache(), lengths)
+    with pytest.raises(ValueError, match="requests"):
+        _decode(stack, _cache(), len(lengths))
+    with pytest.raises(ValueError, match="layers"):
+        _forward(stack, _cache(L=L + 1))
+    with pytest.raises(ValueError, match="layers"):
+        _decode(stack, _cache(L=L - 1), R)
+    with pytest.raises(ValueError, match="positions"):
+        _decode(stack, _cache(), R, R + 1)
+
+
+def test_a_refused_step_leaves_the_cache_as_it_was(stack):
+    cache = _cache()
+    with pytest.raises(ValueError):
+        _decode(stack, cache, R + 1)
+    assert (cache.kv_len == 0).all()
