@@ -18,19 +18,22 @@
 //    ring runs across items, so a new item's first tiles are there when the last one's sums are written;
 //  * four consumer warps take 16 keys of a tile each and need no barrier between tiles: each has its own
 //    running maximum and sums, joined through the last stage when the item ends;
-//  * a call so short that every chunk can have a CTA at once is one launch: the chunks of a row are a cluster and
-//    join through its shared memory (one 4K request: 9.9 -> 8.4 us, and one launch less for the host).
+//  * a call in which every chunk that its tables have room for can have a CTA at once is one launch: the chunks of a
+//    row are a cluster and join through its shared memory (one 4K request in a table of 4K: 9.9 -> 8.4 us, and one launch
+//    less for the host).  The host knows no lengths, so the tables' width decides, not the requests' lengths.
 // The products are m16n8k16 with the long side of each in the 16 rows: scores = keys x queries (16 keys, 8
 // heads), outputs = values transposed x weights transposed (16 columns, 8 heads), so that a group of up to 8
 // heads, and a second tile of 8 above that, leaves little of them empty.  The scores' own layout, transposed
-// in the registers, is the weights' operand.  A matrix unit with larger tiles has nothing to win here: 8 or
-// 16 queries are all there is to multiply with, and the products fill 12 to 16% of the tensor pipe.
+// in the registers, is the weights' operand.  With up to 8 heads a group the copies bound the call and the products fill
+// 12 to 16% of the tensor pipe, so a larger matrix unit has nothing to win.  Beyond 8 heads issue slots and not copies
+// bound it (44% of what HBM would allow with 32 heads on one of 128 in bf16, 21% in e4m3): there keys and value columns
+// as the 64 or 128 rows of a tcgen05 product, the heads its columns, could win; not built.
 //
 // Measured (one GB300, 6.69 TB/s measured copy): 64 requests of 32K, 8 heads of 256 in bf16, 2.44 ms, 7.0 TB/s;
 // 16 of 4K-128K, 8 heads of 128 in bf16, 426 us, 6.6 TB/s; 4 of 128K, 2 heads of 256 in e4m3, 97 us, 5.6 TB/s;
 // 64 of 0-8K, 8 heads of 128 in e4m3, 109 us, 5.3 TB/s.  With e4m3 half the bytes come with the same work per
-// number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K takes 8.4 us, a chain of
-// latencies (its length, its pages, the copies, four tiles, the join); its bytes would take 2.5 us.
+// number: there the starts and ends of items and the join weigh 5 to 20%.  One request of 4K in a table of 4K takes
+// 8.8 us, a chain of latencies (its length, its pages, the copies, four tiles, the join); its bytes would take 2.5 us.
 #include <stdint.h>
 
 #include <algorithm>
@@ -1059,8 +1062,8 @@ __device__ void join_team(const Args& a, Control<LDQ, HT, NS>& sh) {
     }
 }
 
-// TEAM: a call short enough for every chunk to have a CTA at once (one request of up to 8K tokens on 8 key heads);
-// the chunks of a row are a cluster and join there, without a second launch.
+// TEAM: a call whose tables are narrow enough for every chunk to have a CTA at once (one request in a table of up to 8K
+// tokens on 8 key heads); the chunks of a row are a cluster and join there, without a second launch.
 template <int DK, bool E4M3, int HT, bool TEAM>
 __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, HT>::kCtas))
 split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
