@@ -18,6 +18,14 @@
  *   up_kv_read       cache rows back to a packed bf16 stream (the K of up_score_blocks)
  *   up_paged_decode  attention of one new token per request over its pages, with up_seqused's lengths
  *
+ * Rotary positions of the stream's queries and keys:
+ *   up_rope          turns them by their tokens' positions, or a gradient back
+ *
+ * Taking tokens out of the cache while decoding goes on, for every key head by itself:
+ *   up_kv_mass       adds up the attention weight that every cached row has had
+ *   up_kv_evict      chooses the rows that stay and which of them change places
+ *   up_kv_move       moves those rows, so that the ones that stay are the first of their request again
+ *
  * Conventions shared by every call:
  *  - All array pointers are DEVICE pointers owned by the caller; the library
  *    never allocates, frees or keeps a pointer after a call returns.
@@ -74,6 +82,8 @@ typedef enum {
 #define UP_DEV_BAD_SLOT         8   /* a cache slot outside [-1, num_blocks * B)                  */
 #define UP_DEV_BAD_PAGE         9   /* a block-table entry in use lies outside [0, num_blocks)    */
 #define UP_DEV_BAD_LENGTH      10   /* seqused outside [0, max_blocks * B]                        */
+#define UP_DEV_BAD_BUDGET      11   /* a budget below 0                                           */
+#define UP_DEV_TOO_MANY_MOVES  12   /* a request may have more moves than the list holds          */
 
 #define UP_MAX_BLOCKS_PER_REQUEST 8192   /* up to this many blocks up_select_topp sorts a request in
                                             shared memory; longer requests need its workspace */
@@ -315,6 +325,106 @@ up_status up_paged_decode(const uint16_t* q, int64_t q_stride, const up_kv_cache
                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------------- */
+/* rotary positions                                                                             */
+
+#define UP_ROPE_HALVES 0    /* number j of a head's first rot turns with number j + rot/2            */
+#define UP_ROPE_PAIRS  1    /* number 2j with number 2j + 1                                          */
+
+#define UP_ROPE_PLAIN  0    /* f_j = theta^(-2j/rot) radians per position                            */
+#define UP_ROPE_LINEAR 1    /* f_j / factor                                                          */
+#define UP_ROPE_BANDS  2    /* by the turns u_j = f_j original_len / (2 pi) that a pair makes over the trained
+                               length: f_j where u_j >= high, f_j / factor where u_j <= low, and
+                               (1 - x) f_j / factor + x f_j, x = (u_j - low) / (high - low), between   */
+#define UP_ROPE_RAMP   3    /* by the pair's index: f_j up to pair a, f_j / factor from pair b on, and
+                               (1 - x) f_j + x f_j / factor, x = (j - a) / (b - a), between; with
+                               c(u) = rot ln(original_len / (2 pi u)) / (2 ln theta), the pair that makes u turns,
+                               a = max(floor(c(high)), 0) and b = min(ceil(c(low)), rot - 1) (b = a + 1/1000 if
+                               they meet); rotated numbers are multiplied by 1 + ln(factor) / 10       */
+
+#define UP_ROPE_MAX_PAIRS 128
+
+/* How the heads of a model turn; made once by up_rope_plan, a plain host value that the caller keeps. */
+typedef struct {
+    uint64_t turns[UP_ROPE_MAX_PAIRS];   /* of pair j per position, in units of 2^-64 turn */
+    float gain;                          /* what rotated numbers are multiplied by         */
+    int32_t rot, layout;
+} up_rope_table;
+
+/* Fills a table (host only, no CUDA call).  rot: numbers of a head that turn, a multiple of 16 up to 256; theta in
+ * (1, 1e300]; factor >= 1; scaling other than UP_ROPE_PLAIN ignores no argument that its formula above names:
+ * original_len > 0, 0 < low < high.  gain > 0 takes the place of the scaling's own; 0 leaves that. */
+up_status up_rope_plan(int rot, double theta, int layout, int scaling, double factor, double original_len, double low,
+                       double high, double gain, up_rope_table* plan);
+
+/* Rotary positions: for token t, pair j of every head, a and b the pair's numbers and x = positions[t] * f_j:
+ *   a' = gain * (a cos x - b sin x),   b' = gain * (b cos x + a sin x);
+ * transpose != 0 turns by -x, which is the gradient of the above (and its inverse, times gain^2).  The head's
+ * numbers past rot are copied.
+ * q [T, Hq, dk] -> q_out, k [T, Hkv, dk] -> k_out (bf16): token t's heads lie packed at q + t * q_stride (strides in
+ * elements, multiples of 8, >= heads * dk when T > 1), 16-byte aligned.  q_out may be q, with the same stride; apart from
+ * that no output overlaps an input or the other output.  Either pair may be NULL.
+ * positions: int64 [T], any value.  dk in {64, 128, 256}, plan->rot <= dk.
+ * Tokens t < *num_tokens (or < T if num_tokens is NULL; a count outside [0, T] sets UP_DEV_BAD_TOKEN_COUNT and nothing is
+ * written); the rows of the others are left alone.
+ * Arithmetic: angles in 64-bit fixed point modulo a turn (errors of a few 2^-53 of the angle and of 2^-32 turn, however far the
+ * position), cosine, sine and the products in fp32, one rounding to bf16. */
+up_status up_rope(const up_rope_table* plan, const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
+                  int Hq, const uint16_t* k, int64_t k_stride, uint16_t* k_out, int64_t k_out_stride, int Hkv, int dk,
+                  const int64_t* positions, int64_t T, const int32_t* num_tokens, int transpose, int32_t* dev_status,
+                  void* stream);
+
+/* ------------------------------------------------------------------------------------------- */
+/* eviction                                                                                     */
+
+/* A cache's rows have two records each, at [page, head, token of the page] (arrays [num_blocks, Hkv, B], 4-byte aligned):
+ *   mass  fp32, the attention weight that the row has had, added up over decode steps and the key head's query heads
+ *   born  int32, the row's number in its layer's stream: 0 for the request's first token there, whatever moved since
+ * A page belongs to one request while these calls work on it: requests that share a page would write each other's records and rows. */
+
+/* One decode step's weights, after up_paged_decode with the same q, cache, block_table, seqused and sm_scale, window 0:
+ *   mass_out = decay * mass + sum_{h of the key head} exp(q[r, h] . K_i * sm_scale - lse[r, h])   for i in [0, seqused[r]).
+ * Rows at positions i >= counted[r] (int32 [R], optional: NULL means that every row has been counted before) are new: they
+ * start from 0, whatever mass holds, and get born = total[r] - seqused[r] + i, total[r] (int32 [R], optional; NULL means
+ * seqused) being the tokens that the layer's stream has had.  A head with lse = -inf adds nothing.  mass_out may be mass; apart
+ * from that they do not overlap.  Records at other positions are left alone.
+ * decay in [0, 1].  A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a row whose table
+ * entry lies outside [0, num_blocks) sets UP_DEV_BAD_PAGE and has no record.
+ * Arithmetic: as up_paged_decode's scores; weights and sums in fp32, the heads' in a fixed order. */
+up_status up_kv_mass(const uint16_t* q, int64_t q_stride, const up_kv_cache* cache, const int32_t* block_table,
+                     const int32_t* seqused, const float* lse, int R, int max_blocks, int Hq, float sm_scale,
+                     const int32_t* counted, const int32_t* total, float decay, const float* mass, float* mass_out,
+                     int32_t* born, int32_t* dev_status, void* stream);
+
+/* Which rows stay: of every request and key head the k = min(budget[r], len) first, len = seqused[r], of the rows ranked
+ *   1. protected ones (born < sinks, or born >= total[r] - recent; total NULL means seqused) before the others,
+ *   2. by mass, larger first (NaN before every number, -0 equal to 0),
+ *   3. by position, lower first.
+ * Positions [0, k) hold the rows that stay once the ones at or beyond k have moved into the holes below it:
+ *   moves[(r * Hkv + h) * max_moves + i] = (position from, position to), both ascending in i < num_moves[r * Hkv + h];
+ *   new_len[r] = k.
+ * moves: int32 [R, Hkv, max_moves, 2] (entries past num_moves are left alone), 8-byte aligned; num_moves: int32 [R, Hkv];
+ * new_len, budget, seqused: int32 [R].  budget, seqused and total are not written and new_len must not be one of them.
+ * A request is left as it is (no moves, new_len = its length) where min(k, len - k) > max_moves
+ * (UP_DEV_TOO_MANY_MOVES), budget[r] < 0 (UP_DEV_BAD_BUDGET) or a table entry in use lies outside [0, num_blocks)
+ * (UP_DEV_BAD_PAGE; where all rows stay, or none, no entry is in use).  A seqused entry outside [0, max_blocks * B] sets
+ * UP_DEV_BAD_LENGTH and counts as 0.
+ * 1 <= B <= 2^20; max_blocks * B at most 2^30; R * Hkv at most 2^24 (UP_ERR_SHAPE otherwise). */
+up_status up_kv_evict(const float* mass, const int32_t* born, int64_t num_blocks, int Hkv, int B,
+                      const int32_t* block_table, const int32_t* seqused, const int32_t* budget, int R, int max_blocks,
+                      const int32_t* total, int sinks, int recent, int32_t* moves, int64_t max_moves,
+                      int32_t* num_moves, int32_t* new_len, int32_t* dev_status, void* stream);
+
+/* Moves rows of the cache: position moves[..., 0] of request r's key head h to position moves[..., 1], keys, values and
+ * scale bytes, and their records (mass and born, each optional).  moves and num_moves as up_kv_evict writes them; in any
+ * other list no position may be moved to twice, or be both moved from and moved to.
+ * A move from or to a position outside [0, max_blocks * B), or on a table entry outside [0, num_blocks), is skipped and sets
+ * UP_DEV_BAD_SLOT or UP_DEV_BAD_PAGE; a num_moves entry outside [0, max_moves] sets UP_DEV_TOO_MANY_MOVES and moves nothing of its head.
+ * R * Hkv at most 2^24, max_blocks * B at most 2^30 (UP_ERR_SHAPE otherwise). */
+up_status up_kv_move(const up_kv_cache* cache, const int32_t* block_table, int R, int max_blocks, const int32_t* moves,
+                     int64_t max_moves, const int32_t* num_moves, float* mass, int32_t* born, int32_t* dev_status,
+                     void* stream);
+
+/* ------------------------------------------------------------------------------------------- */
 /* status and introspection                                                                     */
 
 /* Synchronises `stream`, copies *dev_status to *host_out, returns UP_ERR_DEVICE if it is not 0. */
@@ -326,8 +436,8 @@ const char* up_status_string(int code, int device);
 /* Number of kernels this library has launched in this process (for launch accounting). */
 uint64_t up_kernel_launches(void);
 
-/* ABI version of this header: 2 (up_select_topp takes a workspace; the cache's entry points were added
- * without changing an older one). */
+/* ABI version of this header: 2 (up_select_topp takes a workspace; the entry points of the cache, of rotary positions and of
+ * eviction were added without changing an older one). */
 int up_abi_version(void);
 
 /* 1 in the bounds-checked build of the library (compiled with -DUP_DEBUG_BOUNDS, a development aid:

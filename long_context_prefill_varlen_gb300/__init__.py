@@ -60,7 +60,21 @@ _SIGNATURES.update({
                                _c_p, _sz, _c_p, _c_p]),
 })
 
+_SIGNATURES.update({
+    "up_rope_plan": (_i32, [_i32, _f64, _i32, _i32, _f64, _f64, _f64, _f64, _f64, _c_p]),
+    "up_rope": (_i32, [_c_p, _c_p, _i64, _c_p, _i64, _i32, _c_p, _i64, _c_p, _i64, _i32, _i32, _c_p, _i64, _c_p, _i32,
+                       _c_p, _c_p]),
+    "up_kv_mass": (_i32, [_c_p, _i64, _c_p, _c_p, _c_p, _c_p, _i32, _i32, _i32, _f32, _c_p, _c_p, _f32, _c_p, _c_p, _c_p,
+                          _c_p, _c_p]),
+    "up_kv_evict": (_i32, [_c_p, _c_p, _i64, _i32, _i32, _c_p, _c_p, _c_p, _i32, _i32, _c_p, _i32, _i32, _c_p, _i64, _c_p,
+                           _c_p, _c_p, _c_p]),
+    "up_kv_move": (_i32, [_c_p, _c_p, _i32, _i32, _c_p, _i64, _c_p, _c_p, _c_p, _c_p, _c_p]),
+})
+
 KV_BF16, KV_E4M3 = 0, 1
+ROPE_LAYOUTS = {"halves": 0, "pairs": 1}
+# the scalings of rotary frequencies, with the turns over the trained length between which they blend
+ROPE_SCALINGS = {"none": (0, 1.0, 2.0), "linear": (1, 1.0, 2.0), "bands": (2, 1.0, 4.0), "ramp": (3, 1.0, 32.0)}
 
 
 class _KvCache(ctypes.Structure):
@@ -68,6 +82,11 @@ class _KvCache(ctypes.Structure):
     _fields_ = [("k", _c_p), ("v", _c_p), ("k_scale", _c_p), ("v_scale", _c_p), ("num_blocks", _i64),
                 ("stride_block", _i64), ("stride_head", _i64), ("stride_token", _i64),
                 ("Hkv", ctypes.c_int32), ("B", ctypes.c_int32), ("dk", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class RopeTable(ctypes.Structure):
+    """up_rope_table: how the heads of a model turn (up_rope_plan)"""
+    _fields_ = [("turns", _u64 * 128), ("gain", _f32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32)]
 
 
 _BF16, _E4M3, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
@@ -316,6 +335,117 @@ def up_paged_decode(q, k_cache, v_cache, block_table, seqused, out, ws, dev_stat
                                           _stream(stream))
     if code:
         raise UpError(code, "up_paged_decode")
+
+
+# ------------------------------------------------------------------------------------------ rotary positions
+
+def up_rope_plan(rot, theta=10000.0, layout="halves", scaling="none", factor=1.0, original_len=0, low=None, high=None,
+                 gain=0.0):
+    """The RopeTable of heads whose first `rot` numbers turn, in the layout "halves" or "pairs", with frequencies as they
+    are ("none") or scaled: "linear", "bands" or "ramp" (up_rope_plan in include/uniprefill.h has the formulas; low and
+    high, in turns over original_len, are 1 and 4 for bands and 1 and 32 for ramp unless given)."""
+    kind, low0, high0 = ROPE_SCALINGS[scaling]
+    plan = RopeTable()
+    _check(load_library().up_rope_plan(rot, theta, ROPE_LAYOUTS[layout], kind, factor, original_len,
+                                       low0 if low is None else low, high0 if high is None else high, gain,
+                                       ctypes.byref(plan)), "up_rope_plan")
+    return plan
+
+
+def _here(*tensors):
+    """The device of a call's tensors, all on the current one: a launch goes to the current device's stream."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        assert t is None or t.device.index == device, "tensors on another device than the current one"
+
+
+def up_rope(plan, positions, dev_status, q=None, q_out=None, k=None, k_out=None, num_tokens=None, transpose=False,
+            stream=None):
+    """q [T, Hq, dk] -> q_out, k [T, Hkv, dk] -> k_out (either pair may be None), turned by positions [T] int64;
+    q_out may be q.  transpose: the gradient of that."""
+    T = positions.numel()
+    assert (q is None) == (q_out is None) and (k is None) == (k_out is None)
+    assert positions.dtype == _I64 and positions.is_contiguous()
+    assert num_tokens is None or num_tokens.dtype == _I32
+    _here(positions, dev_status, q, q_out, k, k_out, num_tokens)
+    dk = 128 if q is None and k is None else (k if q is None else q).shape[2]
+    sides = []
+    for x, y in ((q, q_out), (k, k_out)):
+        heads = 0 if x is None else x.shape[1]
+        for t in (x, y):
+            sides += (None, 0) if t is None else _rows(t, T, heads, dk)
+        sides.append(heads)
+    code = load_library().up_rope(ctypes.byref(plan), *sides, dk, positions.data_ptr(), T, _p(num_tokens), bool(transpose),
+                                  dev_status.data_ptr(), _stream(stream))
+    if code:
+        raise UpError(code, "up_rope")
+
+
+# ------------------------------------------------------------------------------------------ eviction
+
+def _int32(t, *shape):
+    assert t.dtype == _I32 and t.is_contiguous() and t.shape == shape
+    return t.data_ptr()
+
+
+def _records(mass, born, shape):
+    """A cache's records, contiguous [num_blocks, Hkv, B]: fp32 and int32 (either may be None)"""
+    assert mass is None or (mass.dtype == torch.float32 and mass.is_contiguous() and mass.shape == shape)
+    assert born is None or (born.dtype == _I32 and born.is_contiguous() and born.shape == shape)
+    return _p(mass), _p(born)
+
+
+def up_kv_mass(q, k_cache, v_cache, block_table, seqused, lse, mass, born, dev_status, k_scale=None, v_scale=None,
+               mass_out=None, counted=None, total=None, decay=1.0, sm_scale=None, stream=None):
+    """mass_out (mass itself where None) <- decay * mass + the weights that q [R, Hq, dk] gave the cached rows, lse [R, Hq]
+    being up_paged_decode's; mass [num_blocks, Hkv, B] fp32, born the same in int32; counted, total [R] int32."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    R, Hq, dk = q.shape
+    out = mass if mass_out is None else mass_out
+    _here(q, k_cache, v_cache, block_table, seqused, lse, mass, out, born, dev_status, k_scale, v_scale, counted, total)
+    shape = (k_cache.shape[0], cache.Hkv, cache.B)
+    mp, bp = _records(mass, born, shape)
+    op, _ = _records(out, None, shape)
+    assert dk == cache.dk and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (R, Hq)
+    qp, qs = _rows(q, R, Hq, dk)
+    code = load_library().up_kv_mass(qp, qs, ctypes.byref(cache), _int32(block_table, R, block_table.shape[1]),
+                                     _int32(seqused, R), lse.data_ptr(), R, block_table.shape[1], Hq,
+                                     dk ** -0.5 if sm_scale is None else sm_scale,
+                                     None if counted is None else _int32(counted, R),
+                                     None if total is None else _int32(total, R), decay, mp, op, bp, dev_status.data_ptr(),
+                                     _stream(stream))
+    if code:
+        raise UpError(code, "up_kv_mass")
+
+
+def up_kv_evict(mass, born, block_table, seqused, budget, moves, num_moves, new_len, dev_status, total=None, sinks=0,
+                recent=0, stream=None):
+    """Which rows of every request and head stay, budget [R] of them, and how they come to be the first:
+    moves [R, Hkv, max_moves, 2] (from, to), num_moves [R, Hkv], new_len [R], all int32."""
+    num_blocks, Hkv, B = mass.shape
+    R, max_blocks = block_table.shape
+    _here(mass, born, block_table, seqused, budget, moves, num_moves, new_len, dev_status, total)
+    mp, bp = _records(mass, born, mass.shape)
+    code = load_library().up_kv_evict(mp, bp, num_blocks, Hkv, B, _int32(block_table, R, max_blocks), _int32(seqused, R),
+                                      _int32(budget, R), R, max_blocks, None if total is None else _int32(total, R), sinks,
+                                      recent, _int32(moves, R, Hkv, moves.shape[2], 2), moves.shape[2],
+                                      _int32(num_moves, R, Hkv), _int32(new_len, R), dev_status.data_ptr(), _stream(stream))
+    if code:
+        raise UpError(code, "up_kv_evict")
+
+
+def up_kv_move(k_cache, v_cache, block_table, moves, num_moves, dev_status, k_scale=None, v_scale=None, mass=None,
+               born=None, stream=None):
+    """Moves the rows of up_kv_evict's lists, with their records (mass and born, either may be None)."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    R, max_blocks = block_table.shape
+    _here(k_cache, v_cache, block_table, moves, num_moves, dev_status, k_scale, v_scale, mass, born)
+    mp, bp = _records(mass, born, (k_cache.shape[0], cache.Hkv, cache.B))
+    code = load_library().up_kv_move(ctypes.byref(cache), _int32(block_table, R, max_blocks), R, max_blocks,
+                                     _int32(moves, R, cache.Hkv, moves.shape[2], 2), moves.shape[2],
+                                     _int32(num_moves, R, cache.Hkv), mp, bp, dev_status.data_ptr(), _stream(stream))
+    if code:
+        raise UpError(code, "up_kv_move")
 
 
 # ------------------------------------------------------------------------------------------ status

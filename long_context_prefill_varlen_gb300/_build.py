@@ -17,7 +17,7 @@ DEBUG_LIB = os.path.join(PKG, "libuniprefill_debug.so")
 # that gives up says so; not loaded by the package either
 WAITS_LIB = os.path.join(PKG, "libuniprefill_waits_%d.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["up_score.cu", "up_select.cu", "up_compact.cu", "up_meta.cu", "up_kv.cu", "up_decode.cu"]
+SOURCES = ["up_score.cu", "up_select.cu", "up_compact.cu", "up_meta.cu", "up_kv.cu", "up_decode.cu", "up_rope.cu", "up_mass.cu", "up_evict.cu"]
 
 
 def nvcc():

@@ -158,6 +158,8 @@ extern "C" const char* up_status_string(int code, int device) {
             case UP_DEV_BAD_SLOT: return "a cache slot lies outside [-1, num_blocks * B)";
             case UP_DEV_BAD_PAGE: return "a block-table entry in use lies outside [0, num_blocks)";
             case UP_DEV_BAD_LENGTH: return "seqused lies outside [0, max_blocks * B]";
+            case UP_DEV_BAD_BUDGET: return "a budget of rows is below 0";
+            case UP_DEV_TOO_MANY_MOVES: return "a request may have more moves than the list holds";
             default: return "unknown device status";
         }
     }
