@@ -6,10 +6,10 @@
 // After up_paged_decode has found a step's lse, a row's weight needs no other row:
 //   mass_i <- decay mass_i + sum_h exp(q_h . K_i sm_scale - lse_h),
 // so the keys are read once more and nothing is joined: 2 dk (dk + 1) bytes a row in bf16 (e4m3) and 8 of records,
-// which HBM bounds.  A warp takes units of 16 to 64 rows of one head, straight from memory to registers: lane 4g + t reads
-// 16-byte pieces t, t + 4, ... of rows g and g + 8, whose numbers are the products' first operand as they come if the
-// queries' columns are taken in the same order (a sum over columns does not care); m16n8k16 with keys in the 16 rows and
-// query heads in the 8 columns.
+// which HBM bounds.  A warp takes its equal share of all requests' tiles of 16 rows, one after another, through a ring of its
+// own in shared memory (copies that need no registers and no other warp).  Lane 4g + t copies, and reads back, 16-byte pieces
+// t, t + 4, ... of rows g and g + 8: they are the products' first operand as they come if the queries' columns are taken in
+// the same order (a sum over columns does not care), in m16n8k16 with keys in the 16 rows and query heads in the 8 columns.
 #include <stdint.h>
 
 #include <algorithm>
@@ -44,13 +44,23 @@ struct Args {
     int32_t* status;
 };
 
-template <int DK, bool E4M3>
+constexpr int kRows = 16;      // of a tile
+
+template <int DK, bool E4M3, bool MANY>
 struct Shape {
     static constexpr int kRowBytes = DK * (E4M3 ? 1 : 2);
-    static constexpr int kPieces = kRowBytes / 64;                     // 16-byte pieces of a row that a lane reads
-    static constexpr int kTiles = kPieces >= 4 ? 1 : 4 / kPieces;      // tiles of 16 rows in a unit: 8 loads in flight or more
-    static constexpr int kRows = 16 * kTiles;
-    static constexpr int kCtas = DK == 256 || (DK == 64 && E4M3) ? 4 : DK == 128 && E4M3 ? 5 : 6;      // on an SM: 128, 96 and 80 registers a thread
+    static constexpr int kPieces = kRowBytes / 64;                     // 16-byte pieces of a row that a lane copies
+    static constexpr int kKeys = kRows * kRowBytes;
+    static constexpr int kStage = kKeys + 128 * (E4M3 ? 3 : 1);        // and a word a lane: its record's mass, its rows' scales
+    // Two tiles in flight a warp and five CTAs an SM (20 warps of 96 registers) against three tiles: 64 requests of 0-8K in
+    // e4m3 58 / 59 us, 32 of up to 16K on heads of 256 63 / 77; against six CTAs (80 registers, spills): 58 / 62.
+    static constexpr int kStages = 2;
+    static constexpr int kBlock = DK == 256 ? 2 : 4;                   // tiles of 8 query heads that a warp keeps in shared memory
+    static constexpr int kTile = (DK / 8 + 8) * 128;                   // bytes of such a tile: the lanes' operands and factors
+    static constexpr int kSmem = kWarps * (kStages * kStage + (MANY ? kBlock * kTile : 0));
+    static constexpr int kFit = 224 * 1024 / (kSmem + 1024);
+    static constexpr int kMost = DK == 256 ? 4 : 5;
+    static constexpr int kCtas = kFit < kMost ? kFit : kMost;
 };
 
 template <bool F16>
@@ -78,11 +88,10 @@ __device__ __forceinline__ float high_of(uint32_t bf2) { return __uint_as_float(
 // The queries of a tile of 8 heads as a lane's second operands, and what turns its sums into log2 weights.
 template <int DK, bool E4M3>
 struct Queries {
-    static constexpr int KS = DK / 16;
+    static constexpr int KS = DK / 16, V = (2 * KS + 8) / 4;
     uint32_t b[KS][2];         // head g of the tile, the columns of the lane's pieces
-    float hi[2], lo[2];        // factors of heads 2t, 2t + 1 (in two parts), and their lse in log2
-    float ref_hi[2], ref_lo[2];
-    bool counts[2];
+    float hi[2], lo[2];        // factors of heads 2t, 2t + 1 (in two parts)
+    float ref_hi[2], ref_lo[2];        // and their lse in log2; infinite: nothing to add
 
     __device__ __forceinline__ void load(const Args& a, int r, int head, int h0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, heads = a.group - h0;
@@ -115,35 +124,61 @@ struct Queries {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int h = 2 * t + x;
-            const float l = h < heads ? a.lse[(int64_t)r * a.Hq + head * a.group + h0 + h] : -INFINITY;
-            counts[x] = l != -INFINITY;
+            const float l = h < heads ? a.lse[(int64_t)r * a.Hq + head * a.group + h0 + h] : INFINITY;
             // lse * log2 e to about 48 bits: fp32 alone would leave 2^-24 |lse| of a weight's exponent
-            ref_hi[x] = l * 1.44269502f;
+            ref_hi[x] = fabsf(l) < INFINITY ? l * 1.44269502f : fabsf(l);
             ref_lo[x] = fabsf(l) < INFINITY ? fmaf(l, 1.44269502f, -ref_hi[x]) + l * 1.92596303e-8f : 0.f;
             hi[x] = a.scale_hi * back[x];
             lo[x] = a.scale_lo * back[x];
         }
     }
+    // to and from a warp's place in shared memory
+    __device__ __forceinline__ void put(uint8_t* at) const {
+        uint32_t w[4 * V];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) w[2 * k] = b[k][0], w[2 * k + 1] = b[k][1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            w[2 * KS + x] = __float_as_uint(hi[x]), w[2 * KS + 2 + x] = __float_as_uint(lo[x]);
+            w[2 * KS + 4 + x] = __float_as_uint(ref_hi[x]), w[2 * KS + 6 + x] = __float_as_uint(ref_lo[x]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            reinterpret_cast<uint4*>(at)[v * 32 + (threadIdx.x & 31)] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+    }
+    __device__ __forceinline__ void get(const uint8_t* at) {
+        uint32_t w[4 * V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint4 x = reinterpret_cast<const uint4*>(at)[v * 32 + (threadIdx.x & 31)];
+            w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) b[k][0] = w[2 * k], b[k][1] = w[2 * k + 1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            hi[x] = __uint_as_float(w[2 * KS + x]), lo[x] = __uint_as_float(w[2 * KS + 2 + x]);
+            ref_hi[x] = __uint_as_float(w[2 * KS + 4 + x]), ref_lo[x] = __uint_as_float(w[2 * KS + 6 + x]);
+        }
+    }
 };
 
-// A warp's run of units: of all requests' units in the order request, head, rows, its equal share.
+// A warp's run of units (tiles of rows): of all requests' units in the order request, head, rows, its equal share.
 struct Walk {
     int r, head, unit, units;      // units: of the request's head
-    int len;
-    int64_t left;
+    int len, from;                 // rows of the request; the first new one
+    int left;                      // units of the run still to come
 
-    template <int ROWS>
     __device__ __forceinline__ int units_of(const Args& a, int n) const {
-        return n < 0 || n > (int64_t)a.max_blocks * static_cast<int64_t>(a.by_b.d) ? 0 : (n + ROWS - 1) / ROWS;
+        return n < 0 || n > (int64_t)a.max_blocks * static_cast<int64_t>(a.by_b.d) ? 0 : (n + kRows - 1) / kRows;
     }
-    template <int ROWS>
     __device__ __forceinline__ void seek(const Args& a, int64_t warp, int64_t warps) {
         const int lane = threadIdx.x & 31;
         left = 0;
         int n = 0, mine = 0, upto = 0;
         auto scan = [&](int r0) {
             n = r0 + lane < a.R && UP_IN(r0 + lane, a.R, a.status) ? a.seqused[r0 + lane] : 0;
-            mine = units_of<ROWS>(a, n);
+            mine = units_of(a, n);
             if (mine == 0 && n != 0) set_status(a.status, UP_DEV_BAD_LENGTH);
             upto = mine;
 #pragma unroll
@@ -166,7 +201,7 @@ struct Walk {
             left = first < all ? 1 : 0;
         } else {
             first = all * warp / warps;
-            left = all * (warp + 1) / warps - first;
+            left = static_cast<int>(all * (warp + 1) / warps - first);
         }
         if (left == 0) return;
         int64_t before = 0;
@@ -181,150 +216,238 @@ struct Walk {
                 const int64_t at = first - before - (int64_t)__shfl_sync(0xffffffffu, upto - mine, l) * a.c.Hkv;
                 head = static_cast<int>(at / units);
                 unit = static_cast<int>(at - (int64_t)head * units);
+                from = a.counted ? a.counted[r] : len;
                 return;
             }
             before += (int64_t)__shfl_sync(0xffffffffu, upto, 31) * a.c.Hkv;
         }
     }
-    // on to the next unit; true where it is another head's
-    template <int ROWS>
-    __device__ __forceinline__ bool next(const Args& a) {
-        if (--left == 0 || ++unit < units) return false;
+    // n units on, no further than to the end of the request's head; true where that is another head's
+    __device__ __forceinline__ bool skip(const Args& a, int n) {
+        left -= n;
+        unit += n;
+        if (left == 0 || unit < units) return false;
         unit = 0;
         if (++head < a.c.Hkv) return true;
         head = 0;
         do {
             ++r;
             len = UP_IN(r, a.R, a.status) ? a.seqused[r] : 0;
-            units = units_of<ROWS>(a, len);
+            units = units_of(a, len);
         } while (units == 0);                          // a unit is left, so a request with one follows
+        from = a.counted ? a.counted[r] : len;
         return true;
     }
 };
 
-template <int DK, bool E4M3, bool MANY>
-__global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3>::kCtas)) mass_kernel(const __grid_constant__ Args a) {
-    using S = Shape<DK, E4M3>;
-    constexpr int NP = S::kPieces, NT = S::kTiles;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where the tiles ahead lie, found by the lanes side by side: a tile of 16 rows lies in one page (WHOLE, pages of a
+// multiple of 16), and a lane finds a tile's; or each row has its own, and a lane finds a row's.  The table's entries are
+// read a batch ahead.
+template <bool WHOLE>
+struct Batch {
+    static constexpr int kTiles = WHOLE ? 32 : 2;
+    Walk next;                 // the batch after this one
+    int next_n, page;
+    int n, i, p0;              // tiles of this one, those used, and its first row
+    int len, from;             // rows of its request, and those whose mass counts
+    int64_t row, rec, sc;      // of the lane's tile (row): bytes, record, scale byte
+    uint32_t valid;            // bit i: lane i's tile (row) has a record
+
+    __device__ __forceinline__ void look(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        next_n = next.left > 0 ? min(kTiles, min(next.units - next.unit, next.left)) : 0;
+        const int pos = next.unit * kRows + (WHOLE ? lane * kRows : lane);
+        const int64_t e = (int64_t)next.r * a.max_blocks + div_of(pos, a.by_b);
+        page = (WHOLE ? lane < next_n : lane < kRows * next_n && pos < next.len) && UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
+    }
+    __device__ __forceinline__ void turn(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        n = next_n;
+        i = 0;
+        p0 = next.unit * kRows, len = next.len, from = a.decay != 0.f ? next.from : 0;
+        if (n == 0) return;
+        const int pos = p0 + (WHOLE ? lane * kRows : lane);
+        const int tok = pos - static_cast<int>(div_of(pos, a.by_b) * a.by_b.d);
+        const bool wanted = WHOLE ? lane < n : lane < kRows * n && pos < len, in = page >= 0 && page < a.c.num_blocks;
+        if (wanted && !in) set_status(a.status, UP_DEV_BAD_PAGE);
+        // what is nowhere copies rows that are there, and leaves no record
+        const int64_t pg = wanted && in ? page : 0, ph = pg * a.c.Hkv + next.head;
+        row = pg * a.c.sb + next.head * a.c.sh + tok * a.c.st;
+        rec = ph * a.by_b.d + tok;
+        sc = ph * a.c.Bp + tok;
+        valid = __ballot_sync(0xffffffffu, wanted && in);
+        next.skip(a, n);
+        look(a);
+    }
+};
+
+template <int DK, bool E4M3, bool MANY, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass_kernel(const __grid_constant__ Args a) {
+    using S = Shape<DK, E4M3, MANY>;
+    constexpr int NP = S::kPieces, NS = S::kStages, NB = S::kBlock;
+    extern __shared__ __align__(16) uint8_t smem[];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    Walk w{};
-    w.seek<S::kRows>(a, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), (int64_t)gridDim.x * kWarps);
-    Queries<DK, E4M3> q;
-    bool fresh = true;
-    while (w.left > 0) {
-        const int p0 = w.unit * S::kRows;
-        if (!MANY && fresh) q.load(a, w.r, w.head, 0);
-        // rows 16 i + 8 j + g of the unit: keys, scale bytes
-        uint4 x[NT][2][NP];
-        float scale[NT][2];
-        int64_t at[NT][2];                             // the row's records, -1 for none
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+    uint8_t* const ring = smem + warp * (S::kSmem / kWarps);
+    uint8_t* const tiles = ring + NS * S::kStage;          // MANY: a block of tiles of queries
+    const uint32_t dst = smem_u32(ring) + 16 * lane, dst4 = smem_u32(ring) + S::kKeys + 4 * lane;
+
+    Batch<WHOLE> ahead{};
+    ahead.next.seek(a, (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
+    if (ahead.next.left == 0) return;
+    Walk w = ahead.next;
+    ahead.look(a);
+    // What a lane keeps of a tile while its keys are on their way: the record that it writes, of row g (t = 0) or g + 8
+    // (t = 1), -1 for none, and where its rows' scale bytes lie in their words.  Nothing that is loaded stays in registers: a
+    // wait for an older tile's would be one for the newer tiles' as well (64 requests of 0-8K in e4m3: 86 -> 67 us).
+    int64_t record[NS];
+    uint32_t byte[NS][2];
+    const uint8_t* const keys = a.c.k + 16 * t + (WHOLE ? g * a.c.st : 0);
+    const int64_t half = 8 * a.c.st;
+    const auto copy = [&](int stage) {
+        if (ahead.i == ahead.n) ahead.turn(a);
+        if (ahead.i < ahead.n) {
+            int64_t row[2], rec[2], sc[2];
+            bool valid[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int pos = p0 + 16 * i + 8 * j + g;
-                const int col = div_of(pos, a.by_b), tok = pos - col * a.by_b.d;
-                const int64_t e = (int64_t)w.r * a.max_blocks + col;
-                int page = -1;
-                if (pos < w.len) {
-                    page = UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : 0;
-                    if (page < 0 || page >= a.c.num_blocks) {
-                        set_status(a.status, UP_DEV_BAD_PAGE);
-                        page = -1;
-                    }
+                if (WHOLE && j) {
+                    row[j] = row[0] + half, rec[j] = rec[0] + 8, sc[j] = sc[0] + 8, valid[j] = valid[0];
+                } else {
+                    const int from = WHOLE ? ahead.i : ahead.i * kRows + 8 * j + g;
+                    row[j] = __shfl_sync(0xffffffffu, ahead.row, from);
+                    rec[j] = __shfl_sync(0xffffffffu, ahead.rec, from) + (WHOLE ? g : 0);
+                    // pages of a multiple of 16 have as many scale bytes
+                    sc[j] = WHOLE ? rec[j] : E4M3 ? __shfl_sync(0xffffffffu, ahead.sc, from) : 0;
+                    valid[j] = ahead.valid >> from & 1;
                 }
-                at[i][j] = page < 0 ? -1 : ((int64_t)page * a.c.Hkv + w.head) * a.by_b.d + tok;
-                scale[i][j] = 1.f;
-                const int64_t row = (int64_t)page * a.c.sb + w.head * a.c.sh + tok * a.c.st + 16 * t;
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    x[i][j][p] = make_uint4(0, 0, 0, 0);
-                    if (page >= 0 && UP_IN(row + 64 * p, a.c.row_limit, a.status))
-                        x[i][j][p] = *reinterpret_cast<const uint4*>(a.c.k + row + 64 * p);
-                }
+                for (int p = 0; p < NP; ++p)
+                    if (UP_IN(row[j] + 64 * p, a.c.row_limit, a.status)) copy16(dst + stage * S::kStage + (j * NP + p) * 512, keys + row[j] + 64 * p);
                 if constexpr (E4M3) {
-                    const int64_t sc = ((int64_t)page * a.c.Hkv + w.head) * a.c.Bp + tok;
-                    if (page >= 0 && UP_IN(sc, a.c.scale_limit, a.status))
-                        scale[i][j] = __uint_as_float(max(static_cast<uint32_t>(a.c.ks[sc]) << 23, 0x00400000u));       // 2^(b - 127)
+                    byte[stage][j] = (WHOLE ? g : static_cast<uint32_t>(sc[j])) & 3;
+                    if (UP_IN(sc[j], a.c.scale_limit, a.status)) copy4(dst4 + stage * S::kStage + 128 * (1 + j), a.c.ks + (sc[j] & ~int64_t{3}));
                 }
             }
-        // lane t of four keeps the records of the rows (i, j) with 2 i + j = t mod 4
-        constexpr int OWN = NT == 1 ? 1 : NT / 2;
-        float old[OWN];
-        const int from = a.counted ? a.counted[w.r] : w.len;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pos = p0 + 16 * i + 8 * j + g;
-                if (((2 * i + j) & 3) == t) {
-                    old[(2 * i + j) / 4] = 0.f;
-                    if (at[i][j] >= 0 && pos < from && a.decay != 0.f && UP_IN(at[i][j], a.records, a.status))
-                        old[(2 * i + j) / 4] = a.mass[at[i][j]];
-                }
-            }
-        float sum[NT][2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) sum[i][0] = sum[i][1] = 0.f;
-        for (int h0 = 0; h0 < (MANY ? a.group : 1); h0 += 8) {
-            if (MANY) q.load(a, w.r, w.head, h0);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[i][0][p]);
-                    const uint32_t* v = reinterpret_cast<const uint32_t*>(&x[i][1][p]);
-                    if constexpr (E4M3) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t a0, a1, a2, a3;
-                            kv::e4m3x4_to_f16x4(u[k], a0, a2);
-                            kv::e4m3x4_to_f16x4(v[k], a1, a3);
-                            mma<true>(d, a0, a1, a2, a3, q.b[4 * p + k][0], q.b[4 * p + k][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            mma<false>(d, u[2 * k], v[2 * k], u[2 * k + 1], v[2 * k + 1], q.b[2 * p + k][0], q.b[2 * p + k][1]);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float y[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float z = d[2 * j + k] * scale[i][j];            // exact
-                        const float e = fmaf(z, q.hi[k], -q.ref_hi[k]) + fmaf(z, q.lo[k], -q.ref_lo[k]);
-                        y[k] = q.counts[k] ? ex2(e) : 0.f;
-                    }
-                    sum[i][j] += y[0] + y[1];
-                }
-            }
+            const int pos = ahead.p0 + ahead.i * kRows + 8 * t + g;
+            const bool mine = t < 2 && (t ? valid[1] : valid[0]) && pos < ahead.len;
+            const int64_t at = t ? rec[1] : rec[0];
+            record[stage] = mine ? at : -1;
+            const uint32_t word = dst4 + stage * S::kStage;
+            if (mine && pos < ahead.from && UP_IN(at, a.records, a.status))
+                copy4(word, a.mass + at);
+            else
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(word), "r"(0) : "memory");
+            ++ahead.i;
         }
+        end_group();
+    };
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NS - 1; ++i) copy(i);
+    Queries<DK, E4M3> q;
+    const int blocks = (a.group + 8 * NB - 1) / (8 * NB);
+    bool fresh = true;
+    for (;;) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                sum[i][j] += __shfl_xor_sync(0xffffffffu, sum[i][j], 1);
-                sum[i][j] += __shfl_xor_sync(0xffffffffu, sum[i][j], 2);
-                const int pos = p0 + 16 * i + 8 * j + g;
-                if (((2 * i + j) & 3) == t && at[i][j] >= 0 && UP_IN(at[i][j], a.records, a.status)) {
-                    a.out[at[i][j]] = fmaf(a.decay, old[(2 * i + j) / 4], sum[i][j]);
-                    if (pos >= from) a.born[at[i][j]] = (a.total ? a.total[w.r] : w.len) - w.len + pos;
+        for (int stage = 0; stage < NS; ++stage) {         // unrolled: a stage's rows are registers
+            if (w.left == 0) return;
+            copy((stage + NS - 1) % NS);
+            if (!MANY && fresh) q.load(a, w.r, w.head, 0);
+            wait_groups<NS - 1>();
+            const uint32_t* const words = reinterpret_cast<const uint32_t*>(ring + stage * S::kStage + S::kKeys) + lane;
+            float scale[2] = {1.f, 1.f};
+            if constexpr (E4M3)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    scale[j] = __uint_as_float(max((words[32 * (1 + j)] >> (8 * byte[stage][j]) & 0xffu) << 23, 0x00400000u));      // 2^(b - 127)
+            float sum[2] = {0.f, 0.f};
+            for (int b = 0; b < (MANY ? blocks : 1); ++b) {
+                const int here = MANY ? min(NB, (a.group - 8 * NB * b + 7) / 8) : 1;
+                if (MANY && (fresh || blocks > 1))         // a lane reads what it has put
+                    for (int i = 0; i < here; ++i) {
+                        q.load(a, w.r, w.head, 8 * (NB * b + i));
+                        q.put(tiles + i * S::kTile);
+                    }
+                for (int i = 0; i < here; ++i) {
+                    if (MANY) q.get(tiles + i * S::kTile);
+                    float d[2][4] = {};                    // in two parts, so that a product need not wait for the one before
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(ring + stage * S::kStage + p * 512 + 16 * lane);
+                        const uint4 z = *reinterpret_cast<const uint4*>(ring + stage * S::kStage + (NP + p) * 512 + 16 * lane);
+                        const uint32_t u[4] = {y.x, y.y, y.z, y.w}, v[4] = {z.x, z.y, z.z, z.w};
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t a0, a1, a2, a3;
+                                kv::e4m3x4_to_f16x4(u[k], a0, a2);
+                                kv::e4m3x4_to_f16x4(v[k], a1, a3);
+                                mma<true>(d[k & 1], a0, a1, a2, a3, q.b[4 * p + k][0], q.b[4 * p + k][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                mma<false>(d[k & 1], u[2 * k], v[2 * k], u[2 * k + 1], v[2 * k + 1], q.b[2 * p + k][0], q.b[2 * p + k][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float y[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float z = (d[0][2 * j + k] + d[1][2 * j + k]) * scale[j];        // the scale: exact
+                            const float e = fmaf(z, q.hi[k], -q.ref_hi[k]) + fmaf(z, q.lo[k], -q.ref_lo[k]);
+                            y[k] = q.ref_hi[k] == INFINITY ? 0.f : ex2(e);
+                        }
+                        sum[j] += y[0] + y[1];
+                    }
                 }
             }
-        fresh = w.next<S::kRows>(a);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+            }
+            const int64_t at = record[stage];
+            if (at >= 0 && UP_IN(at, a.records, a.status)) {
+                const int pos = w.unit * kRows + 8 * t + g;
+                a.out[at] = fmaf(a.decay, __uint_as_float(words[0]), t ? sum[1] : sum[0]);
+                if (pos >= w.from) a.born[at] = (a.total ? a.total[w.r] : w.len) - w.len + pos;
+            }
+            fresh = w.skip(a, 1);
+        }
     }
+}
+
+template <int DK, bool E4M3, bool MANY, bool WHOLE>
+static cudaError_t launch_one(const Args& a, cudaStream_t st) {
+    using S = Shape<DK, E4M3, MANY>;
+    static DeviceSet done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(mass_kernel<DK, E4M3, MANY, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t units = (int64_t)a.R * a.c.Hkv * cdiv((int64_t)a.max_blocks * a.c.B, kRows);
+    const int64_t ctas = std::min<int64_t>(units, (int64_t)S::kCtas * num_sms());
+    return launch_pdl(mass_kernel<DK, E4M3, MANY, WHOLE>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), S::kSmem, st, a);
 }
 
 template <int DK, bool E4M3, bool MANY>
 static cudaError_t launch(const Args& a, cudaStream_t st) {
-    const int64_t units = (int64_t)a.R * a.c.Hkv * cdiv((int64_t)a.max_blocks * a.c.B, Shape<DK, E4M3>::kRows);
-    const int64_t ctas = std::min<int64_t>(units, (int64_t)Shape<DK, E4M3>::kCtas * num_sms());
-    return launch_pdl(mass_kernel<DK, E4M3, MANY>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, a);
+    return a.c.B % kRows == 0 ? launch_one<DK, E4M3, MANY, true>(a, st) : launch_one<DK, E4M3, MANY, false>(a, st);
 }
 
 template <int DK>
