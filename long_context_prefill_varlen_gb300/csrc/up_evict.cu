@@ -7,13 +7,15 @@
 // at or beyond k, as many as there are holes below, move into the holes.  That is the least that can move, and since no
 // row is both a source and a destination the moves need no order among themselves.
 //
-// evict_kernel finds the k-th largest of a list of 32-bit keys, a cluster of CTAs to a (request, head): the keys are read
-// once into shared memory and the digits of the k-th largest found from the top, a histogram of a digit's values a pass,
-// which the cluster's CTAs add up through distributed shared memory.  Then every position's rank among the rows
-// that stay is the number of larger keys before it plus the number of equal ones before it, as far as they stay.
+// evict_kernel finds the k-th largest of a list of 32-bit keys, a CTA or a cluster of CTAs to a (request, head): the keys are
+// read once into shared memory and the digits of the k-th largest (11, 11 and 10 bits) found from the top, a histogram of a
+// digit's values a pass, which the cluster's CTAs add up through distributed shared memory.  Then every position's rank
+// among the rows that stay is the number of larger keys before it plus the number of equal ones before it, as far as they
+// stay.  A lane takes four neighbouring positions at a time: one table entry and two 16-byte loads, where pages allow it.
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "up_kv.cuh"
 
@@ -22,10 +24,10 @@ namespace evict {
 
 using kv::FastDiv;
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kDigit = 8, kBins = 1 << kDigit, kPasses = 32 / kDigit;
+constexpr int kShift0 = 21, kShift1 = 10;    // where a key's first and second digit start
+constexpr int kBins = 2048, kCoarse = kBins / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMostKeys = 48 * 1024;         // keys of a CTA in shared memory; a longer part is read again by every pass
+constexpr int kMostKeys = 32 * 1024;         // keys of a CTA in shared memory; a longer part is read again by every pass
 
 struct Args {
     const float* mass;
@@ -40,6 +42,8 @@ struct Args {
     int64_t num_blocks, records, max_moves;
     int R, Hkv, max_blocks, sinks, recent;
     int room;                // keys that the CTA's shared memory holds
+    int part;                // keys that make a CTA of the cluster worth while
+    bool quads;              // four neighbouring records lie side by side, 16-byte aligned
     FastDiv by_b, by_heads;
     int32_t* status;
 };
@@ -65,21 +69,37 @@ __device__ __forceinline__ uint32_t ld_rank(const void* p, int rank) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t add_at_rank(const void* p, int rank, uint32_t x) {
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(at), "r"(x) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_rank(const void* p, int rank, uint32_t x) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+
 // 32-bit keys in the order of the ranking: numbers by size, -0 as 0, every NaN above them, protected rows above all
-constexpr uint32_t kNan = 0xff800001u, kProtected = 0xffffffffu;
+constexpr uint32_t kZero = 0x80000000u, kNan = 0xff800001u, kProtected = 0xffffffffu;
 __device__ __forceinline__ uint32_t key_of(float x) {
     if (x != x) return kNan;
     const uint32_t b = __float_as_uint(x + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+template <int W>
 struct Shared {
-    uint32_t hist[2][kBins];         // of a digit, every other pass
-    uint32_t scan[kWarps + 1];
-    uint32_t guarded, bad;           // protected rows and bad table entries of the CTA's part
+    alignas(16) uint32_t hist[2][kBins];     // of a digit, every other pass; the second also for candidates
+    uint32_t coarse[2][kCoarse];             // and of 32 neighbouring values together
+    uint32_t guarded, bad, zeros;    // protected rows, bad table entries and zeros of the CTA's part
+    uint32_t candidates;             // of the list, where this CTA collects them
     uint32_t above[2], equal[2];     // of the CTA's part: larger and equal keys below k, and in all
-    uint32_t warp_above[kWarps], warp_equal[kWarps];
-    uint32_t found[2];               // a pass's digit and what remains of k
+    uint32_t warp_above[W], warp_equal[W], warp_above_low[W], warp_equal_low[W];
+    uint32_t list[3];                // protected rows, bad entries and zeros of the list
+    uint32_t found[3];               // a pass's digit, what remains of k, and keys with that digit
+    uint32_t sums[4];                // `above` and `equal` of the list below k, and of the CTAs before
 };
 
 // A list: (request, head) and what its rows are ranked by.
@@ -89,7 +109,7 @@ struct List {
     int recent_from;                 // rows born there or later are protected
     bool few;                        // the protected rows do not all fit: only they are candidates
 
-    // the row's record, -1 for a bad table entry
+    // the record of a position, -1 for a bad table entry
     __device__ __forceinline__ int64_t at(int pos) const {
         const int col = div_of(pos, a.by_b);
         const int64_t e = (int64_t)r * a.max_blocks + col;
@@ -97,39 +117,97 @@ struct List {
         if (page < 0 || page >= a.num_blocks) return -1;
         return ((int64_t)page * a.Hkv + head) * a.by_b.d + (pos - col * static_cast<int>(a.by_b.d));
     }
-    __device__ __forceinline__ uint32_t key(int pos, bool* guarded, bool* bad) const {
-        const int64_t i = at(pos);
-        *bad = i < 0;
-        *guarded = false;
-        if (i < 0 || !UP_IN(i, a.records, a.status)) return 0;
-        const int born = a.born[i];
-        *guarded = born < a.sinks || born >= recent_from;
-        const uint32_t key = key_of(a.mass[i]);
-        return few ? (*guarded ? key : 0u) : *guarded ? kProtected : key;
+    __device__ __forceinline__ uint32_t key(float mass, int born, uint32_t* guards) const {
+        const bool guarded = born < a.sinks || born >= recent_from;
+        *guards += guarded;
+        const uint32_t key = key_of(mass);
+        return few ? (guarded ? key : 0u) : guarded ? kProtected : key;
+    }
+    // Four neighbouring records from pos on (a multiple of 4): where they are, then what they hold.
+    struct Quad {
+        int64_t at[4];               // the first one's where they lie side by side
+        float m[4];
+        int b[4];
+    };
+    // false for a bad table entry
+    __device__ __forceinline__ bool locate(int pos, Quad& q) const {
+        if (a.quads) {
+            q.at[0] = pos < len ? at(pos) : -1;
+            return pos >= len || q.at[0] >= 0;
+        }
+        bool good = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            q.at[j] = pos + j < len ? at(pos + j) : -1;
+            good &= pos + j >= len || q.at[j] >= 0;
+        }
+        return good;
+    }
+    __device__ __forceinline__ void fetch(Quad& q) const {
+        if (a.quads) {
+            if (q.at[0] >= 0 && UP_IN(q.at[0] + 3, a.records, a.status)) {
+                *reinterpret_cast<float4*>(q.m) = *reinterpret_cast<const float4*>(a.mass + q.at[0]);
+                *reinterpret_cast<int4*>(q.b) = *reinterpret_cast<const int4*>(a.born + q.at[0]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (q.at[j] >= 0 && UP_IN(q.at[j], a.records, a.status)) q.m[j] = a.mass[q.at[j]], q.b[j] = a.born[q.at[j]];
+        }
+    }
+    // their keys, 0 (below every key) for those that the list does not have
+    __device__ __forceinline__ uint4 keys(int pos, const Quad& q, uint32_t* guards) const {
+        uint32_t x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = pos + j < len ? key(q.m[j], q.b[j], guards) : 0u;
+        return make_uint4(x[0], x[1], x[2], x[3]);
     }
 };
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ Args a) {
-    extern __shared__ uint32_t keys[];
-    __shared__ Shared sh;
+// where the other CTAs' sums are: their own shared memory, or this CTA's alone
+template <bool TEAM>
+__device__ __forceinline__ void meet() {
+    if constexpr (TEAM) cluster_meet(); else __syncthreads();
+}
+template <bool TEAM>
+__device__ __forceinline__ uint32_t of_cta(const uint32_t* p, int rank) {
+    if constexpr (TEAM) return ld_rank(p, rank); else return *p;
+}
+// the sum of a word over the list's CTAs, all on their way at once
+template <bool TEAM>
+__device__ __forceinline__ uint32_t over_ctas(const uint32_t* p, int ctas) {
+    if constexpr (!TEAM) return *p;
+    uint32_t v[kMaxCluster], n = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) v[c] = c < ctas ? ld_rank(p, c) : 0u;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) n += v[c];
+    return n;
+}
+
+template <int W, bool TEAM>
+__global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __grid_constant__ Args a) {
+    constexpr int kThreads = 32 * W;
+    extern __shared__ __align__(16) uint4 keys[];
+    __shared__ Shared<W> sh;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = cluster_rank(), ctas = cluster_size();
-    const int list = static_cast<int>(blockIdx.x) / ctas;
+    const int size = TEAM ? cluster_size() : 1, rank = TEAM ? cluster_rank() : 0;
+    const int list = TEAM ? static_cast<int>(blockIdx.x) / size : blockIdx.x;
     const int r = div_of(list, a.by_heads), head = list - r * a.Hkv;
     const bool first = rank == 0 && tid == 0;
     List l{a, r, head, 0, 0, 0, false};
     // what the list's CTAs all see alike, and leave together for
     const int64_t cap = (int64_t)a.max_blocks * a.by_b.d;
     l.len = UP_IN(r, a.R, a.status) ? a.seqused[r] : 0;
+    const int budget = a.budget[r], total = a.total ? a.total[r] : 0;
     if (l.len < 0 || l.len > cap) {
         if (first) set_status(a.status, UP_DEV_BAD_LENGTH);
         l.len = 0;
     }
-    const int budget = a.budget[r];
     l.k = min(budget, l.len);
-    l.recent_from = static_cast<int>(max((int64_t)(a.total ? a.total[r] : l.len) - a.recent, (int64_t)INT32_MIN));
+    l.recent_from = static_cast<int>(max((int64_t)(a.total ? total : l.len) - a.recent, (int64_t)INT32_MIN));
     const auto leave = [&](int len) {
         if (first) a.num_moves[list] = 0;
         if (first && head == 0) a.new_len[r] = len;
@@ -143,127 +221,275 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         return leave(l.len);
     }
     if (l.k == l.len || l.k == 0) return leave(l.k);       // all rows stay, or none
-    // the CTA's part of the positions and the warp's part of that
-    const int per_warp = static_cast<int>((l.len + (int64_t)ctas * kThreads - 1) / (ctas * kThreads)) * 32, per = per_warp * kWarps;
-    const int start = rank * per, from = min(start + warp * per_warp, l.len), to = min(from + per_warp, l.len);
+    // As many CTAs as the list is worth; the others leave at once (a cluster's barriers wait for those that stay).  A CTA
+    // has a part of the positions, a warp a part of that, in steps of 128.
+    const int ctas = TEAM ? min(size, (l.len + a.part - 1) / a.part) : 1;
+    if (rank >= ctas) return;
+    const int steps = (l.len + ctas * (128 * W) - 1) / (ctas * (128 * W)), per = steps * 128 * W;
+    const int from = rank * per + warp * steps * 128 + 4 * lane;      // the lane's first position
     const bool held = per <= a.room;
-    for (int i = tid; i < 2 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-    if (tid == 0) sh.guarded = sh.bad = 0;
+    uint4* const mine = keys + (warp * steps * 32 + lane);
+    const auto clear = [&](uint32_t* hist) {
+        for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    };
+    clear(sh.hist[0]);
+    clear(sh.hist[1]);
+    if (tid == 0) sh.guarded = sh.bad = sh.zeros = sh.candidates = 0;
     __syncthreads();
 
-    uint32_t prefix = 0;             // the digits found so far
-    const auto key_at = [&](int pos) {
-        if (held) return keys[pos - start];
-        bool guarded, bad;
-        return l.key(pos, &guarded, &bad);
-    };
-    // the keys, and the histogram of their first digit
-    const auto load = [&]() {
-        uint32_t guards = 0, bads = 0;
-        for (int p = from + lane; p < to; p += 32) {
-            bool guarded, bad;
-            const uint32_t key = l.key(p, &guarded, &bad);
-            guards += guarded;
-            bads += bad;
-            if (held) keys[p - start] = key;
-            atomicAdd(&sh.hist[0][key >> (32 - kDigit)], 1u);
+    const auto load = [&]() {            // the keys, and the histogram of their first digit
+        uint32_t guards = 0, bads = 0, zeros = 0;
+        typename List::Quad q[2], next[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) bads += !l.locate(u < steps ? from + 128 * u : l.len, q[u]);
+        for (int i0 = 0; i0 < steps; i0 += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) l.fetch(q[u]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)                // the next step's places while this one's records are on their way
+                bads += !l.locate(i0 + 2 + u < steps ? from + 128 * (i0 + 2 + u) : l.len, next[u]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int p = from + 128 * (i0 + u);
+                if (i0 + u < steps && p < l.len) {
+                    const uint4 y = l.keys(p, q[u], &guards);
+                    if (held) mine[32 * (i0 + u)] = y;
+                    const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {      // zeros and protected rows are many, and counted apart
+                        zeros += x[j] == kZero;
+                        if (x[j] != kZero && x[j] != kProtected && x[j] != 0) atomicAdd(&sh.hist[0][x[j] >> kShift0], 1u);
+                    }
+                }
+                q[u] = next[u];
+            }
         }
+        if (held)                        // positions behind the list
+            for (int i = 0; i < steps; ++i)
+                if (from + 128 * i >= l.len) mine[32 * i] = make_uint4(0, 0, 0, 0);
         guards = __reduce_add_sync(0xffffffffu, guards);
         bads = __reduce_add_sync(0xffffffffu, bads);
-        if (lane == 0 && guards) atomicAdd(&sh.guarded, guards);
-        if (lane == 0 && bads) atomicAdd(&sh.bad, bads);
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        if (lane == 0) {
+            if (guards) atomicAdd(&sh.guarded, guards);
+            if (bads) atomicAdd(&sh.bad, bads);
+            if (zeros) {
+                atomicAdd(&sh.zeros, zeros);
+                atomicAdd(&sh.hist[0][kZero >> kShift0], zeros);
+            }
+            if (guards && !l.few) atomicAdd(&sh.hist[0][kProtected >> kShift0], guards);
+        }
+    };
+    // step i's keys again
+    const auto again = [&](int i) {
+        if (held) return mine[32 * i];
+        typename List::Quad q;
+        uint32_t guards = 0;
+        l.locate(from + 128 * i, q);
+        l.fetch(q);
+        return l.keys(from + 128 * i, q, &guards);
+    };
+    // sums of 32 neighbouring values of a histogram, a warp some
+    const auto coarsen = [&](int which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = warp; i < kCoarse; i += W) {
+            const uint32_t n = __reduce_add_sync(0xffffffffu, sh.hist[which][32 * i + lane]);
+            if (lane == 0) sh.coarse[which][i] = n;
+        }
+    };
+    // protected rows, bad entries and zeros of the list
+    const auto gather = [&]() {
+        if (warp == 0) {
+            const uint32_t x[3] = {over_ctas<TEAM>(&sh.guarded, ctas), over_ctas<TEAM>(&sh.bad, ctas), over_ctas<TEAM>(&sh.zeros, ctas)};
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (lane == i) sh.list[i] = x[i];
+        }
+        __syncthreads();
     };
     load();
-    cluster_meet();
-    uint32_t guards = 0, bads = 0;
-    for (int c = 0; c < ctas; ++c) {
-        guards += ld_rank(&sh.guarded, c);
-        bads += ld_rank(&sh.bad, c);
-    }
-    if (bads) {
+    coarsen(0);
+    meet<TEAM>();
+    gather();
+    if (sh.list[1]) {
         if (first) set_status(a.status, UP_DEV_BAD_PAGE);
-        cluster_meet();                            // no CTA leaves while another reads its sums
+        meet<TEAM>();                              // no CTA leaves while another reads its sums
         return leave(l.len);
     }
-    if (guards > static_cast<uint32_t>(l.k)) {
+    if (sh.list[0] > static_cast<uint32_t>(l.k)) {
         l.few = true;
-        cluster_meet();                            // nobody reads the first keys' histogram
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+        meet<TEAM>();                              // all have read the counts
+        clear(sh.hist[0]);
+        if (tid == 0) sh.zeros = 0;
         __syncthreads();
         load();
-        cluster_meet();
+        coarsen(0);
+        meet<TEAM>();
+        gather();
     }
-    uint32_t need = l.k;                           // how many of the keys with this prefix stay
-    for (int pass = 0; pass < kPasses; ++pass) {
-        const int shift = 32 - kDigit * (pass + 1);
-        uint32_t* const hist = sh.hist[pass & 1];
-        if (pass) {
-            for (int p = from + lane; p < to; p += 32) {
-                const uint32_t key = key_at(p);
-                if ((key ^ prefix) >> (shift + kDigit) == 0) atomicAdd(&hist[(key >> shift) & (kBins - 1)], 1u);
+    uint32_t prefix = 0, need = l.k;               // the digits found so far, and how many of the keys with them stay
+    // The digit whose keys, and all larger ones, are the first to reach `need`: first of 32 values together, then of one.
+    // TOGETHER: over the histograms of all the list's CTAs, or this one's alone.
+    const auto find = [&](int which, int shift, auto together) {
+        constexpr bool TOGETHER = TEAM && decltype(together)::value;
+        if (warp == 0) {
+            uint32_t before = 0, count = 0;
+            int bin = 0;
+#pragma unroll
+            for (int level = 0; level < 2; ++level) {
+                constexpr int kEach[2] = {kCoarse / 32, 1};        // words of a lane; lane 0 has the largest
+                uint32_t n[2] = {}, all = 0;
+#pragma unroll
+                for (int j = 0; j < kEach[level]; ++j) {
+                    const int at = level ? 32 * bin + 31 - lane : kCoarse - 1 - (kEach[0] * lane + j);
+                    n[j] = over_ctas<TOGETHER>(level ? &sh.hist[which][at] : &sh.coarse[which][at], ctas);
+                    all += n[j];
+                }
+                uint32_t upto = all;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                // the first lane that reaches it, and of its words the first
+                const int l0 = __ffs(__ballot_sync(0xffffffffu, before + upto >= need)) - 1;
+                uint32_t sum = before + upto - all;
+                int j = 0;
+                if (kEach[level] == 2 && sum + n[0] < need) sum += n[0], j = 1;
+                const int at = level ? 32 * bin + 31 - lane : kCoarse - 1 - (kEach[0] * lane + j);
+                before = __shfl_sync(0xffffffffu, sum, l0);
+                bin = __shfl_sync(0xffffffffu, at, l0);
+                count = __shfl_sync(0xffffffffu, n[0], l0);
             }
-            cluster_meet();
+            if (lane == 0) sh.found[0] = bin, sh.found[1] = need - before, sh.found[2] = count;
         }
-        // the digit whose keys, and all larger ones, are the first to reach `need`; thread i has digit kBins - 1 - i
-        uint32_t n = 0, upto;
-        if (tid < kBins)
-            for (int c = 0; c < ctas; ++c) n += ld_rank(&hist[kBins - 1 - tid], c);
-        upto = n;
+        __syncthreads();
+        prefix |= sh.found[0] << shift;
+        need = sh.found[1];
+    };
+    find(0, kShift0, std::true_type{});
+    const uint32_t digit = prefix >> kShift0, rest = sh.found[2];
+    if (digit == kProtected >> kShift0) {
+        prefix = kProtected;                       // that digit's one key
+    } else if (digit == kZero >> kShift0 && rest == sh.list[2]) {
+        prefix = kZero;                            // nothing but zeros
+    } else if (rest <= kBins) {
+        // The keys with that digit, few by now, go to the first CTA, which finds the other digits alone.
+        uint32_t n = 0;
+        for (int i = 0; i < steps; ++i) {
+            const uint4 y = again(i);
+            n += (y.x >> kShift0 == digit) + (y.y >> kShift0 == digit) + (y.z >> kShift0 == digit) + (y.w >> kShift0 == digit);
+        }
+        uint32_t upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
-        if (lane == 31) sh.scan[warp] = upto;
-        __syncthreads();
-        uint32_t before = upto - n;
-        for (int w = 0; w < warp && w < kBins / 32; ++w) before += sh.scan[w];
-        if (tid < kBins && before < need && before + n >= need) {
-            sh.found[0] = kBins - 1 - tid;
-            sh.found[1] = need - before;
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        if (all) {
+            uint32_t at = 0;
+            if (lane == 0) at = TEAM ? add_at_rank(&sh.candidates, 0, all) : atomicAdd(&sh.candidates, all);
+            at = __shfl_sync(0xffffffffu, at, 0) + upto - n;
+            for (int i = 0; i < steps && n; ++i) {
+                const uint4 y = again(i);
+                const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (x[j] >> kShift0 == digit) {
+                        if (TEAM) st_rank(&sh.hist[1][at], 0, x[j]); else sh.hist[1][at] = x[j];
+                        ++at;
+                        --n;
+                    }
+            }
         }
-        // the other histogram was read before this pass's meeting
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
-        __syncthreads();
-        prefix |= sh.found[0] << shift;
-        need = sh.found[1];
+        meet<TEAM>();                              // all have read the first histograms, too
+        if (rank == 0) {
+#pragma unroll
+            for (int pass = 1; pass < 3; ++pass) {
+                const int known = pass == 1 ? kShift0 : kShift1, shift = pass == 1 ? kShift1 : 0;
+                clear(sh.hist[0]);
+                __syncthreads();
+                for (uint32_t i = tid; i < rest; i += kThreads) {
+                    const uint32_t x = sh.hist[1][i];
+                    if ((x ^ prefix) >> known == 0) atomicAdd(&sh.hist[0][x >> shift & ((1u << (known - shift)) - 1)], 1u);
+                }
+                coarsen(0);
+                __syncthreads();
+                find(0, shift, std::false_type{});
+            }
+            __syncthreads();
+            if (tid == 0) sh.found[0] = prefix;
+        }
+        if (TEAM) {
+            meet<TEAM>();
+            prefix = of_cta<TEAM>(&sh.found[0], 0);
+            need = of_cta<TEAM>(&sh.found[1], 0);
+        }
+    } else {
+#pragma unroll
+        for (int pass = 1; pass < 3; ++pass) {
+            const int known = pass == 1 ? kShift0 : kShift1, shift = pass == 1 ? kShift1 : 0;
+            for (int i = 0; i < steps; ++i) {
+                const uint4 y = again(i);
+                const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((x[j] ^ prefix) >> known == 0) atomicAdd(&sh.hist[pass & 1][x[j] >> shift & ((1u << (known - shift)) - 1)], 1u);
+            }
+            coarsen(pass & 1);
+            meet<TEAM>();
+            if (pass == 1) clear(sh.hist[0]);      // read before this pass's meeting
+            find(pass & 1, shift, std::true_type{});
+        }
     }
-    // prefix is the k-th largest key: rows with larger ones stay, and the first `need` with equal ones
+    // prefix is the k-th largest key: rows with larger ones stay, and the first `need` with equal ones.  Counts of either: the
+    // lower and the upper half of a sum where it is of one step's 128 keys.
+    const auto compare = [&](uint32_t x) { return x > prefix ? 1u : x == prefix ? 0x10000u : 0u; };
     uint32_t above = 0, equal = 0, above_low = 0, equal_low = 0;
-    for (int p = from + lane; p < to; p += 32) {
-        const uint32_t key = key_at(p);
-        above += key > prefix;
-        equal += key == prefix;
-        above_low += key > prefix && p < l.k;
-        equal_low += key == prefix && p < l.k;
+    for (int i = 0; i < steps; ++i) {
+        const int p = from + 128 * i;
+        const uint4 y = again(i);
+        const uint32_t c[4] = {compare(y.x), compare(y.y), compare(y.z), compare(y.w)};
+        uint32_t all = 0, low = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            all += c[j];
+            low += p + j < l.k ? c[j] : 0u;
+        }
+        above += all & 0xffffu, equal += all >> 16;
+        above_low += low & 0xffffu, equal_low += low >> 16;
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
     above_low = __reduce_add_sync(0xffffffffu, above_low);
     equal_low = __reduce_add_sync(0xffffffffu, equal_low);
-    if (tid < 2) sh.above[tid] = sh.equal[tid] = 0;
-    if (lane == 0) sh.warp_above[warp] = above, sh.warp_equal[warp] = equal;
-    __syncthreads();
     if (lane == 0) {
-        atomicAdd(&sh.above[0], above_low);
-        atomicAdd(&sh.equal[0], equal_low);
-        atomicAdd(&sh.above[1], above);
-        atomicAdd(&sh.equal[1], equal);
+        sh.warp_above[warp] = above, sh.warp_equal[warp] = equal;
+        sh.warp_above_low[warp] = above_low, sh.warp_equal_low[warp] = equal_low;
     }
-    cluster_meet();
-    above = equal = above_low = equal_low = 0;     // now: before the warp's part, and below k in the whole list
-    for (int c = 0; c < ctas; ++c) {
-        above_low += ld_rank(&sh.above[0], c);
-        equal_low += ld_rank(&sh.equal[0], c);
-        if (c < rank) {
-            above += ld_rank(&sh.above[1], c);
-            equal += ld_rank(&sh.equal[1], c);
+    __syncthreads();
+    // of the CTA below k, and of its warps before this one
+    const auto over_warps = [&](const uint32_t* x, int warps) { return __reduce_add_sync(0xffffffffu, lane < warps ? x[lane] : 0u); };
+    above_low = over_warps(sh.warp_above_low, W), equal_low = over_warps(sh.warp_equal_low, W);
+    above = over_warps(sh.warp_above, warp), equal = over_warps(sh.warp_equal, warp);
+    if (TEAM) {
+        if (warp == 0) {
+            const uint32_t x = over_warps(sh.warp_above, W), y = over_warps(sh.warp_equal, W);
+            if (lane == 0) sh.above[0] = above_low, sh.equal[0] = equal_low, sh.above[1] = x, sh.equal[1] = y;
         }
-    }
-    cluster_meet();                                // as above
-    for (int w = 0; w < warp; ++w) {
-        above += sh.warp_above[w];
-        equal += sh.warp_equal[w];
+        meet<TEAM>();
+        if (warp == 0) {
+            const uint32_t x[4] = {over_ctas<TEAM>(&sh.above[0], ctas), over_ctas<TEAM>(&sh.equal[0], ctas),
+                                   over_ctas<TEAM>(&sh.above[1], rank), over_ctas<TEAM>(&sh.equal[1], rank)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lane == i) sh.sums[i] = x[i];
+        }
+        meet<TEAM>();                              // and no CTA leaves while another reads its sums
+        above_low = sh.sums[0], equal_low = sh.sums[1];
+        above += sh.sums[2], equal += sh.sums[3];
     }
     const uint32_t stay_low = above_low + min(equal_low, need);
     if (first) {
@@ -271,21 +497,64 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         if (head == 0) a.new_len[r] = l.k;
     }
     int32_t* const moves = a.moves + (int64_t)list * a.max_moves * 2;
-    const uint32_t under = (1u << lane) - 1;
-    for (int p0 = from; p0 < to; p0 += 32) {
-        const int p = p0 + lane;
-        const uint32_t key = p < to ? key_at(p) : 0;
-        const uint32_t gt = __ballot_sync(0xffffffffu, p < to && key > prefix), eq = __ballot_sync(0xffffffffu, p < to && key == prefix);
-        const uint32_t eq_before = equal + __popc(eq & under);
-        const uint32_t stay_before = above + __popc(gt & under) + min(eq_before, need);
-        const bool stays = key > prefix || (key == prefix && eq_before < need);
-        if (p < to && (p < l.k) != stays) {
-            const int64_t i = p < l.k ? p - stay_before : stay_before - stay_low;
-            if (UP_IN(i, a.max_moves, a.status)) moves[2 * i + (p < l.k ? 1 : 0)] = p;
+    for (int i = 0; i < steps; ++i) {
+        const int p = from + 128 * i, p0 = p - 4 * lane;
+        const uint4 y = again(i);
+        const uint32_t c[4] = {compare(y.x), compare(y.y), compare(y.z), compare(y.w)};
+        const uint32_t own = c[0] + c[1] + c[2] + c[3], all = __reduce_add_sync(0xffffffffu, own);
+        const uint32_t here = (all & 0xffffu) + min(equal + (all >> 16), need) - min(equal, need);     // rows of the step that stay
+        // nothing moves where all of a step's rows below k stay, or none of those beyond
+        if (!(p0 + 128 <= l.k && here == 128) && !(p0 >= l.k && here == 0)) {
+            uint32_t upto = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += z;
+            }
+            uint32_t gt = above + ((upto - own) & 0xffffu), eq = equal + ((upto - own) >> 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t stay_before = gt + min(eq, need);
+                const bool stays = c[j] == 1u || (c[j] != 0u && eq < need), low = p + j < l.k;
+                if (p + j < l.len && low != stays) {
+                    const uint32_t m = low ? p + j - stay_before : stay_before - stay_low;
+                    if (UP_IN(m, a.max_moves, a.status)) moves[2 * (size_t)m + low] = p + j;
+                }
+                gt += c[j] & 1u;
+                eq += c[j] >> 16;
+            }
         }
-        above += __popc(gt);
-        equal += __popc(eq);
+        above += all & 0xffffu;
+        equal += all >> 16;
     }
+}
+
+// The CTAs of a list and the keys that they hold.  One CTA has the keys of 32K positions at most in 128 KB; where the lists
+// leave SMs idle, or are longer, a cluster shares one.
+template <int W, bool TEAM>
+static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_t st) {
+    static DeviceSet done{0};
+    cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(evict_kernel<W, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d;
+    a.room = static_cast<int>(std::min<int64_t>(cdiv(cap, (int64_t)cluster * 128 * W) * 128 * W, kMostKeys));
+    if (!TEAM) return launch_pdl(evict_kernel<W, TEAM>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(lists * cluster));
+    cfg.blockDim = dim3(32 * W);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.room) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, evict_kernel<W, TEAM>, a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -440,29 +709,12 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     a.by_heads = kv::fast_div(Hkv);
     a.status = dev_status;
     const int64_t lists = (int64_t)R * Hkv, cap = (int64_t)max_blocks * B;
+    a.quads = B % 4 == 0 && aligned16(mass) && aligned16(born);
     int cluster = 1;
-    while (cluster < kMaxCluster && lists * cluster * 2 <= 2 * num_sms() && cap > (int64_t)cluster * 2 * kThreads) cluster *= 2;
-    const int64_t part = cdiv(cap, (int64_t)cluster * kThreads) * kThreads;
-    a.room = static_cast<int>(std::min<int64_t>(part, kMostKeys));
-    static DeviceSet done{0};
-    cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
-    });
-    if (e != cudaSuccess) return failed_launch();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(lists * cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.room) * 4;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, evict_kernel, a);
+    a.part = lists > num_sms() ? kMostKeys / 2 : 1024;
+    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part && (lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys)) cluster *= 2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cluster > 1 ? launch_evict<16, true>(a, cluster, lists, st) : launch_evict<16, false>(a, 1, lists, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();
