@@ -352,11 +352,16 @@ def up_rope_plan(rot, theta=10000.0, layout="halves", scaling="none", factor=1.0
     return plan
 
 
-def _here(*tensors):
-    """The device of a call's tensors, all on the current one: a launch goes to the current device's stream."""
+def _launch(stream, *tensors):
+    """The handle of a call's stream; its tensors, and the stream, belong to the current device, which is launched on."""
     device = torch.cuda.current_device()
     for t in tensors:
-        assert t is None or t.device.index == device, "tensors on another device than the current one"
+        if t is not None and t.get_device() != device:
+            raise AssertionError("a tensor on another device than the current one")
+    if stream is None:
+        return _c_p(torch._C._cuda_getCurrentRawStream(device))
+    assert stream.device.index == device
+    return _c_p(stream.cuda_stream)
 
 
 def up_rope(plan, positions, dev_status, q=None, q_out=None, k=None, k_out=None, num_tokens=None, transpose=False,
@@ -365,34 +370,40 @@ def up_rope(plan, positions, dev_status, q=None, q_out=None, k=None, k_out=None,
     q_out may be q.  transpose: the gradient of that."""
     T = positions.numel()
     assert (q is None) == (q_out is None) and (k is None) == (k_out is None)
-    assert positions.dtype == _I64 and positions.is_contiguous()
-    assert num_tokens is None or num_tokens.dtype == _I32
-    _here(positions, dev_status, q, q_out, k, k_out, num_tokens)
-    dk = 128 if q is None and k is None else (k if q is None else q).shape[2]
-    sides = []
-    for x, y in ((q, q_out), (k, k_out)):
-        heads = 0 if x is None else x.shape[1]
-        for t in (x, y):
-            sides += (None, 0) if t is None else _rows(t, T, heads, dk)
-        sides.append(heads)
-    code = load_library().up_rope(ctypes.byref(plan), *sides, dk, positions.data_ptr(), T, _p(num_tokens), bool(transpose),
-                                  dev_status.data_ptr(), _stream(stream))
+    assert positions.dtype is _I64 and positions.is_contiguous()
+    assert num_tokens is None or num_tokens.dtype is _I32
+    st = _launch(stream, positions, dev_status, q, q_out, k, k_out, num_tokens)
+    Hq = Hkv = 0
+    dk, qp, qs, qo, qos, kp, ks, ko, kos = 128, None, 0, None, 0, None, 0, None, 0
+    if q is not None:
+        _, Hq, dk = q.shape
+        (qp, qs), (qo, qos) = _rows(q, T, Hq, dk), _rows(q_out, T, Hq, dk)
+    if k is not None:
+        Hkv = k.shape[1]
+        dk = k.shape[2] if q is None else dk
+        (kp, ks), (ko, kos) = _rows(k, T, Hkv, dk), _rows(k_out, T, Hkv, dk)
+    code = load_library().up_rope(ctypes.byref(plan), qp, qs, qo, qos, Hq, kp, ks, ko, kos, Hkv, dk, positions.data_ptr(), T,
+                                  _p(num_tokens), bool(transpose), dev_status.data_ptr(), st)
     if code:
         raise UpError(code, "up_rope")
 
 
 # ------------------------------------------------------------------------------------------ eviction
 
-def _int32(t, *shape):
-    assert t.dtype == _I32 and t.is_contiguous() and t.shape == shape
+def _int32(t, n):
+    """n contiguous int32 numbers, or None"""
+    if t is None:
+        return None
+    assert t.dtype is _I32 and t.is_contiguous() and t.numel() == n
     return t.data_ptr()
 
 
-def _records(mass, born, shape):
-    """A cache's records, contiguous [num_blocks, Hkv, B]: fp32 and int32 (either may be None)"""
-    assert mass is None or (mass.dtype == torch.float32 and mass.is_contiguous() and mass.shape == shape)
-    assert born is None or (born.dtype == _I32 and born.is_contiguous() and born.shape == shape)
-    return _p(mass), _p(born)
+def _records(t, dtype, shape):
+    """A cache's records, contiguous [num_blocks, Hkv, B], or None"""
+    if t is None:
+        return None
+    assert t.dtype is dtype and t.is_contiguous() and t.shape == shape
+    return t.data_ptr()
 
 
 def up_kv_mass(q, k_cache, v_cache, block_table, seqused, lse, mass, born, dev_status, k_scale=None, v_scale=None,
@@ -401,19 +412,17 @@ def up_kv_mass(q, k_cache, v_cache, block_table, seqused, lse, mass, born, dev_s
     being up_paged_decode's; mass [num_blocks, Hkv, B] fp32, born the same in int32; counted, total [R] int32."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     R, Hq, dk = q.shape
-    out = mass if mass_out is None else mass_out
-    _here(q, k_cache, v_cache, block_table, seqused, lse, mass, out, born, dev_status, k_scale, v_scale, counted, total)
-    shape = (k_cache.shape[0], cache.Hkv, cache.B)
-    mp, bp = _records(mass, born, shape)
-    op, _ = _records(out, None, shape)
-    assert dk == cache.dk and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (R, Hq)
+    rows, max_blocks = block_table.shape
+    st = _launch(stream, q, k_cache, v_cache, block_table, seqused, lse, mass, mass_out, born, dev_status, k_scale, v_scale,
+                 counted, total)
+    shape = (cache.num_blocks, cache.Hkv, cache.B)
+    mp, bp = _records(mass, torch.float32, shape), _records(born, _I32, shape)
+    op = mp if mass_out is None else _records(mass_out, torch.float32, shape)
+    assert dk == cache.dk and rows == R and lse.dtype is torch.float32 and lse.is_contiguous() and lse.shape == (R, Hq)
     qp, qs = _rows(q, R, Hq, dk)
-    code = load_library().up_kv_mass(qp, qs, ctypes.byref(cache), _int32(block_table, R, block_table.shape[1]),
-                                     _int32(seqused, R), lse.data_ptr(), R, block_table.shape[1], Hq,
-                                     dk ** -0.5 if sm_scale is None else sm_scale,
-                                     None if counted is None else _int32(counted, R),
-                                     None if total is None else _int32(total, R), decay, mp, op, bp, dev_status.data_ptr(),
-                                     _stream(stream))
+    code = load_library().up_kv_mass(qp, qs, ctypes.byref(cache), _int32(block_table, R * max_blocks), _int32(seqused, R),
+                                     lse.data_ptr(), R, max_blocks, Hq, dk ** -0.5 if sm_scale is None else sm_scale,
+                                     _int32(counted, R), _int32(total, R), decay, mp, op, bp, dev_status.data_ptr(), st)
     if code:
         raise UpError(code, "up_kv_mass")
 
@@ -422,14 +431,16 @@ def up_kv_evict(mass, born, block_table, seqused, budget, moves, num_moves, new_
                 recent=0, stream=None):
     """Which rows of every request and head stay, budget [R] of them, and how they come to be the first:
     moves [R, Hkv, max_moves, 2] (from, to), num_moves [R, Hkv], new_len [R], all int32."""
-    num_blocks, Hkv, B = mass.shape
+    shape = mass.shape
+    num_blocks, Hkv, B = shape
     R, max_blocks = block_table.shape
-    _here(mass, born, block_table, seqused, budget, moves, num_moves, new_len, dev_status, total)
-    mp, bp = _records(mass, born, mass.shape)
-    code = load_library().up_kv_evict(mp, bp, num_blocks, Hkv, B, _int32(block_table, R, max_blocks), _int32(seqused, R),
-                                      _int32(budget, R), R, max_blocks, None if total is None else _int32(total, R), sinks,
-                                      recent, _int32(moves, R, Hkv, moves.shape[2], 2), moves.shape[2],
-                                      _int32(num_moves, R, Hkv), _int32(new_len, R), dev_status.data_ptr(), _stream(stream))
+    st = _launch(stream, mass, born, block_table, seqused, budget, moves, num_moves, new_len, dev_status, total)
+    rows, heads, max_moves, two = moves.shape
+    assert rows == R and heads == Hkv and two == 2
+    code = load_library().up_kv_evict(_records(mass, torch.float32, shape), _records(born, _I32, shape), num_blocks, Hkv, B,
+                                      _int32(block_table, R * max_blocks), _int32(seqused, R), _int32(budget, R), R, max_blocks,
+                                      _int32(total, R), sinks, recent, _int32(moves, R * Hkv * max_moves * 2), max_moves,
+                                      _int32(num_moves, R * Hkv), _int32(new_len, R), dev_status.data_ptr(), st)
     if code:
         raise UpError(code, "up_kv_evict")
 
@@ -439,11 +450,13 @@ def up_kv_move(k_cache, v_cache, block_table, moves, num_moves, dev_status, k_sc
     """Moves the rows of up_kv_evict's lists, with their records (mass and born, either may be None)."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     R, max_blocks = block_table.shape
-    _here(k_cache, v_cache, block_table, moves, num_moves, dev_status, k_scale, v_scale, mass, born)
-    mp, bp = _records(mass, born, (k_cache.shape[0], cache.Hkv, cache.B))
-    code = load_library().up_kv_move(ctypes.byref(cache), _int32(block_table, R, max_blocks), R, max_blocks,
-                                     _int32(moves, R, cache.Hkv, moves.shape[2], 2), moves.shape[2],
-                                     _int32(num_moves, R, cache.Hkv), mp, bp, dev_status.data_ptr(), _stream(stream))
+    st = _launch(stream, k_cache, v_cache, block_table, moves, num_moves, dev_status, k_scale, v_scale, mass, born)
+    shape = (cache.num_blocks, cache.Hkv, cache.B)
+    rows, heads, max_moves, two = moves.shape
+    assert rows == R and heads == cache.Hkv and two == 2
+    code = load_library().up_kv_move(ctypes.byref(cache), _int32(block_table, R * max_blocks), R, max_blocks,
+                                     _int32(moves, R * heads * max_moves * 2), max_moves, _int32(num_moves, R * heads),
+                                     _records(mass, torch.float32, shape), _records(born, _I32, shape), dev_status.data_ptr(), st)
     if code:
         raise UpError(code, "up_kv_move")
 

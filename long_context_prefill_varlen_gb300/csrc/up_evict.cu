@@ -529,8 +529,6 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
     }
 }
 
-// The CTAs of a list and the keys that they hold.  One CTA has the keys of 32K positions at most in 128 KB; where the lists
-// leave SMs idle, or are longer, a cluster shares one.
 template <int W, bool TEAM>
 static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_t st) {
     static DeviceSet done{0};
@@ -538,8 +536,9 @@ static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_
         return cudaFuncSetAttribute(evict_kernel<W, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
     });
     if (e != cudaSuccess) return e;
-    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d;
-    a.room = static_cast<int>(std::min<int64_t>(cdiv(cap, (int64_t)cluster * 128 * W) * 128 * W, kMostKeys));
+    // the most that a CTA of the cluster gets, of the longest list or of one that is not worth more CTAs
+    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d, most = std::max<int64_t>(cdiv(cap, cluster), std::min<int64_t>(cap, a.part));
+    a.room = static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
     if (!TEAM) return launch_pdl(evict_kernel<W, TEAM>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(lists * cluster));
@@ -560,7 +559,10 @@ static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_
 // ------------------------------------------------------------------------------------------------
 // the moves
 
-constexpr int kMoveThreads = 128, kChunk = 16, kMoveUnroll = 8;
+// Two rows' keys and values in flight a lane, and the registers for eight CTAs an SM, against eight rows of one side: 16
+// requests of 4K-128K in bf16, half of the rows, 268 -> 230 us (6.2 TB/s); four of 128K in e4m3 to 16K 26.8 -> 26.2 (24.7 with
+// sixteen, which takes a fifth longer on rows of 64 numbers).  Half as many CTAs: 243 us.
+constexpr int kMoveThreads = 128, kChunk = 16, kMoveUnroll = 2, kMovePerSm = 64;
 
 struct MoveArgs {
     kv::Cache c;
@@ -635,21 +637,23 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
             if (a.mass && mine && UP_IN(src.record, a.records, a.status)) mass = a.mass[src.record];
             if (a.born && mine && UP_IN(src.record, a.records, a.status)) born = a.born[src.record];
 #pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                uint8_t* const base = side ? a.v : a.k;
+            for (int j0 = 0; j0 < IT; j0 += U) {
+                uint4 x[U], y[U];
 #pragma unroll
-                for (int j0 = 0; j0 < IT; j0 += U) {
-                    uint4 x[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int64_t row = __shfl_sync(0xffffffffu, src.row, (j0 + u) * RPI + grp);
-                        x[u] = make_uint4(0, 0, 0, 0);
-                        if (row >= 0 && UP_IN(row + 16 * sub, a.c.row_limit, a.status)) x[u] = *reinterpret_cast<const uint4*>(base + row + 16 * sub);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = __shfl_sync(0xffffffffu, src.row, (j0 + u) * RPI + grp);
+                    x[u] = y[u] = make_uint4(0, 0, 0, 0);
+                    if (row >= 0 && UP_IN(row + 16 * sub, a.c.row_limit, a.status)) {
+                        x[u] = *reinterpret_cast<const uint4*>(a.k + row + 16 * sub);
+                        y[u] = *reinterpret_cast<const uint4*>(a.v + row + 16 * sub);
                     }
+                }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int64_t row = __shfl_sync(0xffffffffu, dst.row, (j0 + u) * RPI + grp);
-                        if (row >= 0 && UP_IN(row + 16 * sub, a.c.row_limit, a.status)) *reinterpret_cast<uint4*>(base + row + 16 * sub) = x[u];
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = __shfl_sync(0xffffffffu, dst.row, (j0 + u) * RPI + grp);
+                    if (row >= 0 && UP_IN(row + 16 * sub, a.c.row_limit, a.status)) {
+                        *reinterpret_cast<uint4*>(a.k + row + 16 * sub) = x[u];
+                        *reinterpret_cast<uint4*>(a.v + row + 16 * sub) = y[u];
                     }
                 }
             }
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 template <int LPR, bool SCALED>
 static cudaError_t launch_move(const MoveArgs& a, cudaStream_t st) {
     const int64_t y = std::min<int64_t>(a.lists, 65535);
-    const int64_t x = std::min<int64_t>(cdiv(a.max_moves, kChunk * (kMoveThreads / 32)), std::max<int64_t>(1, cdiv(32 * (int64_t)num_sms(), y)));
+    const int64_t x = std::min<int64_t>(cdiv(a.max_moves, kChunk * (kMoveThreads / 32)), std::max<int64_t>(1, cdiv(kMovePerSm * (int64_t)num_sms(), y)));
     return launch_pdl(move_kernel<LPR, SCALED>, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kMoveThreads), 0, st, a);
 }
 
@@ -710,11 +714,18 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     a.status = dev_status;
     const int64_t lists = (int64_t)R * Hkv, cap = (int64_t)max_blocks * B;
     a.quads = B % 4 == 0 && aligned16(mass) && aligned16(born);
+    // A list's CTAs: one where the lists are many; a cluster where they leave SMs idle, or where they are longer than a CTA
+    // holds at two or three on an SM.
     int cluster = 1;
-    a.part = lists > num_sms() ? kMostKeys / 2 : 1024;
-    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part && (lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys)) cluster *= 2;
+    const bool many = lists > num_sms();
+    a.part = many ? kMostKeys / 2 : 1024;
+    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part && (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys)) cluster *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cluster > 1 ? launch_evict<16, true>(a, cluster, lists, st) : launch_evict<16, false>(a, 1, lists, st);
+    // Many short lists (of as many positions as a CTA holds) go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
+    // 27.1 -> 26.1; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.
+    const cudaError_t e = cluster > 1            ? launch_evict<16, true>(a, cluster, lists, st)
+                          : many && cap <= a.part ? launch_evict<8, false>(a, 1, lists, st)
+                                                 : launch_evict<16, false>(a, 1, lists, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();

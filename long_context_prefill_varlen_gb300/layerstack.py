@@ -11,7 +11,8 @@ GEMMs through torch.matmul, PyTorch's varlen flash-attention forward, torch elem
 random weights, so that the time a drop saves on a real layer stack can be measured.  The drop step
 itself (score, top-p select, compaction with its metadata and drop history, Eq. 8 scatter) runs in
 libuniprefill through DropStep, and so do the paged key-value cache that a prefill can fill (StackCache:
-every layer holds the tokens its stream held, Eqs. 16-17) and the attention of the tokens decoded from it.
+every layer holds the tokens its stream held, Eqs. 16-17), the attention of the tokens decoded from it, the eviction
+of cached tokens by the weight that they have had, and rotary positions, where the geometry has a plan for them.
 
 Layer l (pre-norm LLaMA block, GQA, rotary positions):
     x = h + Wo . attn(rope(Wq . rms(h)), rope(Wk . rms(h)), Wv . rms(h))     causal per request
@@ -29,18 +30,20 @@ A drop at layer l_k (the reading of Eqs. 7-10 this module takes):
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
-from . import (up_kv_scale_row, up_kv_write, up_paged_decode, up_paged_decode_workspace_bytes, up_read_status,
-               up_seqused, up_slot_mapping, up_status_string)
+from . import (RopeTable, up_kv_evict, up_kv_mass, up_kv_move, up_kv_scale_row, up_kv_write, up_paged_decode,
+               up_paged_decode_workspace_bytes, up_read_status, up_rope, up_rope_plan, up_seqused, up_slot_mapping,
+               up_status_string)
 from .step import DropStep
 
 
 @dataclass(frozen=True)
 class StackGeometry:
-    """Shape of one decoder layer: hidden size d, query / KV heads, head dim, FFN width."""
+    """Shape of one decoder layer: hidden size d, query / KV heads, head dim, FFN width.  rope: how its heads turn
+    (up_rope_plan), through up_rope; None: whole heads by rope_theta, through torch operations with 32-bit angles."""
     d: int = 4096
     Hq: int = 32
     Hkv: int = 8
@@ -48,9 +51,16 @@ class StackGeometry:
     ffn: int = 14336
     rope_theta: float = 500000.0
     eps: float = 1e-5
+    rope: RopeTable | None = None
 
 
 LLAMA_3_1_8B = StackGeometry()
+
+
+def with_rope(geom, rot=None, **how):
+    """`geom` with a plan for its rotary positions: the first `rot` numbers of a head (all by default), and up_rope_plan's
+    layout and scaling; LLaMA-3.1's are with_rope(LLAMA_3_1_8B, scaling="bands", factor=8.0, original_len=8192)."""
+    return replace(geom, rope=up_rope_plan(rot or geom.dk, **{"theta": geom.rope_theta, **how}))
 
 
 # ------------------------------------------------------------------------------------------ FLOPs accounting
@@ -106,9 +116,13 @@ class StackCache:
 
     A layer's cache positions count the tokens of its own stream: the i-th token that a request has at that
     layer is position i, whatever its rotary position.  A prefill's dropped tokens therefore leave no holes, and
-    the tokens decoded later follow at up_seqused's length (Eq. 17)."""
+    the tokens decoded later follow at up_seqused's length (Eq. 17).
 
-    def __init__(self, L, R, Hkv, dk, max_len, B=16, e4m3=True, device="cuda"):
+    With weigh=True every decode step adds the weights that it gave the cached tokens to their records, and evict() takes
+    the tokens with the least of it out again, of every layer and key head by itself: a layer then has up_seqused's
+    tokens less those that went."""
+
+    def __init__(self, L, R, Hkv, dk, max_len, B=16, e4m3=True, device="cuda", weigh=False):
         dev = torch.device(device)
         self.L, self.R, self.B, self.max_blocks = L, R, B, -(-int(max_len) // B)
         num_blocks = max(1, R * self.max_blocks)
@@ -130,6 +144,12 @@ class StackCache:
         self.status = torch.zeros(1, **i32)
         self.one_each = torch.arange(R + 1, **i32)
         self.ws = None
+        self.weigh, self.weighed = weigh, False
+        if weigh:
+            self.records = [(torch.zeros(num_blocks, Hkv, B, device=dev), torch.zeros(num_blocks, Hkv, B, **i32))
+                            for _ in range(L)]
+            # tokens that went, and tokens whose records are up to date, per layer
+            self.evicted, self.counted = torch.zeros(L, R, **i32), torch.zeros(L, R, **i32)
 
     def fit(self, L, R):
         """Refuse a stack or a batch of another size: the cache's buffers, and the kernels' writes, are L and R long."""
@@ -143,6 +163,10 @@ class StackCache:
         self.drop_layer.zero_()
         self.orig_len.copy_(cu_seqlens.diff())
         self.kv_len.copy_(self.orig_len)
+        self.weighed = False
+        if self.weigh:
+            self.evicted.zero_()
+            self.counted.zero_()
 
     def record_drop(self, step):
         """Take over the drop history row that a DropStep's compaction wrote (section 3.5)."""
@@ -162,20 +186,57 @@ class StackCache:
         up_kv_write(k, v, slots, kc, vc, self.status, **scales)
 
     def seqused(self, layer):
-        """Tokens that each request has at `layer` (Eq. 17), the one being decoded included."""
+        """Tokens that each request has had at `layer` (Eq. 17), the one being decoded included."""
         out = torch.empty_like(self.kv_len)
         up_seqused(self.kept_len, self.drop_layer, layer, self.orig_len, self.kv_len, out)
         return out
 
-    def attend(self, layer, q, seqused, sm_scale):
+    def rows(self, layer, seqused):
+        """Those of them that the cache still holds."""
+        return seqused - self.evicted[layer] if self.weigh else seqused
+
+    def attend(self, layer, q, rows, sm_scale, seqused=None):
+        """Attention of q over the layer's rows; with weigh, their records follow (seqused: Eq. 17's number of tokens)."""
         kc, vc, scales = self.layers[layer]
         R, Hq, dk = q.shape
         nbytes = up_paged_decode_workspace_bytes(R, Hq, kc.shape[1], dk, self.B, self.max_blocks)
         if self.ws is None or self.ws.numel() < nbytes:
             self.ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
         out = torch.empty_like(q)
-        up_paged_decode(q, kc, vc, self.block_table, seqused, out, self.ws, self.status, sm_scale=sm_scale, **scales)
+        lse = torch.empty(R, Hq, device=q.device) if self.weigh else None
+        up_paged_decode(q, kc, vc, self.block_table, rows, out, self.ws, self.status, sm_scale=sm_scale, lse=lse, **scales)
+        if self.weigh:
+            mass, born = self.records[layer]
+            up_kv_mass(q, kc, vc, self.block_table, rows, lse, mass, born, self.status, sm_scale=sm_scale,
+                       counted=self.counted[layer], total=seqused, **scales)
+            self.counted[layer].copy_(rows)
         return out
+
+    def evict(self, budget, sinks=0, recent=0):
+        """Leave each request at most `budget` tokens (a number, or int32 [R]) at every layer and key head: its first
+        `sinks` and last `recent` before the others, those by their weight.  Between decode steps; the host does not wait."""
+        if not self.weigh:
+            raise ValueError("evict() needs a cache that weighs its tokens (weigh=True)")
+        if not self.weighed:
+            raise ValueError("no token has been decoded since the prefill: the cached tokens have no weights yet")
+        dev, cap = self.kv_len.device, self.max_blocks * self.B
+        if isinstance(budget, int):
+            if budget < 0:
+                raise ValueError(f"a budget of {budget} tokens")
+            most, budget = min(budget, cap // 2), torch.full((self.R,), budget, device=dev, dtype=torch.int32)
+        else:
+            most = cap // 2                        # as many move as there are holes: never more than half
+        Hkv = self.layers[0][0].shape[1]
+        moves = torch.empty(self.R, Hkv, max(1, most), 2, device=dev, dtype=torch.int32)
+        num = torch.empty(self.R, Hkv, device=dev, dtype=torch.int32)
+        for layer, ((kc, vc, scales), (mass, born)) in enumerate(zip(self.layers, self.records)):
+            seqused = self.seqused(layer)
+            left = torch.empty_like(seqused)
+            up_kv_evict(mass, born, self.block_table, self.rows(layer, seqused), budget, moves, num, left, self.status,
+                        total=seqused, sinks=sinks, recent=recent)
+            up_kv_move(kc, vc, self.block_table, moves, num, self.status, mass=mass, born=born, **scales)
+            self.evicted[layer].copy_(seqused - left)
+            self.counted[layer].copy_(left)
 
     def check(self, stream=None):
         code = up_read_status(self.status, stream)
@@ -221,6 +282,7 @@ class RandomLlamaStack:
     def __init__(self, L, geom: StackGeometry = LLAMA_3_1_8B, seed=0, device="cuda", init_device=None):
         self.L, self.g = L, geom
         self.device = torch.device(device)
+        self.status = torch.zeros(1, device=self.device, dtype=torch.int32)        # of up_rope
         init_device = torch.device(init_device) if init_device is not None else self.device
         gen = torch.Generator(device=init_device)
         gen.manual_seed(seed)
@@ -242,6 +304,10 @@ class RandomLlamaStack:
         g, Wt = self.g, self.layers[layer]
         T = h.shape[0]
         a = _rms(h, g.eps)
+        if g.rope is not None:
+            q, k, v = (torch.matmul(a, Wt[w]).view(T, n, g.dk) for w, n in (("wq", g.Hq), ("wk", g.Hkv), ("wv", g.Hkv)))
+            up_rope(g.rope, positions, self.status, q=q, q_out=q, k=k, k_out=k)
+            return q, k, v
         cos, sin = rope_tables(positions, g.dk, g.rope_theta)
         q = apply_rope(torch.matmul(a, Wt["wq"]).view(T, g.Hq, g.dk), cos, sin)
         k = apply_rope(torch.matmul(a, Wt["wk"]).view(T, g.Hkv, g.dk), cos, sin)
@@ -325,8 +391,8 @@ class RandomLlamaStack:
 
     def decode(self, hidden, positions, cache):
         """One new token per request through all layers: hidden [R, d] bf16, positions [R] int64 (rotary: the
-        tokens the request has had so far, dropped ones included).  Each layer appends the token's key and value to
-        its part of the cache and attends over the tokens it holds.  Returns the token's output [R, d].  The host does not
+        tokens the request has had so far, dropped ones and evicted ones included).  Each layer appends the token's key and
+        value to its part of the cache and attends over the tokens it holds.  Returns the token's output [R, d].  The host does not
         wait: cache.check() tells of a request that has outgrown the cache, whose output is then none."""
         g = self.g
         R = hidden.shape[0]
@@ -338,10 +404,12 @@ class RandomLlamaStack:
         for layer in range(self.L):
             q, k, v = self.qkv(layer, h, positions)
             seq = cache.seqused(layer)
+            rows = cache.rows(layer, seq)
             slot = torch.empty(R, device=h.device, dtype=torch.int64)
-            up_slot_mapping(seq.long() - 1, cache.one_each, cache.block_table, cache.B, slot, cache.status)
+            up_slot_mapping(rows.long() - 1, cache.one_each, cache.block_table, cache.B, slot, cache.status)
             cache.write(layer, k, v, slot)
-            o = cache.attend(layer, q, seq, g.dk ** -0.5)
+            o = cache.attend(layer, q, rows, g.dk ** -0.5, seq)
             x = h + torch.matmul(o.view(R, g.Hq * g.dk), self.layers[layer]["wo"])
             h = self.ffn_sublayer(layer, x)
+        cache.weighed = True
         return h

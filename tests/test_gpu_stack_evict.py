@@ -1,0 +1,148 @@
+"""Eviction and planned rotary positions inside the random-weight decoder stack (GPU).
+
+Each decode step is checked against a float64 CPU recomputation that attends over what the cache holds (read back head by
+head through up_kv_read), with the stack tests' tolerances; a budget that takes nothing out changes no bit; a layer's stream and
+the sinks stay what they are however often tokens go."""
+import numpy as np
+import pytest
+import torch
+
+from long_context_prefill_varlen_gb300 import layerstack as ls
+from synth import cpu as gen
+from synth import gpu as sgpu
+from synth import recipe
+from tests import evict_ref, kv_ref, stack_ref
+from tests.test_gpu_generate import A, G, GEOM, L, LENGTHS, REL_FRO, REL_ROW, _read, _ref_decode, n
+from tests.test_gpu_kvcache import _bits
+from tests.test_gpu_rope import _turns
+
+pytestmark = pytest.mark.gpu
+
+
+def _prefill(e4m3, drops, weigh, geom=GEOM, lengths=LENGTHS):
+    w = recipe.small(lengths=lengths, Hq=geom.Hq, Hkv=geom.Hkv, dk=geom.dk, hdim=geom.d, G=G, n=n, A=A, salt=257)
+    d = sgpu.to_device(gen.materialize(w))
+    stack = ls.RandomLlamaStack(L, geom, seed=11, device="cuda", init_device="cpu")
+    cache = ls.StackCache(L, len(lengths), geom.Hkv, geom.dk, max(lengths) + 8, e4m3=e4m3, weigh=weigh)
+    out, info = stack.forward(d["hidden"], d["positions"], d["cu_seqlens"], max(lengths), drops=drops, G=G, n=n, A=A, cache=cache)
+    return stack, cache, out, info
+
+
+def _steps(seed, count, lengths=LENGTHS):
+    rng = np.random.default_rng(seed)
+    for i in range(count):
+        hidden = torch.from_numpy(rng.standard_normal((len(lengths), GEOM.d)).astype(np.float32)).cuda().to(torch.bfloat16)
+        yield hidden, torch.tensor(lengths, device="cuda") + i
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("drops", [[], [(1, 0.8)]], ids=["none", "one"])
+def test_decoding_from_a_cache_that_rows_leave(drops, e4m3):
+    stack, cache, _, _ = _prefill(e4m3, drops, True)
+    R, sinks, recent = len(LENGTHS), 4, 16
+    budgets = [None, 600, None, torch.tensor([500, 40, 3, 700, 0], dtype=torch.int32, device="cuda"), 20]
+    held = [cache.seqused(layer).cpu().numpy().astype(int) for layer in range(L)]
+    had = [x.copy() for x in held]
+    for step, (hidden, pos) in enumerate(_steps(3, len(budgets))):
+        got = stack.decode(hidden, pos, cache).double().cpu()
+        cache.check()
+        for layer in range(L):
+            held[layer] += 1
+            had[layer] += 1
+            assert np.array_equal(cache.rows(layer, cache.seqused(layer)).cpu().numpy(), held[layer])
+        ref = _ref_decode(stack, hidden, pos.cpu(), [_read(cache, layer, list(held[layer])) for layer in range(L)])
+        fro = float(torch.linalg.norm(got - ref) / torch.linalg.norm(ref))
+        rows = (torch.linalg.norm(got - ref, dim=1) / torch.linalg.norm(ref, dim=1)).max()
+        assert fro < REL_FRO and float(rows) < REL_ROW, (step, fro, float(rows))
+        for layer in range(L):
+            mass, born = (x.cpu().numpy() for x in cache.records[layer])
+            for r in range(R):
+                p = np.arange(held[layer][r])
+                page = cache.block_table[r].cpu().numpy()[p // cache.B]
+                b, m = born[page, :, p % cache.B], mass[page, :, p % cache.B]
+                assert all(len(set(b[:, h])) == len(p) for h in range(GEOM.Hkv)) and (b < had[layer][r]).all()
+                assert np.isfinite(m).all() and (m >= 0).all()
+                if step == 0:                      # a head's weights add up to its query heads, to the weights' own error
+                    assert np.array_equal(b, np.tile(p[:, None], (1, GEOM.Hkv)))
+                    assert np.allclose(m.sum(0), GEOM.Hq // GEOM.Hkv, rtol=1e-4)
+        if budgets[step] is not None:
+            cache.evict(budgets[step], sinks=sinks, recent=recent)
+            cache.check()
+            k = np.full(R, budgets[step]) if isinstance(budgets[step], int) else budgets[step].cpu().numpy()
+            for layer in range(L):
+                held[layer] = np.minimum(held[layer], k)
+                born = cache.records[layer][1].cpu().numpy()
+                for r in range(R):
+                    p = np.arange(held[layer][r])
+                    b = born[cache.block_table[r].cpu().numpy()[p // cache.B], :, p % cache.B]
+                    for h in range(GEOM.Hkv):
+                        if len(p) >= sinks + recent:
+                            t = had[layer][r]
+                            assert set(range(min(sinks, t))) | set(range(max(0, t - recent), t)) <= set(b[:, h].tolist())
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_weighing_alone_and_a_large_budget_change_nothing(e4m3):
+    outs = []
+    for weigh in (False, True):
+        stack, cache, _, _ = _prefill(e4m3, [(1, 0.8)], weigh)
+        got = []
+        for hidden, pos in _steps(5, 3):
+            got.append(stack.decode(hidden, pos, cache))
+            if weigh:
+                cache.evict(10_000, sinks=4, recent=4)
+        cache.check()
+        outs.append((got, cache))
+    for x, y in zip(outs[0][0], outs[1][0]):
+        assert torch.equal(x, y)
+    for (k0, v0, _), (k1, v1, _) in zip(outs[0][1].layers, outs[1][1].layers):
+        assert torch.equal(k0.view(torch.uint8), k1.view(torch.uint8)) and torch.equal(v0.view(torch.uint8), v1.view(torch.uint8))
+
+
+def test_a_new_prefill_forgets_what_was_evicted():
+    stack, cache, _, _ = _prefill(True, [], True)
+    for hidden, pos in _steps(6, 2):
+        stack.decode(hidden, pos, cache)
+        cache.evict(50)
+    w = recipe.small(lengths=LENGTHS, Hq=GEOM.Hq, Hkv=GEOM.Hkv, dk=GEOM.dk, hdim=GEOM.d, G=G, n=n, A=A, salt=257)
+    d = sgpu.to_device(gen.materialize(w))
+    stack.forward(d["hidden"], d["positions"], d["cu_seqlens"], max(LENGTHS), cache=cache)
+    with pytest.raises(ValueError, match="weights"):
+        cache.evict(50)
+    fresh = _prefill(True, [], True)[1]
+    for hidden, pos in _steps(7, 2):
+        a, b = stack.decode(hidden, pos, cache), stack.decode(hidden, pos, fresh)
+        assert torch.equal(a, b)
+    for layer in range(L):
+        rows = cache.rows(layer, cache.seqused(layer)).cpu().numpy()
+        for r in range(len(LENGTHS)):
+            p = np.arange(rows[r])
+            page = cache.block_table[r].cpu().numpy()[p // cache.B]
+            for x, y in zip(cache.records[layer], fresh.records[layer]):
+                assert np.array_equal(x.cpu().numpy()[page, :, p % cache.B], y.cpu().numpy()[page, :, p % cache.B])
+
+
+@pytest.mark.parametrize("how", [dict(), dict(layout="pairs", rot=32), dict(scaling="bands", factor=8.0, original_len=512)],
+                         ids=["plain", "pairs_of_a_part", "bands"])
+def test_the_stacks_planned_positions(how):
+    """q and k of a layer are the projections turned by the plan; without scaling, the stack gives what 32-bit angles give, to the
+    stack tests' tolerances"""
+    geom = ls.with_rope(GEOM, **how)
+    stack = ls.RandomLlamaStack(L, geom, seed=11, device="cuda", init_device="cpu")
+    base = ls.RandomLlamaStack(L, ls.with_rope(GEOM), seed=11, device="cuda", init_device="cpu")
+    w = recipe.small(lengths=LENGTHS, Hq=GEOM.Hq, Hkv=GEOM.Hkv, dk=GEOM.dk, hdim=GEOM.d, G=G, n=n, A=A, salt=257)
+    host = gen.materialize(w)
+    d = sgpu.to_device(host)
+    q0, k0, v0 = base.qkv(0, d["hidden"], torch.zeros_like(d["positions"]))        # position 0 turns nothing
+    q, k, v = stack.qkv(0, d["hidden"], d["positions"])
+    assert torch.equal(v, v0)
+    turns = _turns(geom.rope, d["positions"].tolist())
+    for x, x0 in ((q, q0), (k, k0)):
+        y, tol = evict_ref.turned(kv_ref.bf16_value(_bits(x0)), turns, geom.rope.gain, how.get("layout", "halves"))
+        assert (np.abs(kv_ref.bf16_value(_bits(x)) - y) <= tol).all()
+    if not how:
+        out, _ = stack.forward(d["hidden"], d["positions"], d["cu_seqlens"], max(LENGTHS))
+        hidden = torch.from_numpy(gen.bf16_bits_to_f32(host["hidden"]).astype(np.float64))
+        ref = stack_ref.forward(stack, hidden, host["positions"], LENGTHS)
+        got = out.double().cpu()
+        assert float(torch.linalg.norm(got - ref) / torch.linalg.norm(ref)) < REL_FRO

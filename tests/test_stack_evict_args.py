@@ -1,0 +1,41 @@
+"""What a StackCache refuses of an eviction, on the host and before any work (no GPU needed)."""
+import pytest
+import torch
+
+from long_context_prefill_varlen_gb300 import layerstack as ls
+
+
+def _cache(weigh):
+    return ls.StackCache(3, 2, 1, 64, 16, device="cpu", weigh=weigh)
+
+
+def test_a_cache_without_records_and_one_without_weights():
+    with pytest.raises(ValueError, match="weigh"):
+        _cache(False).evict(4)
+    with pytest.raises(ValueError, match="weights"):
+        _cache(True).evict(4)
+    cache = _cache(True)
+    cache.weighed = True
+    with pytest.raises(ValueError, match="budget"):
+        cache.evict(-1)
+    cache.start(torch.tensor([0, 3, 7], dtype=torch.int32))
+    with pytest.raises(ValueError, match="weights"):
+        cache.evict(4)
+
+
+def test_a_cache_without_records_holds_all_that_its_layers_had():
+    n = torch.tensor([3, 4], dtype=torch.int32)
+    assert _cache(False).rows(1, n) is n
+    cache = _cache(True)
+    cache.evicted[1] = torch.tensor([1, 0], dtype=torch.int32)
+    assert cache.rows(1, n).tolist() == [2, 4] and cache.rows(0, n).tolist() == [3, 4]
+    cache.start(torch.tensor([0, 3, 7], dtype=torch.int32))
+    assert cache.rows(1, n).tolist() == [3, 4]
+
+
+def test_a_geometry_with_a_plan():
+    from long_context_prefill_varlen_gb300 import _build
+    _build.build()
+    geom = ls.with_rope(ls.LLAMA_3_1_8B, scaling="bands", factor=8.0, original_len=8192)
+    assert (geom.rope.rot, geom.rope.layout, geom.rope.gain) == (128, 0, 1.0) and ls.LLAMA_3_1_8B.rope is None
+    assert geom.d == ls.LLAMA_3_1_8B.d and ls.with_rope(geom, rot=32, layout="pairs").rope.rot == 32
