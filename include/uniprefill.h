@@ -385,7 +385,7 @@ up_status up_rope(const up_rope_table* plan, const uint16_t* q, int64_t q_stride
  *   mass_out = decay * mass + sum_{h of the key head} exp(q[r, h] . K_i * sm_scale - lse[r, h])   for i in [0, seqused[r]).
  * Rows at positions i >= counted[r] (int32 [R], optional: NULL means that every row has been counted before) are new: they
  * start from 0, whatever mass holds, and get born = total[r] - seqused[r] + i, total[r] (int32 [R], optional; NULL means
- * seqused) being the tokens that the layer's stream has had.  A head with lse = -inf adds nothing.  mass_out may be mass; apart
+ * seqused) being the tokens that the layer's stream has had.  A head whose lse is infinite adds nothing.  mass_out may be mass; apart
  * from that they do not overlap.  Records at other positions are left alone.
  * decay in [0, 1].  A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a row whose table
  * entry lies outside [0, num_blocks) sets UP_DEV_BAD_PAGE and has no record.
@@ -402,7 +402,8 @@ up_status up_kv_mass(const uint16_t* q, int64_t q_stride, const up_kv_cache* cac
  * Positions [0, k) hold the rows that stay once the ones at or beyond k have moved into the holes below it:
  *   moves[(r * Hkv + h) * max_moves + i] = (position from, position to), both ascending in i < num_moves[r * Hkv + h];
  *   new_len[r] = k.
- * moves: int32 [R, Hkv, max_moves, 2] (entries past num_moves are left alone), 8-byte aligned; num_moves: int32 [R, Hkv];
+ * moves: int32 [R, Hkv, max_moves, 2] (entries past num_moves are left alone), 8-byte aligned, NULL where max_moves = 0;
+ * num_moves: int32 [R, Hkv];
  * new_len, budget, seqused: int32 [R].  budget, seqused and total are not written and new_len must not be one of them.
  * A request is left as it is (no moves, new_len = its length) where min(k, len - k) > max_moves
  * (UP_DEV_TOO_MANY_MOVES), budget[r] < 0 (UP_DEV_BAD_BUDGET) or a table entry in use lies outside [0, num_blocks)

@@ -686,9 +686,9 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
                                  int max_blocks, const int32_t* total, int sinks, int recent, int32_t* moves,
                                  int64_t max_moves, int32_t* num_moves, int32_t* new_len, int32_t* dev_status, void* stream) {
     using namespace up::evict;
-    if (!mass || !born || !block_table || !seqused || !budget || !moves || !num_moves || !new_len || !dev_status) return UP_ERR_ARG;
+    if (!mass || !born || !block_table || !seqused || !budget || !num_moves || !new_len || !dev_status) return UP_ERR_ARG;
     if (R <= 0 || Hkv <= 0 || max_blocks <= 0 || B <= 0 || B > (1 << 20) || num_blocks <= 0 || num_blocks > 0x7fffffff) return UP_ERR_ARG;
-    if (sinks < 0 || recent < 0 || max_moves < 0) return UP_ERR_ARG;
+    if (sinks < 0 || recent < 0 || max_moves < 0 || (max_moves > 0 && !moves)) return UP_ERR_ARG;
     if (new_len == seqused || new_len == budget || new_len == total) return UP_ERR_ARG;      // other heads' CTAs still read those
     if (!fits(R, Hkv, max_blocks, B) || reinterpret_cast<uintptr_t>(moves) % 8) return UP_ERR_SHAPE;
     Args a{};
@@ -736,7 +736,7 @@ extern "C" up_status up_kv_move(const up_kv_cache* cache, const int32_t* block_t
                                 int32_t* born, int32_t* dev_status, void* stream) {
     using namespace up::evict;
     MoveArgs a{};
-    if (!block_table || !moves || !num_moves || !dev_status) return UP_ERR_ARG;
+    if (!block_table || !num_moves || !dev_status || (max_moves > 0 && !moves)) return UP_ERR_ARG;
     const up_status s = kv::check(cache, &a.c);
     if (s != UP_OK) return s;
     if (R <= 0 || max_blocks <= 0 || max_moves < 0) return UP_ERR_ARG;

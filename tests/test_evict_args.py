@@ -9,6 +9,7 @@ import torch
 
 from tests import evict_ref
 from tests.test_kvcache_args import A, BAD_CACHES, ODD, _cache, up  # noqa: F401
+from tests.test_launch_host import lib  # noqa: F401
 
 
 # ------------------------------------------------------------------------------------------ the plan
@@ -142,7 +143,7 @@ def test_what_move_refuses(up):
         assert call(**bad) == up.UP_ERR_ARG, bad
     for bad in (dict(max_blocks=(1 << 26) + 1), dict(R=1 << 24), dict(moves=A + 4)):
         assert call(**bad) == up.UP_ERR_SHAPE, bad
-    assert call(max_moves=0) == up.UP_OK                             # room for no move: none
+    assert call(max_moves=0) == up.UP_OK and call(max_moves=0, moves=None) == up.UP_OK       # room for no move: none
 
 
 def test_the_status_strings(up):
@@ -188,3 +189,40 @@ def test_the_reference_choice():
     assert evict_ref.evict(mass, born, 7, 5, 0, 0) == [(6, 2)]                   # and of the equal ones row 1
     assert evict_ref.evict(mass, born, 7, 3, 2, 2) == [(6, 2)]                   # rows 0, 1, 5, 6 protected, by mass, then position
     assert evict_ref.evict(mass, born, 7, 7, 0, 0) == [] and evict_ref.evict(mass, born, 7, 0, 3, 3) == []
+
+
+# ------------------------------------------------------------------------------------------ launches
+
+def _calls(m, up):
+    """every kernel's form of the calls, on sizes that want them"""
+    plan = up.RopeTable()
+    assert m.up_rope_plan(64, 10000.0, 0, 0, 1.0, 0, 0, 0, 0, ctypes.byref(plan)) == 0
+    for dk in (64, 128, 256):
+        for layout in (0, 1):
+            plan.layout = layout
+            yield lambda dk=dk: m.up_rope(ctypes.byref(plan), A, 4 * dk, A, 4 * dk, 4, None, 0, None, 0, 0, dk, A, 100, None, 0, A, None)
+        for e4m3 in (0, 1):
+            for B in (16, 24):
+                cache = up._KvCache(A, A, A, A, 8, 2 * B * dk, B * dk, dk, 2, B, dk, e4m3)
+                for Hq in (4, 40):
+                    yield lambda cache=cache, Hq=Hq, dk=dk: m.up_kv_mass(A, Hq * dk, ctypes.byref(cache), A, A, A, 2, 4, Hq, 0.1, None, None, 1.0,
+                                                                         A, A, A, A, None)
+            yield lambda cache=cache: m.up_kv_move(ctypes.byref(cache), A, 2, 4, A, 10, A, None, None, A, None)
+    for R, max_blocks in ((1, 4), (1, 60000), (300, 4), (300, 2000), (60, 1500)):
+        yield lambda R=R, max_blocks=max_blocks: m.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None)
+
+
+def test_every_call_launches_on_every_device_and_an_error_is_its_own(lib, up):
+    for device in (40, 41):
+        for call in _calls(lib, up):
+            lib.fake_reset(device, 16)
+            assert call() == 0 and lib.fake_launches() == 1
+            lib.fake_fail(0, 1)
+            assert call() == 4 and call() == 0
+
+
+def test_a_list_goes_to_a_cluster_where_it_is_worth_one(lib, up):
+    for R, max_blocks, cluster in ((1, 4, 1), (1, 60000, 8), (300, 4, 1), (300, 2000, 2), (300, 60000, 8), (30, 1000, 2)):
+        lib.fake_reset(42, 8)
+        assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
+        assert lib.fake_launch_cluster(0) == cluster, (R, max_blocks)

@@ -244,8 +244,38 @@ def test_the_choice_in_clusters_of_every_size(R, n, Hkv):
     _check_choice(R, lens, [int(x * rng.random()) for x in lens], Hkv, 16, sinks=4, recent=10)
 
 
+@pytest.mark.parametrize("name", ["equal", "few_values", "last_bits", "zeros"])
+def test_ties_of_lists_that_have_a_cta_each(name):
+    """more keys with one first digit than the candidates' place holds, without a cluster"""
+    _check_choice(7, (6000,) + (30,) * 99, (2500,) + (10,) * 99, values=EDGES[name], sinks=3, recent=20)
+    _check_choice(8, (6000, 3000), (5999, 100), Hkv=80, values=EDGES[name])
+
+
+def test_records_that_are_not_aligned():
+    rng = np.random.default_rng(9)
+    lens, budget = (700, 5, 2000), (300, 2, 1990)
+    table, nb = _tables(rng, lens, 16)
+    mass, born = torch.rand(nb, 2, 16, device="cuda"), torch.randint(0, 3000, (nb, 2, 16), device="cuda", dtype=torch.int32)
+    want = _choose(mass, born, table, lens, budget, sinks=9, recent=3)
+    odd = [torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape) for x in (mass, born)]
+    for o, x in zip(odd, (mass, born)):
+        o.copy_(x)
+    for m, b in ((odd[0], born), (mass, odd[1]), odd):
+        got = _choose(m, b, table, lens, budget, sinks=9, recent=3)
+        assert got[0] == want[0] == 0 and all(torch.equal(x, y) for x, y in zip(got[1:], want[1:]))
+
+
+def test_room_for_no_moves():
+    mass, born = torch.rand(3, 1, 16, device="cuda"), torch.zeros(3, 1, 16, dtype=torch.int32, device="cuda")
+    table = np.array([[0, 1, 2]], dtype=np.int32)
+    status, _, num, new_len = _choose(mass, born, table, (40,), (50,), max_moves=0)
+    assert status == 0 and int(num) == 0 and int(new_len) == 40
+    status, _, num, new_len = _choose(mass, born, table, (40,), (30,), max_moves=0)
+    assert status == 12 and int(num) == 0 and int(new_len) == 40
+
+
 def test_a_list_longer_than_shared_memory():
-    for n, k in ((500_001, 20_000), (500_001, 499_990)):
+    for n, k, sinks in ((500_001, 20_000, 100), (500_001, 499_990, 100), (500_001, 50, 400_000)):
         rng = np.random.default_rng(k)
         mass = np.exp(2 * rng.standard_normal(n)).astype(np.float32)
         mass[rng.random(n) < 0.3] = 0
@@ -258,11 +288,11 @@ def test_a_list_longer_than_shared_memory():
             p = torch.arange(n, device="cuda")
             page = torch.from_numpy(table[0]).cuda().long()[p // 64]
             md[page, 0, p % 64], bd[page, 0, p % 64] = torch.from_numpy(mass).cuda(), torch.from_numpy(born).cuda()
-            status, moves, num, new_len = _choose(md, bd, table, lens, budget, sinks=100, recent=1000)
+            status, moves, num, new_len = _choose(md, bd, table, lens, budget, sinks=sinks, recent=1000)
             assert status == 0 and int(new_len[0]) == k and (num[1:] == 0).all()
-            key = np.where((born < 100) | (born >= n - 1000), np.inf, mass)
+            safe = (born < sinks) | (born >= n - 1000)
             stay = np.zeros(n, dtype=bool)
-            stay[np.lexsort((np.arange(n), -key))[:k]] = True
+            stay[np.lexsort((np.arange(n), -mass, ~safe))[:k]] = True
             want = np.stack((np.flatnonzero(stay[k:]) + k, np.flatnonzero(~stay[:k])), 1)
             assert int(num[0, 0]) == len(want) and np.array_equal(moves[0, 0, :len(want)].cpu().numpy(), want)
 
