@@ -721,11 +721,12 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     a.part = many ? kMostKeys / 2 : 1024;
     while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part && (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys)) cluster *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Many short lists (of as many positions as a CTA holds) go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
-    // 27.1 -> 26.1; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.
-    const cudaError_t e = cluster > 1            ? launch_evict<16, true>(a, cluster, lists, st)
-                          : many && cap <= a.part ? launch_evict<8, false>(a, 1, lists, st)
-                                                 : launch_evict<16, false>(a, 1, lists, st);
+    // Many short lists go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
+    // 27.1 -> 26.2; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.  Few lists with much for
+    // each CTA of a cluster take all that an SM has: 4 of 128K on 2 heads 26.1 -> 25.0, one of a million on one 229 -> 169.
+    const cudaError_t e = cluster == 1 ? many && cap <= a.part ? launch_evict<8, false>(a, 1, lists, st) : launch_evict<16, false>(a, 1, lists, st)
+                          : !many && cap > (int64_t)cluster * 8192 ? launch_evict<32, true>(a, cluster, lists, st)
+                                                                   : launch_evict<16, true>(a, cluster, lists, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();

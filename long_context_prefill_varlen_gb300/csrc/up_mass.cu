@@ -10,6 +10,12 @@
 // own in shared memory (copies that need no registers and no other warp).  Lane 4g + t copies, and reads back, 16-byte pieces
 // t, t + 4, ... of rows g and g + 8: they are the products' first operand as they come if the queries' columns are taken in
 // the same order (a sum over columns does not care), in m16n8k16 with keys in the 16 rows and query heads in the 8 columns.
+// Beyond 8 query heads a key head the share is a CTA's, whose warps take a tile each and have the queries in common.
+//
+// Measured (one GB300, 6.79 TB/s measured copy): 16 requests of 4K-128K, 8 heads of 128 in bf16, 225 us, 6.4 TB/s; 64 of 0-8K, 8
+// heads of 128 in e4m3, 58 us, 5.3 TB/s; 32 of up to 16K, 8 heads of 256 in bf16 112 us (6.2), in e4m3 63 us (5.6); 32 of up to
+// 32K, 32 query heads on one of 128 in bf16, 22 us (3.9; the heads' exponentials are four times the work per byte).  One
+// request of 4K takes 4.6 us, a chain of latencies (its length, its pages, the copies).
 #include <stdint.h>
 
 #include <algorithm>
@@ -55,9 +61,10 @@ struct Shape {
     // Two tiles in flight a warp and five CTAs an SM (20 warps of 96 registers) against three tiles: 64 requests of 0-8K in
     // e4m3 58 / 59 us, 32 of up to 16K on heads of 256 63 / 77; against six CTAs (80 registers, spills): 58 / 62.
     static constexpr int kStages = 2;
-    static constexpr int kBlock = DK == 256 ? 2 : 4;                   // tiles of 8 query heads that a warp keeps in shared memory
+    static constexpr int kBlock = 4;                                   // tiles of 8 query heads that a CTA keeps in shared memory
     static constexpr int kTile = (DK / 8 + 8) * 128;                   // bytes of such a tile: the lanes' operands and factors
-    static constexpr int kSmem = kWarps * (kStages * kStage + (MANY ? kBlock * kTile : 0));
+    static constexpr int kRings = kWarps * kStages * kStage;
+    static constexpr int kSmem = kRings + (MANY ? kBlock * kTile : 0);
     static constexpr int kFit = 224 * 1024 / (kSmem + 1024);
     static constexpr int kMost = DK == 256 ? 4 : 5;
     static constexpr int kCtas = kFit < kMost ? kFit : kMost;
@@ -132,7 +139,7 @@ struct Queries {
             lo[x] = a.scale_lo * back[x];
         }
     }
-    // to and from a warp's place in shared memory
+    // to and from a place in shared memory
     __device__ __forceinline__ void put(uint8_t* at) const {
         uint32_t w[4 * V];
 #pragma unroll
@@ -163,16 +170,18 @@ struct Queries {
     }
 };
 
-// A warp's run of units (tiles of rows): of all requests' units in the order request, head, rows, its equal share.
+// A run of units: of all requests' units in the order request, head, rows, an equal share.  A unit is a tile of rows and the run
+// a warp's, or with many query heads a tile for every warp of a CTA, which share the queries.
+template <int UNIT>
 struct Walk {
     int r, head, unit, units;      // units: of the request's head
     int len, from;                 // rows of the request; the first new one
     int left;                      // units of the run still to come
 
     __device__ __forceinline__ int units_of(const Args& a, int n) const {
-        return n < 0 || n > (int64_t)a.max_blocks * static_cast<int64_t>(a.by_b.d) ? 0 : (n + kRows - 1) / kRows;
+        return n < 0 || n > (int64_t)a.max_blocks * static_cast<int64_t>(a.by_b.d) ? 0 : (n + UNIT - 1) / UNIT;
     }
-    __device__ __forceinline__ void seek(const Args& a, int64_t warp, int64_t warps) {
+    __device__ __forceinline__ void seek(const Args& a, int64_t run, int64_t runs) {
         const int lane = threadIdx.x & 31;
         left = 0;
         int n = 0, mine = 0, upto = 0;
@@ -195,13 +204,13 @@ struct Walk {
         all *= a.c.Hkv;
         int64_t first;
         if (all == 0) return;
-        if (all <= warps) {                            // few units: one each, to warps that lie evenly over the grid
-            const int64_t per = warps / all;
-            first = warp % per == 0 && warp / per < all ? warp / per : all;
+        if (all <= runs) {                             // few units: one each, to runs that lie evenly over the grid
+            const int64_t per = runs / all;
+            first = run % per == 0 && run / per < all ? run / per : all;
             left = first < all ? 1 : 0;
         } else {
-            first = all * warp / warps;
-            left = static_cast<int>(all * (warp + 1) / warps - first);
+            first = all * run / runs;
+            left = static_cast<int>(all * (run + 1) / runs - first);
         }
         if (left == 0) return;
         int64_t before = 0;
@@ -252,35 +261,40 @@ __device__ __forceinline__ void wait_groups() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Where the tiles ahead lie, found by the lanes side by side: a tile of 16 rows lies in one page (WHOLE, pages of a
+// Where a warp's tiles ahead lie, found by the lanes side by side: a tile of 16 rows lies in one page (WHOLE, pages of a
 // multiple of 16), and a lane finds a tile's; or each row has its own, and a lane finds a row's.  The table's entries are
 // read a batch ahead.
-template <bool WHOLE>
+template <int UNIT, bool WHOLE>
 struct Batch {
     static constexpr int kTiles = WHOLE ? 32 : 2;
-    Walk next;                 // the batch after this one
+    int sub;                   // the warp's first row in a unit
+    Walk<UNIT> next;           // the batch after this one
     int next_n, page;
     int n, i, p0;              // tiles of this one, those used, and its first row
     int len, from;             // rows of its request, and those whose mass counts
     int64_t row, rec, sc;      // of the lane's tile (row): bytes, record, scale byte
     uint32_t valid;            // bit i: lane i's tile (row) has a record
 
+    static __device__ __forceinline__ int offset() {
+        const int lane = threadIdx.x & 31;
+        return WHOLE ? lane * UNIT : lane / kRows * UNIT + lane % kRows;
+    }
     __device__ __forceinline__ void look(const Args& a) {
         const int lane = threadIdx.x & 31;
         next_n = next.left > 0 ? min(kTiles, min(next.units - next.unit, next.left)) : 0;
-        const int pos = next.unit * kRows + (WHOLE ? lane * kRows : lane);
+        const int pos = next.unit * UNIT + sub + offset();
         const int64_t e = (int64_t)next.r * a.max_blocks + div_of(pos, a.by_b);
-        page = (WHOLE ? lane < next_n : lane < kRows * next_n && pos < next.len) && UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
+        page = (WHOLE ? lane < next_n : lane < kRows * next_n) && pos < next.len && UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
     }
     __device__ __forceinline__ void turn(const Args& a) {
         const int lane = threadIdx.x & 31;
         n = next_n;
         i = 0;
-        p0 = next.unit * kRows, len = next.len, from = a.decay != 0.f ? next.from : 0;
+        p0 = next.unit * UNIT + sub, len = next.len, from = a.decay != 0.f ? next.from : 0;
         if (n == 0) return;
-        const int pos = p0 + (WHOLE ? lane * kRows : lane);
+        const int pos = p0 + offset();
         const int tok = pos - static_cast<int>(div_of(pos, a.by_b) * a.by_b.d);
-        const bool wanted = WHOLE ? lane < n : lane < kRows * n && pos < len, in = page >= 0 && page < a.c.num_blocks;
+        const bool wanted = (WHOLE ? lane < n : lane < kRows * n) && pos < len, in = page >= 0 && page < a.c.num_blocks;
         if (wanted && !in) set_status(a.status, UP_DEV_BAD_PAGE);
         // what is nowhere copies rows that are there, and leaves no record
         const int64_t pg = wanted && in ? page : 0, ph = pg * a.c.Hkv + next.head;
@@ -296,26 +310,28 @@ struct Batch {
 template <int DK, bool E4M3, bool MANY, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass_kernel(const __grid_constant__ Args a) {
     using S = Shape<DK, E4M3, MANY>;
-    constexpr int NP = S::kPieces, NS = S::kStages, NB = S::kBlock;
+    constexpr int NP = S::kPieces, NS = S::kStages, NB = S::kBlock, UNIT = MANY ? kWarps * kRows : kRows;
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
-    uint8_t* const ring = smem + warp * (S::kSmem / kWarps);
-    uint8_t* const tiles = ring + NS * S::kStage;          // MANY: a block of tiles of queries
+    uint8_t* const ring = smem + warp * (NS * S::kStage);
+    uint8_t* const tiles = smem + S::kRings;               // MANY: a block of tiles of queries
     const uint32_t dst = smem_u32(ring) + 16 * lane, dst4 = smem_u32(ring) + S::kKeys + 4 * lane;
 
-    Batch<WHOLE> ahead{};
-    ahead.next.seek(a, (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
+    Batch<UNIT, WHOLE> ahead{};
+    ahead.sub = MANY ? warp * kRows : 0;
+    ahead.next.seek(a, MANY ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp, MANY ? gridDim.x : (int64_t)gridDim.x * kWarps);
     if (ahead.next.left == 0) return;
-    Walk w = ahead.next;
+    Walk<UNIT> w = ahead.next;
     ahead.look(a);
     // What a lane keeps of a tile while its keys are on their way: the record that it writes, of row g (t = 0) or g + 8
     // (t = 1), -1 for none, and where its rows' scale bytes lie in their words.  Nothing that is loaded stays in registers: a
     // wait for an older tile's would be one for the newer tiles' as well (64 requests of 0-8K in e4m3: 86 -> 67 us).
     int64_t record[NS];
     uint32_t byte[NS][2];
-    const uint8_t* const keys = a.c.k + 16 * t + (WHOLE ? g * a.c.st : 0);
+    const int64_t own = 16 * t + (WHOLE ? g * a.c.st : 0);
+    const uint8_t* const keys = a.c.k + own;
     const int64_t half = 8 * a.c.st;
     const auto copy = [&](int stage) {
         if (ahead.i == ahead.n) ahead.turn(a);
@@ -336,13 +352,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
                 }
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
-                    if (UP_IN(row[j] + 64 * p, a.c.row_limit, a.status)) copy16(dst + stage * S::kStage + (j * NP + p) * 512, keys + row[j] + 64 * p);
+                    if (UP_IN(own + row[j] + 64 * p, a.c.row_limit, a.status)) copy16(dst + stage * S::kStage + (j * NP + p) * 512, keys + row[j] + 64 * p);
                 if constexpr (E4M3) {
                     byte[stage][j] = (WHOLE ? g : static_cast<uint32_t>(sc[j])) & 3;
                     if (UP_IN(sc[j], a.c.scale_limit, a.status)) copy4(dst4 + stage * S::kStage + 128 * (1 + j), a.c.ks + (sc[j] & ~int64_t{3}));
                 }
             }
-            const int pos = ahead.p0 + ahead.i * kRows + 8 * t + g;
+            const int pos = ahead.p0 + ahead.i * UNIT + 8 * t + g;
             const bool mine = t < 2 && (t ? valid[1] : valid[0]) && pos < ahead.len;
             const int64_t at = t ? rec[1] : rec[0];
             record[stage] = mine ? at : -1;
@@ -376,11 +392,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
             float sum[2] = {0.f, 0.f};
             for (int b = 0; b < (MANY ? blocks : 1); ++b) {
                 const int here = MANY ? min(NB, (a.group - 8 * NB * b + 7) / 8) : 1;
-                if (MANY && (fresh || blocks > 1))         // a lane reads what it has put
-                    for (int i = 0; i < here; ++i) {
+                if (MANY && (fresh || blocks > 1)) {       // the warps have the same run, and meet here together
+                    __syncthreads();
+                    for (int i = warp; i < here; i += kWarps) {
                         q.load(a, w.r, w.head, 8 * (NB * b + i));
                         q.put(tiles + i * S::kTile);
                     }
+                    __syncthreads();
+                }
                 for (int i = 0; i < here; ++i) {
                     if (MANY) q.get(tiles + i * S::kTile);
                     float d[2][4] = {};                    // in two parts, so that a product need not wait for the one before
@@ -423,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
             }
             const int64_t at = record[stage];
             if (at >= 0 && UP_IN(at, a.records, a.status)) {
-                const int pos = w.unit * kRows + 8 * t + g;
+                const int pos = w.unit * UNIT + ahead.sub + 8 * t + g;
                 a.out[at] = fmaf(a.decay, __uint_as_float(words[0]), t ? sum[1] : sum[0]);
                 if (pos >= w.from) a.born[at] = (a.total ? a.total[w.r] : w.len) - w.len + pos;
             }
@@ -440,7 +459,7 @@ static cudaError_t launch_one(const Args& a, cudaStream_t st) {
         return cudaFuncSetAttribute(mass_kernel<DK, E4M3, MANY, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)a.R * a.c.Hkv * cdiv((int64_t)a.max_blocks * a.c.B, kRows);
+    const int64_t units = (int64_t)a.R * a.c.Hkv * cdiv((int64_t)a.max_blocks * a.c.B, (MANY ? kWarps : 1) * kRows);
     const int64_t ctas = std::min<int64_t>(units, (int64_t)S::kCtas * num_sms());
     return launch_pdl(mass_kernel<DK, E4M3, MANY, WHOLE>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), S::kSmem, st, a);
 }
