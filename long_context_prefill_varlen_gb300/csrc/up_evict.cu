@@ -533,31 +533,80 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
     }
 }
 
+// a launch of evict_kernel, in clusters
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(int64_t lists, int cluster, int threads, size_t smem, cudaStream_t st) : cfg{} {
+        cfg.gridDim = dim3(static_cast<unsigned>(lists * cluster));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+    ClusterLaunch(const ClusterLaunch&) = delete;
+};
+
 template <int W, bool TEAM>
-static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_t st) {
+static cudaError_t prepare_evict() {
     static DeviceSet done{0};
-    cudaError_t e = once_per_device(done, [] {
+    return once_per_device(done, [] {
         return cudaFuncSetAttribute(evict_kernel<W, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
     });
+}
+
+// The most CTAs of a cluster, `cluster` or fewer, that the current device has room for (a partition with small processing
+// clusters may not have it for 8): asked once on each device and for each size, with all the memory that a call may want.
+template <int W>
+static int placed(int cluster) {
+    static std::atomic<uint64_t> yes[4], no[4];        // bit d: device d; sizes 1, 2, 4, 8
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    for (; cluster > 1; cluster /= 2) {
+        int i = 0, n = 0;
+        while ((1 << i) < cluster) ++i;
+        if (yes[i].load(std::memory_order_relaxed) & bit) return cluster;
+        if (no[i].load(std::memory_order_relaxed) & bit) continue;
+        const ClusterLaunch l(1, cluster, 32 * W, kMostKeys * 4, nullptr);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, evict_kernel<W, true>, &l.cfg);
+        if (e != cudaSuccess) cudaGetLastError();      // an answer, too: the next call's check must not find it
+        const bool fits = e == cudaSuccess && n > 0;
+        (fits ? yes : no)[i].fetch_or(bit, std::memory_order_relaxed);
+        if (fits) return cluster;
+    }
+    return 1;
+}
+
+// CTAs of 8 warps take short lists, and never share one.
+template <int W>
+static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_t st) {
+    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d;
+    // the most that a CTA of `n` gets, of the longest list or of one that is not worth more CTAs
+    const auto room = [&](int n) {
+        const int64_t most = std::max<int64_t>(cdiv(cap, n), std::min<int64_t>(cap, a.part));
+        return static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
+    };
+    if constexpr (W > 8) {
+        const cudaError_t e = cluster > 1 ? prepare_evict<W, true>() : cudaSuccess;
+        if (e != cudaSuccess) return e;
+        cluster = placed<W>(cluster);
+        if (cluster > 1) {
+            a.room = room(cluster);
+            const ClusterLaunch l(lists, cluster, 32 * W, (size_t)a.room * 4, st);
+            return cudaLaunchKernelEx(&l.cfg, evict_kernel<W, true>, a);
+        }
+    }
+    const cudaError_t e = prepare_evict<W, false>();
     if (e != cudaSuccess) return e;
-    // the most that a CTA of the cluster gets, of the longest list or of one that is not worth more CTAs
-    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d, most = std::max<int64_t>(cdiv(cap, cluster), std::min<int64_t>(cap, a.part));
-    a.room = static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
-    if (!TEAM) return launch_pdl(evict_kernel<W, TEAM>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(lists * cluster));
-    cfg.blockDim = dim3(32 * W);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.room) * 4;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<W, TEAM>, a);
+    a.room = room(1);
+    return launch_pdl(evict_kernel<W, false>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -671,7 +720,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 template <int LPR, bool SCALED>
 static cudaError_t launch_move(const MoveArgs& a, cudaStream_t st) {
     const int64_t y = std::min<int64_t>(a.lists, 65535);
-    const int64_t x = std::min<int64_t>(cdiv(a.max_moves, kChunk * (kMoveThreads / 32)), std::max<int64_t>(1, cdiv(kMovePerSm * (int64_t)num_sms(), y)));
+    const int64_t x = std::min<int64_t>(cdiv(a.max_moves, kChunk * (kMoveThreads / 32)),
+                                        std::max<int64_t>(1, cdiv(kMovePerSm * (int64_t)num_sms(), y)));
     return launch_pdl(move_kernel<LPR, SCALED>, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kMoveThreads), 0, st, a);
 }
 
@@ -723,14 +773,16 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     int cluster = 1;
     const bool many = lists > num_sms();
     a.part = many ? kMostKeys / 2 : 1024;
-    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part && (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys)) cluster *= 2;
+    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part &&
+           (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys))
+        cluster *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Many short lists go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
     // 27.1 -> 26.2; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.  Few lists with much for
     // each CTA of a cluster take all that an SM has: 4 of 128K on 2 heads 26.1 -> 25.0, one of a million on one 229 -> 169.
-    const cudaError_t e = cluster == 1 ? many && cap <= a.part ? launch_evict<8, false>(a, 1, lists, st) : launch_evict<16, false>(a, 1, lists, st)
-                          : !many && cap > (int64_t)cluster * 8192 ? launch_evict<32, true>(a, cluster, lists, st)
-                                                                   : launch_evict<16, true>(a, cluster, lists, st);
+    const cudaError_t e = cluster == 1 && many && cap <= a.part                         ? launch_evict<8>(a, 1, lists, st)
+                          : cluster > 1 && !many && cap > (int64_t)cluster * 8192 ? launch_evict<32>(a, cluster, lists, st)
+                                                                                   : launch_evict<16>(a, cluster, lists, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();

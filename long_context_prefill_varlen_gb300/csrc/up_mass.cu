@@ -284,7 +284,8 @@ struct Batch {
         next_n = next.left > 0 ? min(kTiles, min(next.units - next.unit, next.left)) : 0;
         const int pos = next.unit * UNIT + sub + offset();
         const int64_t e = (int64_t)next.r * a.max_blocks + div_of(pos, a.by_b);
-        page = (WHOLE ? lane < next_n : lane < kRows * next_n) && pos < next.len && UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
+        const bool wanted = (WHOLE ? lane < next_n : lane < kRows * next_n) && pos < next.len;
+        page = wanted && UP_IN(e, (int64_t)a.R * a.max_blocks, a.status) ? a.table[e] : -1;
     }
     __device__ __forceinline__ void turn(const Args& a) {
         const int lane = threadIdx.x & 31;
@@ -352,10 +353,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
                 }
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
-                    if (UP_IN(own + row[j] + 64 * p, a.c.row_limit, a.status)) copy16(dst + stage * S::kStage + (j * NP + p) * 512, keys + row[j] + 64 * p);
+                    if (UP_IN(own + row[j] + 64 * p, a.c.row_limit, a.status))
+                        copy16(dst + stage * S::kStage + (j * NP + p) * 512, keys + row[j] + 64 * p);
                 if constexpr (E4M3) {
                     byte[stage][j] = (WHOLE ? g : static_cast<uint32_t>(sc[j])) & 3;
-                    if (UP_IN(sc[j], a.c.scale_limit, a.status)) copy4(dst4 + stage * S::kStage + 128 * (1 + j), a.c.ks + (sc[j] & ~int64_t{3}));
+                    if (UP_IN(sc[j], a.c.scale_limit, a.status))
+                        copy4(dst4 + stage * S::kStage + 128 * (1 + j), a.c.ks + (sc[j] & ~int64_t{3}));
                 }
             }
             const int pos = ahead.p0 + ahead.i * UNIT + 8 * t + g;
@@ -387,8 +390,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
             float scale[2] = {1.f, 1.f};
             if constexpr (E4M3)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    scale[j] = __uint_as_float(max((words[32 * (1 + j)] >> (8 * byte[stage][j]) & 0xffu) << 23, 0x00400000u));      // 2^(b - 127)
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t b = words[32 * (1 + j)] >> (8 * byte[stage][j]) & 0xffu;
+                    scale[j] = __uint_as_float(max(b << 23, 0x00400000u));         // 2^(b - 127)
+                }
             float sum[2] = {0.f, 0.f};
             for (int b = 0; b < (MANY ? blocks : 1); ++b) {
                 const int here = MANY ? min(NB, (a.group - 8 * NB * b + 7) / 8) : 1;

@@ -219,7 +219,9 @@ extern "C" up_status up_rope(const up_rope_table* plan, const uint16_t* q, int64
     const int64_t ctas = cdiv(groups * a.slices, rope::kThreads / 32);
     if (ctas > 0x7fffffff) return UP_ERR_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dk == 64 ? rope::launch<64>(a, ctas, st) : dk == 128 ? rope::launch<128>(a, ctas, st) : rope::launch<256>(a, ctas, st);
+    const cudaError_t e = dk == 64    ? rope::launch<64>(a, ctas, st)
+                          : dk == 128 ? rope::launch<128>(a, ctas, st)
+                                      : rope::launch<256>(a, ctas, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();

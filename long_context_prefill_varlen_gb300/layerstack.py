@@ -220,7 +220,8 @@ class StackCache:
         if not self.weighed:
             raise ValueError("no token has been decoded since the prefill: the cached tokens have no weights yet")
         dev, cap = self.kv_len.device, self.max_blocks * self.B
-        if isinstance(budget, int):
+        if not isinstance(budget, torch.Tensor):
+            budget = int(budget)
             if budget < 0:
                 raise ValueError(f"a budget of {budget} tokens")
             most, budget = min(budget, cap // 2), torch.full((self.R,), budget, device=dev, dtype=torch.int32)

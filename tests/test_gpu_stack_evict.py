@@ -146,3 +146,17 @@ def test_the_stacks_planned_positions(how):
         ref = stack_ref.forward(stack, hidden, host["positions"], LENGTHS)
         got = out.double().cpu()
         assert float(torch.linalg.norm(got - ref) / torch.linalg.norm(ref)) < REL_FRO
+
+
+def test_eviction_makes_room_in_a_full_cache():
+    lengths = (16, 40)
+    stack, cache, _, _ = _prefill(True, [], True, lengths=lengths)             # three pages of 16 for the longer request
+    steps = _steps(8, 20, lengths)
+    for _ in range(8):
+        stack.decode(*next(steps), cache)
+    cache.check()
+    cache.evict(np.int64(30), recent=8)
+    for _ in range(12):                                                        # 30 tokens grow to 42
+        stack.decode(*next(steps), cache)
+    cache.check()
+    assert cache.rows(0, cache.seqused(0)).tolist() == [16 + 20, 30 + 12] and cache.seqused(0).tolist() == [36, 60]
