@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
                 const uint32_t x[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (x[j] >> kShift0 == digit && at < kBins) {      // (as are all, unless records change under the call)
+                    if (x[j] >> kShift0 == digit && (held || at < kBins)) {        // (all are, unless records change under the call)
                         if (TEAM) st_rank(&sh.hist[1][at], 0, x[j]); else sh.hist[1][at] = x[j];
                         ++at;
                         --n;
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
         if (head == 0) a.new_len[r] = l.k;
     }
     int32_t* const moves = a.moves + (int64_t)list * a.max_moves * 2;
+    const uint32_t most = static_cast<uint32_t>(min(a.max_moves, (int64_t)INT32_MAX));
     for (int i = 0; i < steps; ++i) {
         const int p = from + 128 * i, p0 = p - 4 * lane;
         const uint4 y = again(i);
@@ -521,8 +522,8 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
                 const bool stays = c[j] == 1u || (c[j] != 0u && eq < need), low = p + j < l.k;
                 if (p + j < l.len && low != stays) {
                     const uint32_t m = low ? p + j - stay_before : stay_before - stay_low;
-                    // (m is below max_moves, unless records change under the call)
-                    if (m < a.max_moves && UP_IN(m, a.max_moves, a.status)) moves[2 * (size_t)m + low] = p + j;
+                    // (m is below most, unless records change under the call)
+                    if (m < most && UP_IN(m, a.max_moves, a.status)) moves[2 * (size_t)m + low] = p + j;
                 }
                 gt += c[j] & 1u;
                 eq += c[j] >> 16;
