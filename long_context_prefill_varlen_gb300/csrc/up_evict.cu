@@ -12,7 +12,7 @@
 // digit's values a pass, which the cluster's CTAs add up through distributed shared memory.  Then every position's rank
 // among the rows that stay is the number of larger keys before it plus the number of equal ones before it, as far as they
 // stay.  A lane takes four neighbouring positions at a time: one table entry and two 16-byte loads, where pages allow it.
-// Measured (one GB300): one request of 4,097 positions on 8 heads 7.5 us, 64 of 0-8K on 8 heads 26 us, 4 of 128K on 2 heads 25 us.
+// Measured (one GB300): one request of 4,097 positions on 8 heads 6.7 us, 64 of 0-8K on 8 heads 27 us, 4 of 128K on 2 heads 25 us.
 // Bytes are not what bounds it (the keys come from L2 in 1 to 3 us) but a chain of latencies, some 4 us of launch, length, table
 // and records, six meetings of the CTA or cluster, and about 450 instructions for a warp's 128 positions.
 #include <stdint.h>
@@ -29,7 +29,6 @@ using kv::FastDiv;
 
 constexpr int kShift0 = 21, kShift1 = 10;    // where a key's first and second digit start
 constexpr int kBins = 2048, kCoarse = kBins / 32;
-constexpr int kMaxCluster = 8;
 constexpr int kMostKeys = 32 * 1024;         // keys of a CTA in shared memory; a longer part is read again by every pass
 
 struct Args {
@@ -177,20 +176,22 @@ __device__ __forceinline__ uint32_t of_cta(const uint32_t* p, int rank) {
     if constexpr (TEAM) return ld_rank(p, rank); else return *p;
 }
 // the sum of a word over the list's CTAs, all on their way at once
-template <bool TEAM>
+template <int C>
 __device__ __forceinline__ uint32_t over_ctas(const uint32_t* p, int ctas) {
-    if constexpr (!TEAM) return *p;
-    uint32_t v[kMaxCluster], n = 0;
+    if constexpr (C == 1) return *p;
+    uint32_t v[C], n = 0;
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) v[c] = c < ctas ? ld_rank(p, c) : 0u;
+    for (int c = 0; c < C; ++c) v[c] = c < ctas ? ld_rank(p, c) : 0u;
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) n += v[c];
+    for (int c = 0; c < C; ++c) n += v[c];
     return n;
 }
 
-template <int W, bool TEAM>
+// C: the most CTAs of a cluster, 1 without clusters
+template <int W, int C>
 __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __grid_constant__ Args a) {
     constexpr int kThreads = 32 * W;
+    constexpr bool TEAM = C > 1;
     extern __shared__ __align__(16) uint4 keys[];
     __shared__ Shared<W> sh;
     pdl_wait();
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
     // protected rows, bad entries and zeros of the list
     const auto gather = [&]() {
         if (warp == 0) {
-            const uint32_t x[3] = {over_ctas<TEAM>(&sh.guarded, ctas), over_ctas<TEAM>(&sh.bad, ctas), over_ctas<TEAM>(&sh.zeros, ctas)};
+            const uint32_t x[3] = {over_ctas<C>(&sh.guarded, ctas), over_ctas<C>(&sh.bad, ctas), over_ctas<C>(&sh.zeros, ctas)};
 #pragma unroll
             for (int i = 0; i < 3; ++i)
                 if (lane == i) sh.list[i] = x[i];
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
 #pragma unroll
                 for (int j = 0; j < kEach[level]; ++j) {
                     const int at = level ? 32 * bin + 31 - lane : kCoarse - 1 - (kEach[0] * lane + j);
-                    n[j] = over_ctas<TOGETHER>(level ? &sh.hist[which][at] : &sh.coarse[which][at], ctas);
+                    n[j] = over_ctas<(TOGETHER ? C : 1)>(level ? &sh.hist[which][at] : &sh.coarse[which][at], ctas);
                     all += n[j];
                 }
                 uint32_t upto = all;
@@ -484,8 +485,8 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
         }
         meet<TEAM>();
         if (warp == 0) {
-            const uint32_t x[4] = {over_ctas<TEAM>(&sh.above[0], ctas), over_ctas<TEAM>(&sh.equal[0], ctas),
-                                   over_ctas<TEAM>(&sh.above[1], rank), over_ctas<TEAM>(&sh.equal[1], rank)};
+            const uint32_t x[4] = {over_ctas<C>(&sh.above[0], ctas), over_ctas<C>(&sh.equal[0], ctas),
+                                   over_ctas<C>(&sh.above[1], rank), over_ctas<C>(&sh.equal[1], rank)};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (lane == i) sh.sums[i] = x[i];
@@ -554,19 +555,20 @@ struct ClusterLaunch {
     ClusterLaunch(const ClusterLaunch&) = delete;
 };
 
-template <int W, bool TEAM>
+template <int W, int C>
 static cudaError_t prepare_evict() {
     static DeviceSet done{0};
     return once_per_device(done, [] {
-        return cudaFuncSetAttribute(evict_kernel<W, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+        const cudaError_t e = cudaFuncSetAttribute(evict_kernel<W, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+        return C > 8 && e == cudaSuccess ? cudaFuncSetAttribute(evict_kernel<W, C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
     });
 }
 
 // The most CTAs of a cluster, `cluster` or fewer, that the current device has room for (a partition with small processing
 // clusters may not have it for 8): asked once on each device and for each size, with all the memory that a call may want.
-template <int W>
+template <int W, int C>
 static int placed(int cluster) {
-    static std::atomic<uint64_t> yes[4], no[4];        // bit d: device d; sizes 1, 2, 4, 8
+    static std::atomic<uint64_t> yes[5], no[5];        // bit d: device d; sizes 1, 2, 4, 8, 16
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
     const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
@@ -576,7 +578,7 @@ static int placed(int cluster) {
         if (yes[i].load(std::memory_order_relaxed) & bit) return cluster;
         if (no[i].load(std::memory_order_relaxed) & bit) continue;
         const ClusterLaunch l(1, cluster, 32 * W, kMostKeys * 4, nullptr);
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, evict_kernel<W, true>, &l.cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, evict_kernel<W, C>, &l.cfg);
         if (e != cudaSuccess) cudaGetLastError();      // an answer, too: the next call's check must not find it
         const bool fits = e == cudaSuccess && n > 0;
         (fits ? yes : no)[i].fetch_or(bit, std::memory_order_relaxed);
@@ -585,29 +587,30 @@ static int placed(int cluster) {
     return 1;
 }
 
-// CTAs of 8 warps take short lists, and never share one.
+// the most keys that a CTA of `cluster` gets, of the longest list or of one that is not worth more CTAs, as far as it holds them
 template <int W>
-static cudaError_t launch_evict(Args& a, int cluster, int64_t lists, cudaStream_t st) {
-    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d;
-    // the most that a CTA of `n` gets, of the longest list or of one that is not worth more CTAs
-    const auto room = [&](int n) {
-        const int64_t most = std::max<int64_t>(cdiv(cap, n), std::min<int64_t>(cap, a.part));
-        return static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
-    };
-    if constexpr (W > 8) {
-        const cudaError_t e = cluster > 1 ? prepare_evict<W, true>() : cudaSuccess;
-        if (e != cudaSuccess) return e;
-        cluster = placed<W>(cluster);
-        if (cluster > 1) {
-            a.room = room(cluster);
-            const ClusterLaunch l(lists, cluster, 32 * W, (size_t)a.room * 4, st);
-            return cudaLaunchKernelEx(&l.cfg, evict_kernel<W, true>, a);
-        }
-    }
-    const cudaError_t e = prepare_evict<W, false>();
+static int room_of(const Args& a, int cluster) {
+    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d, most = std::max<int64_t>(cdiv(cap, cluster), std::min<int64_t>(cap, a.part));
+    return static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
+}
+
+template <int W>
+static cudaError_t launch_alone(Args& a, int64_t lists, cudaStream_t st) {
+    const cudaError_t e = prepare_evict<W, 1>();
     if (e != cudaSuccess) return e;
-    a.room = room(1);
-    return launch_pdl(evict_kernel<W, false>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
+    a.room = room_of<W>(a, 1);
+    return launch_pdl(evict_kernel<W, 1>, dim3(static_cast<unsigned>(lists)), dim3(32 * W), (size_t)a.room * 4, st, a);
+}
+
+template <int W, int C>
+static cudaError_t launch_team(Args& a, int cluster, int64_t lists, cudaStream_t st) {
+    const cudaError_t e = prepare_evict<W, C>();
+    if (e != cudaSuccess) return e;
+    cluster = placed<W, C>(cluster);
+    if (cluster == 1) return launch_alone<W>(a, lists, st);
+    a.room = room_of<W>(a, cluster);
+    const ClusterLaunch l(lists, cluster, 32 * W, (size_t)a.room * 4, st);
+    return cudaLaunchKernelEx(&l.cfg, evict_kernel<W, C>, a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -769,21 +772,25 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     a.status = dev_status;
     const int64_t lists = (int64_t)R * Hkv, cap = (int64_t)max_blocks * B;
     a.quads = B % 4 == 0 && aligned16(mass) && aligned16(born);
-    // A list's CTAs: one where the lists are many; a cluster where they leave SMs idle, or where they are longer than a CTA
-    // holds at two or three on an SM.
-    int cluster = 1;
-    const bool many = lists > num_sms();
+    // A list's CTAs: one where lists are many or short (up to 6K: one of 4K on 8 heads 7.6 us in a cluster, 6.8 alone; of 8K 10.9
+    // and 12); a cluster where they leave SMs idle, or are longer than a CTA holds at two or three on an SM; one of 16, which
+    // may not fit every device and meets more slowly, where 8 do not hold the keys (half a million on one head 93 -> 35 us).
+    const bool many = lists > num_sms(), huge = cap > 8 * (int64_t)kMostKeys && lists * 16 <= num_sms();
     a.part = many ? kMostKeys / 2 : 1024;
-    while (cluster < kMaxCluster && cap > (int64_t)cluster * a.part &&
-           (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys))
-        cluster *= 2;
+    int cluster = 1;
+    if (many || cap > 6144)
+        while (cluster < (huge ? 16 : 8) && cap > (int64_t)cluster * a.part &&
+               (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys))
+            cluster *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Many short lists go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
-    // 27.1 -> 26.2; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.  Few lists with much for
-    // each CTA of a cluster take all that an SM has: 4 of 128K on 2 heads 26.1 -> 25.0, one of a million on one 229 -> 169.
-    const cudaError_t e = cluster == 1 && many && cap <= a.part                         ? launch_evict<8>(a, 1, lists, st)
-                          : cluster > 1 && !many && cap > (int64_t)cluster * 8192 ? launch_evict<32>(a, cluster, lists, st)
-                                                                                   : launch_evict<16>(a, cluster, lists, st);
+    // 28.1 -> 27.3; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.  Few lists with much for
+    // each CTA of a cluster take all that an SM has: 4 of 128K on 2 heads 26.1 -> 25.0, one of a million on one 229 -> 169 (and by 16 97).
+    const cudaError_t e = cluster > 8                                              ? launch_team<32, 16>(a, cluster, lists, st)
+                          : cluster > 1 && !many && cap > (int64_t)cluster * 8192 ? launch_team<32, 8>(a, cluster, lists, st)
+                          : cluster > 1                                            ? launch_team<16, 8>(a, cluster, lists, st)
+                          : many && cap <= a.part                                  ? launch_alone<8>(a, lists, st)
+                                                                                   : launch_alone<16>(a, lists, st);
     if (e != cudaSuccess) return failed_launch();
     count_launch();
     return check_launch();

@@ -222,16 +222,16 @@ def test_every_call_launches_on_every_device_and_an_error_is_its_own(lib, up):
 
 
 def test_a_list_goes_to_a_cluster_where_it_is_worth_one(lib, up):
-    for R, max_blocks, cluster in ((1, 4, 1), (1, 60000, 8), (300, 4, 1), (300, 2000, 2), (300, 60000, 8), (30, 1000, 2)):
-        lib.fake_reset(42, 8)
+    for R, max_blocks, cluster in ((1, 4, 1), (1, 60000, 16), (1, 16384, 8), (1, 300, 1), (300, 4, 1), (300, 2000, 2), (300, 60000, 8), (30, 1000, 2)):
+        lib.fake_reset(42, 16)
         assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
         assert lib.fake_launch_cluster(0) == cluster, (R, max_blocks)
 
 
-@pytest.mark.parametrize("largest", [1, 2, 4, 8])
+@pytest.mark.parametrize("largest", [1, 2, 4, 8, 16])
 def test_a_cluster_that_the_device_cannot_place_is_a_smaller_one(lib, up, largest):
     """(a partition of a GPU may have room for smaller clusters only)"""
-    for R, max_blocks, cluster in ((1, 60000, 8), (1, 200, 4), (300, 2000, 2), (1, 4, 1), (300, 60000, 8)):
+    for R, max_blocks, cluster in ((1, 60000, 16), (1, 500, 8), (300, 2000, 2), (1, 4, 1), (300, 60000, 8)):
         for _ in range(2):
             lib.fake_reset(43 + largest, largest)
             assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
