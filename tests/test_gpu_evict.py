@@ -575,3 +575,76 @@ def test_what_the_binding_refuses():
     with pytest.raises(AssertionError):
         up.up_kv_move(c.k, c.v, t, o["moves"][:2], o["num_moves"], st)
     assert up.up_read_status(st) == 0
+
+
+# ------------------------------------------------------------------------------------------ far and at once
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_rows_beyond_32_bits_of_offset(e4m3):
+    """a cache of five gigabytes a side, of which the last pages are used: against the same rows in a small one"""
+    lens, Hkv, B, dk = (300, 0, 77), 8, 16, 128
+    small, table, rows, qb = _decode_case(11, 16, Hkv, dk, B, lens, e4m3)
+    nb = 5 * (1 << 30) // (Hkv * B * dk * (1 if e4m3 else 2))
+    dt = torch.uint8 if e4m3 else torch.int16
+    big = type(small).__new__(type(small))
+    big.e4m3, big.B, big.Hkv, big.dk, big.num_blocks = e4m3, B, Hkv, dk, nb
+    far = nb - small.num_blocks
+    big.k, big.v = (torch.empty(nb, Hkv, B, dk, dtype=dt, device="cuda").view(torch.float8_e4m3fn if e4m3 else torch.bfloat16) for _ in "kv")
+    big.ks, big.vs = (torch.empty(nb, Hkv, B, dtype=torch.uint8, device="cuda") if e4m3 else None for _ in "kv")
+    for x, y in zip((big.k, big.v, big.ks, big.vs), (small.k, small.v, small.ks, small.vs)):
+        if y is not None:
+            x.view(dt if y.dtype != torch.uint8 else torch.uint8)[far:] = y.view(dt if y.dtype != torch.uint8 else torch.uint8)
+    results = []
+    for c, up_by in ((small, 0), (big, far)):
+        t = np.where((table >= 0) & (table < small.num_blocks), table + up_by, table)
+        mass, born = (torch.empty(c.num_blocks, Hkv, B, dtype=x, device="cuda") for x in (torch.float32, torch.int32))
+        mass[-small.num_blocks:], born[-small.num_blocks:] = 1.0, 5
+        out, new = _step(c, t, lens, _from_bits(qb), mass, born, (100, 3, 40), dict(counted=(250, 0, 0), total=(400, 0, 77)), sinks=2, recent=9)
+        rows_of = [x[-small.num_blocks:].clone() for x in (c.k.view(dt), c.v.view(dt), mass, born)]
+        results.append((out, new, rows_of + ([c.ks[-small.num_blocks:].clone(), c.vs[-small.num_blocks:].clone()] if e4m3 else [])))
+    assert torch.equal(results[0][0], results[1][0]) and results[0][1] == results[1][1]
+    assert all(torch.equal(x, y) for x, y in zip(results[0][2], results[1][2]))
+
+
+def test_records_beyond_32_bits_of_index():
+    nb, B = 36_000_000, 64                                   # 2.3 billion records
+    mass, born = torch.empty(nb, 1, B, device="cuda"), torch.empty(nb, 1, B, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(1)
+    n, k = 1000, 300
+    pages = np.concatenate([[nb - 1, 0, 33_600_000, 17_000_000], np.arange(nb - 14, nb - 2)]).astype(np.int32)
+    m, p = rng.random(n).astype(np.float32), np.arange(n)
+    at = torch.from_numpy(pages).cuda().long()[torch.from_numpy(p).cuda() // B]
+    mass[at, 0, torch.from_numpy(p % B).cuda()] = torch.from_numpy(m).cuda()
+    born[at, 0, torch.from_numpy(p % B).cuda()] = torch.from_numpy(p.astype(np.int32)).cuda()
+    status, moves, num, new_len = _choose(mass, born, pages[None], (n,), (k,), sinks=3, recent=20)
+    want = evict_ref.evict(m, p, n, k, 3, 20)
+    assert status == 0 and int(new_len[0]) == k and moves[0, 0, :int(num[0, 0])].tolist() == [list(x) for x in want]
+
+
+def test_two_streams_at_once():
+    """two layers' steps side by side, over and over: each as it is alone"""
+    alone, at_once = [], []
+    for results, streams in ((alone, [None, None]), (at_once, [torch.cuda.Stream(), torch.cuda.Stream()])):
+        work = []
+        for i, e4m3 in enumerate((False, True)):
+            lens = (3000, 0, 1500, 33) if i else (700, 9000, 1)
+            c, table, rows, qb = _decode_case(20 + i, 8, 2, 128, 16, lens, e4m3)
+            mass, born = _records(c, 20 + i)
+            _, _, lse = _run_decode(c, table, lens, _from_bits(qb))
+            out = torch.zeros_like(mass)
+            n = len(lens)
+            o = dict(budget=_i32([x // 2 for x in lens]), moves=torch.zeros(n, 2, 5000, 2, dtype=torch.int32, device="cuda"),
+                     num=torch.zeros(n, 2, dtype=torch.int32, device="cuda"), new=_i32([0] * n))
+            work.append((c, torch.from_numpy(table).cuda(), _i32(lens), _from_bits(qb), lse, mass, born, out, o, _status()))
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for (c, t, n, q, lse, mass, born, out, o, st), stream in zip(work, streams):
+                up.up_kv_mass(q, c.k, c.v, t, n, lse, mass, born, st, **c.scales(), mass_out=out, stream=stream)
+                up.up_kv_evict(out, born, t, n, o["budget"], o["moves"], o["num"], o["new"], st, sinks=4, recent=16, stream=stream)
+                up.up_kv_move(c.k, c.v, t, o["moves"], o["num"], st, **c.scales(), stream=stream)
+        torch.cuda.synchronize()
+        for c, t, n, q, lse, mass, born, out, o, st in work:
+            assert up.up_read_status(st) == 0
+            results.append([out.cpu().numpy(), o["num"].cpu().numpy(), o["new"].cpu().numpy()] + _all_rows(c))
+    for x, y in zip(alone, at_once):
+        assert all(np.array_equal(a, b, equal_nan=a.dtype.kind == "f") for a, b in zip(x, y))

@@ -200,3 +200,14 @@ def test_tensors_elsewhere_are_refused():
         up.up_rope(plan, torch.zeros(2, dtype=torch.int64, device="cuda"), _status(), q=q)
     with pytest.raises(up.UpError):
         up.up_rope(up.up_rope_plan(128), torch.zeros(2, dtype=torch.int64, device="cuda"), _status(), q=q, q_out=q)
+
+
+def test_streams_beyond_32_bits_of_offset():
+    T, H, dk = 1_100_003, 16, 128                            # 4.5 GB in, as much out
+    q, out = (torch.empty(T, H, dk, dtype=torch.bfloat16, device="cuda") for _ in "io")
+    last = torch.randn(1000, H, dk, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(torch.bfloat16)
+    q[-1000:] = last
+    pos, plan, st = torch.arange(T, device="cuda"), up.up_rope_plan(64), _status()
+    up.up_rope(plan, pos, st, q=q, q_out=out)
+    assert up.up_read_status(st) == 0
+    assert torch.equal(out[-1000:], _call(plan, pos[-1000:].contiguous(), last, None)[0])
