@@ -44,7 +44,8 @@ struct Args {
     int64_t num_blocks, records, max_moves;
     int R, Hkv, max_blocks, sinks, recent;
     int room;                // keys that the CTA's shared memory holds
-    int part;                // keys that make a CTA of the cluster worth while
+    int alone, part;         // keys that one CTA takes; keys that make another CTA of the cluster worth while
+    int more, most;          // the launch's lists: of more than `more` and at most `most` positions
     bool quads;              // four neighbouring records lie side by side, 16-byte aligned
     FastDiv by_b, by_heads;
     int32_t* status;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
         if (first) set_status(a.status, UP_DEV_BAD_LENGTH);
         l.len = 0;
     }
+    if (l.len <= a.more || l.len > a.most) return;         // another launch's
     l.k = min(budget, l.len);
     l.recent_from = static_cast<int>(max((int64_t)(a.total ? total : l.len) - a.recent, (int64_t)INT32_MIN));
     const auto leave = [&](int len) {
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) evict_kernel(const __
     if (l.k == l.len || l.k == 0) return leave(l.k);       // all rows stay, or none
     // As many CTAs as the list is worth; the others leave at once (a cluster's barriers wait for those that stay).  A CTA
     // has a part of the positions, a warp a part of that, in steps of 128.
-    const int ctas = TEAM ? min(size, (l.len + a.part - 1) / a.part) : 1;
+    const int ctas = TEAM && l.len > a.alone ? min(size, (l.len + a.part - 1) / a.part) : 1;
     if (rank >= ctas) return;
     const int steps = (l.len + ctas * (128 * W) - 1) / (ctas * (128 * W)), per = steps * 128 * W;
     const int from = rank * per + warp * steps * 128 + 4 * lane;      // the lane's first position
@@ -590,7 +592,8 @@ static int placed(int cluster) {
 // the most keys that a CTA of `cluster` gets, of the longest list or of one that is not worth more CTAs, as far as it holds them
 template <int W>
 static int room_of(const Args& a, int cluster) {
-    const int64_t cap = (int64_t)a.max_blocks * a.by_b.d, most = std::max<int64_t>(cdiv(cap, cluster), std::min<int64_t>(cap, a.part));
+    const int64_t cap = std::min<int64_t>((int64_t)a.max_blocks * a.by_b.d, a.most);
+    const int64_t most = std::max<int64_t>(cdiv(cap, cluster), std::min<int64_t>(cap, a.alone));
     return static_cast<int>(std::min<int64_t>(cdiv(most, 128 * W) * 128 * W, kMostKeys));
 }
 
@@ -776,13 +779,25 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     // and 12); a cluster where they leave SMs idle, or are longer than a CTA holds at two or three on an SM; one of 16, which
     // may not fit every device and meets more slowly, where 8 do not hold the keys (half a million on one head 93 -> 35 us).
     const bool many = lists > num_sms(), huge = cap > 8 * (int64_t)kMostKeys && lists * 16 <= num_sms();
+    a.alone = many ? kMostKeys / 2 : 6144;
     a.part = many ? kMostKeys / 2 : 1024;
+    a.more = -1;
+    a.most = INT32_MAX;
     int cluster = 1;
-    if (many || cap > 6144)
+    if (cap > a.alone)
         while (cluster < (huge ? 16 : 8) && cap > (int64_t)cluster * a.part &&
                (many || lists * cluster * 2 <= num_sms() || cap > (int64_t)cluster * kMostKeys))
             cluster *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Many lists under wide tables may all be short: those go first, a CTA each, and then the clusters of the others, which leave at
+    // once where they find nothing to do (64 of 0-8K on 8 heads in tables of 128K 84 -> 36 us, in such of 8K 27).
+    const bool apart = many && cluster > 2;
+    if (apart) {
+        a.most = kMostKeys / 4;
+        if (launch_alone<8>(a, lists, st) != cudaSuccess) return failed_launch();
+        a.more = a.most;
+        a.most = INT32_MAX;
+    }
     // Many short lists go by CTAs of 8 warps, more of which an SM has at once: 128 of 1K on 8 heads 25.9 -> 15.5 us, 64 of 0-8K
     // 28.1 -> 27.3; fewer or longer ones want the threads: 16 of 4K 11.0 -> 8.9, 32 of 32K 84 -> 70.  Few lists with much for
     // each CTA of a cluster take all that an SM has: 4 of 128K on 2 heads 26.1 -> 25.0, one of a million on one 229 -> 169 (and by 16 97).
@@ -792,7 +807,7 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
                           : many && cap <= a.part                                  ? launch_alone<8>(a, lists, st)
                                                                                    : launch_alone<16>(a, lists, st);
     if (e != cudaSuccess) return failed_launch();
-    count_launch();
+    count_launch(apart ? 2 : 1);
     return check_launch();
 }
 

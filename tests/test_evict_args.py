@@ -223,9 +223,10 @@ def test_every_call_launches_on_every_device_and_an_error_is_its_own(lib, up):
 
 def test_a_list_goes_to_a_cluster_where_it_is_worth_one(lib, up):
     for R, max_blocks, cluster in ((1, 4, 1), (1, 60000, 16), (1, 16384, 8), (1, 300, 1), (300, 4, 1), (300, 2000, 2), (300, 60000, 8), (30, 1000, 2)):
+        wide = (R, max_blocks) == (300, 60000)                   # short lists first, a CTA each
         lib.fake_reset(42, 16)
         assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
-        assert lib.fake_launch_cluster(0) == cluster, (R, max_blocks)
+        assert [lib.fake_launch_cluster(i) for i in range(lib.fake_launches())] == [1] * wide + [cluster], (R, max_blocks)
 
 
 @pytest.mark.parametrize("largest", [1, 2, 4, 8, 16])
@@ -235,4 +236,5 @@ def test_a_cluster_that_the_device_cannot_place_is_a_smaller_one(lib, up, larges
         for _ in range(2):
             lib.fake_reset(43 + largest, largest)
             assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
-            assert (lib.fake_launches(), lib.fake_launch_cluster(0)) == (1, min(cluster, largest)), (R, max_blocks)
+            n = lib.fake_launches()
+            assert (n, lib.fake_launch_cluster(n - 1)) == (1 + ((R, max_blocks) == (300, 60000)), min(cluster, largest)), (R, max_blocks)

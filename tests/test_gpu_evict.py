@@ -251,6 +251,22 @@ def test_ties_of_lists_that_have_a_cta_each(name):
     _check_choice(8, (6000, 3000), (5999, 100), Hkv=80, values=EDGES[name])
 
 
+@pytest.mark.parametrize("wide", [500, 3000, 30_000])
+def test_the_choice_does_not_go_by_the_tables_width(wide):
+    """many lists, short ones and long ones, under tables of 8K to half a million positions: launches of other forms, the same
+    moves"""
+    rng = np.random.default_rng(10)
+    lens = [0, 1, 5000, 8000] + [int(x) for x in rng.integers(0, 3000, 36)]
+    if wide > 500:
+        lens += [8192, 8193, 16_384, 16_385, 40_000]
+    budget = [int(n * rng.random()) for n in lens]
+    md, bd, table, moves, num, new_len = _check_choice(11, lens, budget, Hkv=8, sinks=4, recent=30)
+    more = np.full((len(lens), max(wide, table.shape[1])), -1, dtype=np.int32)
+    more[:, :table.shape[1]] = table
+    status, m, n, l = _choose(md, bd, more, lens, budget, max_moves=moves.shape[2], sinks=4, recent=30)
+    assert status == 0 and torch.equal(m, moves) and torch.equal(n, num) and torch.equal(l, new_len)
+
+
 def test_records_that_are_not_aligned():
     rng = np.random.default_rng(9)
     lens, budget = (700, 5, 2000), (300, 2, 1990)
