@@ -181,55 +181,65 @@ struct Walk {
     __device__ __forceinline__ int units_of(const Args& a, int n) const {
         return n < 0 || n > (int64_t)a.max_blocks * static_cast<int64_t>(a.by_b.d) ? 0 : (n + UNIT - 1) / UNIT;
     }
-    __device__ __forceinline__ void seek(const Args& a, int64_t run, int64_t runs) {
-        const int lane = threadIdx.x & 31;
-        left = 0;
-        int n = 0, mine = 0, upto = 0;
-        auto scan = [&](int r0) {
-            n = r0 + lane < a.R && UP_IN(r0 + lane, a.R, a.status) ? a.seqused[r0 + lane] : 0;
-            mine = units_of(a, n);
-            if (mine == 0 && n != 0) set_status(a.status, UP_DEV_BAD_LENGTH);
-            upto = mine;
+    // the units of request r, its length reported if it is none
+    __device__ __forceinline__ int look(const Args& a, int r, int* n) const {
+        *n = r < a.R && UP_IN(r, a.R, a.status) ? a.seqused[r] : 0;
+        const int u = units_of(a, *n);
+        if (u == 0 && *n != 0) set_status(a.status, UP_DEV_BAD_LENGTH);
+        return u;
+    }
+    // x and those of the lanes before
+    template <typename T>
+    static __device__ __forceinline__ T upto(T x) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-        };
-        int64_t all = 0;
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-            scan(r0);
-            all += __shfl_sync(0xffffffffu, upto, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const T y = __shfl_up_sync(0xffffffffu, x, o);
+            if ((threadIdx.x & 31) >= o) x += y;
         }
-        all *= a.c.Hkv;
-        int64_t first;
+        return x;
+    }
+    __device__ __forceinline__ void seek(const Args& a, int64_t run, int64_t runs) {
+        const int lane = threadIdx.x & 31, per = (a.R + 31) / 32;      // requests of a lane, side by side
+        left = 0;
+        int n = 0;
+        int64_t mine = 0;
+#pragma unroll 4
+        for (int i = 0; i < per; ++i) mine += look(a, lane * per + i, &n);
+        const int64_t sum = upto(mine), all = __shfl_sync(0xffffffffu, sum, 31) * a.c.Hkv;
         if (all == 0) return;
+        int64_t first;
         if (all <= runs) {                             // few units: one each, to runs that lie evenly over the grid
-            const int64_t per = runs / all;
-            first = run % per == 0 && run / per < all ? run / per : all;
+            const int64_t apart = runs / all;
+            first = run % apart == 0 && run / apart < all ? run / apart : all;
             left = first < all ? 1 : 0;
         } else {
             first = all * run / runs;
             left = static_cast<int>(all * (run + 1) / runs - first);
         }
         if (left == 0) return;
-        int64_t before = 0;
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-            if (a.R > 32) scan(r0);
-            const uint32_t hit = __ballot_sync(0xffffffffu, before + (int64_t)upto * a.c.Hkv > first);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                r = r0 + l;
-                len = __shfl_sync(0xffffffffu, n, l);
-                units = __shfl_sync(0xffffffffu, mine, l);
-                const int64_t at = first - before - (int64_t)__shfl_sync(0xffffffffu, upto - mine, l) * a.c.Hkv;
-                head = static_cast<int>(at / units);
-                unit = static_cast<int>(at - (int64_t)head * units);
-                from = a.counted ? a.counted[r] : len;
-                return;
+        // the lane whose requests the run starts in, and of those the one
+        const int l = __ffs(__ballot_sync(0xffffffffu, sum * a.c.Hkv > first)) - 1;
+        int64_t before = __shfl_sync(0xffffffffu, sum - mine, l);
+        r = l * per;
+        if (per == 1) {
+            len = __shfl_sync(0xffffffffu, n, l);
+            units = __shfl_sync(0xffffffffu, static_cast<int>(mine), l);
+        } else {
+            for (int i0 = 0;; i0 += 32) {              // (some request of the lane's is the one)
+                const int u = i0 + lane < per ? look(a, l * per + i0 + lane, &n) : 0, to = upto(u);
+                const uint32_t hit = __ballot_sync(0xffffffffu, (before + to) * a.c.Hkv > first);
+                const int at = hit ? __ffs(hit) - 1 : 31;
+                before += __shfl_sync(0xffffffffu, hit ? to - u : to, at);
+                len = __shfl_sync(0xffffffffu, n, at);
+                units = __shfl_sync(0xffffffffu, u, at);
+                r = l * per + i0 + at;
+                if (hit || i0 + 32 >= per) break;
             }
-            before += (int64_t)__shfl_sync(0xffffffffu, upto, 31) * a.c.Hkv;
         }
+        const int64_t at = first - before * a.c.Hkv;
+        head = static_cast<int>(at / units);
+        unit = static_cast<int>(at - (int64_t)head * units);
+        from = a.counted ? a.counted[r] : len;
     }
     // n units on, no further than to the end of the request's head; true where that is another head's
     __device__ __forceinline__ bool skip(const Args& a, int n) {
