@@ -118,9 +118,9 @@ class StackCache:
     layer is position i, whatever its rotary position.  A prefill's dropped tokens therefore leave no holes, and
     the tokens decoded later follow at up_seqused's length (Eq. 17).
 
-    With weigh=True every decode step adds the weights that it gave the cached tokens to their records, and evict() takes
-    the tokens with the least of it out again, of every layer and key head by itself: a layer then has up_seqused's
-    tokens less those that went."""
+    With weigh=True the prompt's last token and every decode step add the weights that they gave the cached tokens to
+    their records, and evict() takes the tokens with the least of it out again, of every layer and key head by itself: a
+    layer then has up_seqused's tokens less those that went."""
 
     def __init__(self, L, R, Hkv, dk, max_len, B=16, e4m3=True, device="cuda", weigh=False):
         dev = torch.device(device)
@@ -218,7 +218,7 @@ class StackCache:
         if not self.weigh:
             raise ValueError("evict() needs a cache that weighs its tokens (weigh=True)")
         if not self.weighed:
-            raise ValueError("no token has been decoded since the prefill: the cached tokens have no weights yet")
+            raise ValueError("no prefill has filled the cache: there are no tokens with weights")
         dev, cap = self.kv_len.device, self.max_blocks * self.B
         if not isinstance(budget, torch.Tensor):
             budget = int(budget)
@@ -343,7 +343,8 @@ class RandomLlamaStack:
         compacted.  Each drop synchronises the host
         once, to learn the compacted stream's length.  With a StackCache, every layer's keys and values are
         written to it as the layer's stream holds them, and the drops to its history, for decode(); the host waits for
-        the end and a request that is longer than the cache raises."""
+        the end and a request that is longer than the cache raises.  A cache that weighs gets the weights of each request's
+        last token."""
         upto = self.L if upto is None else upto
         if cache is not None and upto != self.L:
             raise ValueError("upto: a prefill with a cache runs all layers, as decode() does")
@@ -361,6 +362,10 @@ class RandomLlamaStack:
             slots = cache.slots(cu, T)
         for layer in range(upto):
             x, q, kk = self.attention_sublayer(layer, h, pos, cu, max_len, cache, slots)
+            if cache is not None and cache.weigh:
+                lens = cu.diff()
+                last = q[(cu[1:].long() - 1).clamp(min=0)]         # of a request without tokens: anybody's, it sees nothing
+                cache.attend(layer, last, lens, self.g.dk ** -0.5, lens)
             if k < len(drops) and drops[k][0] == layer:
                 p = drops[k][1]
                 step = DropStep(cu, T, self.g.Hq, self.g.Hkv, self.g.dk, self.g.d, G=G, n=n, A=A, p=p, L=self.L,
@@ -388,6 +393,7 @@ class RandomLlamaStack:
             step.check()
         if cache is not None:
             cache.check()                                  # a request longer than the cache has lost its last rows
+            cache.weighed = True
         return h, info
 
     def decode(self, hidden, positions, cache):
@@ -412,5 +418,4 @@ class RandomLlamaStack:
             o = cache.attend(layer, q, rows, g.dk ** -0.5, seq)
             x = h + torch.matmul(o.view(R, g.Hq * g.dk), self.layers[layer]["wo"])
             h = self.ffn_sublayer(layer, x)
-        cache.weighed = True
         return h

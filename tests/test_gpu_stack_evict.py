@@ -62,9 +62,9 @@ def test_decoding_from_a_cache_that_rows_leave(drops, e4m3):
                 b, m = born[page, :, p % cache.B], mass[page, :, p % cache.B]
                 assert all(len(set(b[:, h])) == len(p) for h in range(GEOM.Hkv)) and (b < had[layer][r]).all()
                 assert np.isfinite(m).all() and (m >= 0).all()
-                if step == 0:                      # a head's weights add up to its query heads, to the weights' own error
-                    assert np.array_equal(b, np.tile(p[:, None], (1, GEOM.Hkv)))
-                    assert np.allclose(m.sum(0), GEOM.Hq // GEOM.Hkv, rtol=1e-4)
+                if step == 0:                      # a head's weights add up to its query heads (twice: the prompt's last
+                    assert np.array_equal(b, np.tile(p[:, None], (1, GEOM.Hkv)))               # token had some, too)
+                    assert np.allclose(m.sum(0), (2 if len(p) > 1 else 1) * (GEOM.Hq // GEOM.Hkv), rtol=1e-4)
         if budgets[step] is not None:
             cache.evict(budgets[step], sinks=sinks, recent=recent)
             cache.check()
@@ -107,8 +107,6 @@ def test_a_new_prefill_forgets_what_was_evicted():
     w = recipe.small(lengths=LENGTHS, Hq=GEOM.Hq, Hkv=GEOM.Hkv, dk=GEOM.dk, hdim=GEOM.d, G=G, n=n, A=A, salt=257)
     d = sgpu.to_device(gen.materialize(w))
     stack.forward(d["hidden"], d["positions"], d["cu_seqlens"], max(LENGTHS), cache=cache)
-    with pytest.raises(ValueError, match="weights"):
-        cache.evict(50)
     fresh = _prefill(True, [], True)[1]
     for hidden, pos in _steps(7, 2):
         a, b = stack.decode(hidden, pos, cache), stack.decode(hidden, pos, fresh)
@@ -160,3 +158,36 @@ def test_eviction_makes_room_in_a_full_cache():
         stack.decode(*next(steps), cache)
     cache.check()
     assert cache.rows(0, cache.seqused(0)).tolist() == [16 + 20, 30 + 12] and cache.seqused(0).tolist() == [36, 60]
+
+
+def test_eviction_right_after_the_prefill():
+    """by the weights of each request's last token, which the float64 recomputation of the drop layer's scores has as well"""
+    stack, cache, _, info = _prefill(False, [(1, 0.8)], True)
+    before = [_read(cache, layer, cache.seqused(layer).tolist()) for layer in range(L)]
+    w = recipe.small(lengths=LENGTHS, Hq=GEOM.Hq, Hkv=GEOM.Hkv, dk=GEOM.dk, hdim=GEOM.d, G=G, n=n, A=A, salt=257)
+    d = sgpu.to_device(gen.materialize(w))
+    _, info = stack.forward(d["hidden"], d["positions"], d["cu_seqlens"], max(LENGTHS), drops=[(1, 0.8)], G=G, n=n, A=A, keep_scored=True)
+    q = info[0]["scored"][0].double().cpu()
+    mass, _ = cache.records[1]
+    for r, N in enumerate(LENGTHS):
+        for hq in range(GEOM.Hq if N else 0):
+            at = sum(LENGTHS[:r + 1]) - 1
+            k = before[1][0][r][:, hq // 2]
+            p = torch.softmax(k @ q[at, hq] * GEOM.dk ** -0.5, 0)
+            if hq % 2 == 0:
+                want = p
+            else:
+                page = cache.block_table[r].long()[torch.arange(N, device="cuda") // cache.B]
+                got = mass[page, hq // 2, torch.arange(N, device="cuda") % cache.B].double().cpu()
+                assert torch.allclose(got, want + p, rtol=1e-4, atol=1e-9)
+    cache.evict(64, sinks=4, recent=16)
+    cache.check()
+    for layer in range(L):
+        had = torch.tensor([len(x) for x in before[layer][0]])
+        assert cache.rows(layer, cache.seqused(layer)).tolist() == had.clamp(max=64).tolist()
+    hidden, pos = next(_steps(9, 1))
+    got = stack.decode(hidden, pos, cache).double().cpu()
+    cache.check()
+    rows = [cache.rows(layer, cache.seqused(layer)).tolist() for layer in range(L)]
+    ref = _ref_decode(stack, hidden, pos.cpu(), [_read(cache, layer, rows[layer]) for layer in range(L)])
+    assert float(torch.linalg.norm(got - ref) / torch.linalg.norm(ref)) < REL_FRO
