@@ -404,7 +404,7 @@ up_status up_kv_mass(const uint16_t* q, int64_t q_stride, const up_kv_cache* cac
  *   new_len[r] = k.
  * moves: int32 [R, Hkv, max_moves, 2] (entries past num_moves are left alone), 8-byte aligned, NULL where max_moves = 0;
  * num_moves: int32 [R, Hkv];
- * new_len, budget, seqused: int32 [R].  budget, seqused and total are not written and new_len must not be one of them.
+ * new_len, budget, seqused: int32 [R].  budget, seqused and total are not written, and no output overlaps one of them (UP_ERR_ARG).
  * A request is left as it is (no moves, new_len = its length) where min(k, len - k) > max_moves
  * (UP_DEV_TOO_MANY_MOVES), budget[r] < 0 (UP_DEV_BAD_BUDGET) or a table entry in use lies outside [0, num_blocks)
  * (UP_DEV_BAD_PAGE; where all rows stay, or none, no entry is in use).  A seqused entry outside [0, max_blocks * B] sets

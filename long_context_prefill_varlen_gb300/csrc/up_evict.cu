@@ -732,6 +732,12 @@ static cudaError_t launch_move(const MoveArgs& a, cudaStream_t st) {
     return launch_pdl(move_kernel<LPR, SCALED>, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kMoveThreads), 0, st, a);
 }
 
+// whether n numbers at p and m at q have one in common
+static bool overlap(const int32_t* p, int64_t n, const int32_t* q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b ? b - a < static_cast<uint64_t>(n) * 4 : a - b < static_cast<uint64_t>(m) * 4;
+}
+
 // lists of requests and heads, positions of a request
 static bool fits(int R, int Hkv, int max_blocks, int B) {
     return (int64_t)R * Hkv <= (1 << 24) && (int64_t)max_blocks * B <= (1 << 30);
@@ -750,8 +756,13 @@ extern "C" up_status up_kv_evict(const float* mass, const int32_t* born, int64_t
     if (!mass || !born || !block_table || !seqused || !budget || !num_moves || !new_len || !dev_status) return UP_ERR_ARG;
     if (R <= 0 || Hkv <= 0 || max_blocks <= 0 || B <= 0 || B > (1 << 20) || num_blocks <= 0 || num_blocks > 0x7fffffff) return UP_ERR_ARG;
     if (sinks < 0 || recent < 0 || max_moves < 0 || (max_moves > 0 && !moves)) return UP_ERR_ARG;
-    if (new_len == seqused || new_len == budget || new_len == total) return UP_ERR_ARG;      // other heads' CTAs still read those
     if (!fits(R, Hkv, max_blocks, B) || reinterpret_cast<uintptr_t>(moves) % 8) return UP_ERR_SHAPE;
+    // a finished list's outputs must not be what the other lists, or CTAs of a cluster, still read their length and budget from
+    const int64_t list_words = (int64_t)R * Hkv * std::min<int64_t>(max_moves, int64_t{1} << 35) * 2;
+    for (const int32_t* in : {seqused, budget, total})
+        if (in && (overlap(new_len, R, in, R) || overlap(num_moves, (int64_t)R * Hkv, in, R) ||
+                   (moves && overlap(moves, list_words, in, R))))
+            return UP_ERR_ARG;
     Args a{};
     a.mass = mass;
     a.born = born;

@@ -90,8 +90,8 @@ def test_what_rope_refuses(up):
 
 MASS = dict(q=A, q_stride=512, cache=None, table=A, seqused=A, lse=A, R=2, max_blocks=4, Hq=4, scale=0.1, counted=None,
             total=None, decay=1.0, mass=A, mass_out=A, born=A, status=A, stream=None)
-EVICT = dict(mass=A, born=A, num_blocks=8, Hkv=2, B=16, table=A, seqused=A, budget=2 * A, R=2, max_blocks=4, total=None,
-             sinks=0, recent=0, moves=A, max_moves=10, num_moves=A, new_len=3 * A, status=A, stream=None)
+EVICT = dict(mass=A, born=A, num_blocks=8, Hkv=2, B=16, table=A, seqused=4 * A, budget=2 * A, R=2, max_blocks=4, total=None,
+             sinks=0, recent=0, moves=256 * A, max_moves=10, num_moves=A, new_len=3 * A, status=A, stream=None)
 MOVE = dict(cache=None, table=A, R=2, max_blocks=4, moves=A, max_moves=10, num_moves=A, mass=None, born=None, status=A,
             stream=None)
 
@@ -125,10 +125,14 @@ def test_what_evict_refuses(up):
     for name in ("mass", "born", "table", "seqused", "budget", "moves", "num_moves", "new_len", "status"):
         assert call(**{name: None}) == up.UP_ERR_ARG, name
     for bad in (dict(R=0), dict(Hkv=0), dict(max_blocks=0), dict(B=0), dict(B=(1 << 20) + 1), dict(num_blocks=0),
-                dict(num_blocks=1 << 31), dict(sinks=-1), dict(recent=-1), dict(max_moves=-1), dict(new_len=A),
-                dict(new_len=2 * A), dict(total=3 * A)):
+                dict(num_blocks=1 << 31), dict(sinks=-1), dict(recent=-1), dict(max_moves=-1)):
         assert call(**bad) == up.UP_ERR_ARG, bad
-    for bad in (dict(max_blocks=(1 << 26) + 1), dict(R=1 << 24), dict(moves=A + 4)):
+    # an output that is, or runs into, what other CTAs still read (R = 2: 8 bytes of lengths, 16 of counts, 320 of moves)
+    for bad in (dict(new_len=4 * A), dict(new_len=2 * A), dict(total=3 * A), dict(new_len=4 * A + 4), dict(new_len=4 * A - 4),
+                dict(num_moves=2 * A - 12), dict(num_moves=4 * A + 4), dict(total=A + 12), dict(moves=4 * A - 312),
+                dict(moves=2 * A), dict(total=256 * A + 316), dict(max_moves=1 << 62, budget=300 * A)):
+        assert call(**bad) == up.UP_ERR_ARG, bad
+    for bad in (dict(max_blocks=(1 << 26) + 1), dict(R=1 << 24), dict(moves=256 * A + 4)):
         assert call(**bad) == up.UP_ERR_SHAPE, bad
 
 
@@ -141,7 +145,7 @@ def test_what_move_refuses(up):
         assert call(**{name: None}) == up.UP_ERR_ARG, name
     for bad in (dict(R=0), dict(max_blocks=0), dict(max_moves=-1)):
         assert call(**bad) == up.UP_ERR_ARG, bad
-    for bad in (dict(max_blocks=(1 << 26) + 1), dict(R=1 << 24), dict(moves=A + 4)):
+    for bad in (dict(max_blocks=(1 << 26) + 1), dict(R=1 << 24), dict(moves=256 * A + 4)):
         assert call(**bad) == up.UP_ERR_SHAPE, bad
     assert call(max_moves=0) == up.UP_OK and call(max_moves=0, moves=None) == up.UP_OK       # room for no move: none
 
@@ -209,7 +213,7 @@ def _calls(m, up):
                                                                          A, A, A, A, None)
             yield lambda cache=cache: m.up_kv_move(ctypes.byref(cache), A, 2, 4, A, 10, A, None, None, A, None)
     for R, max_blocks in ((1, 4), (1, 60000), (300, 4), (300, 2000), (60, 1500)):
-        yield lambda R=R, max_blocks=max_blocks: m.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None)
+        yield lambda R=R, max_blocks=max_blocks: m.up_kv_evict(A, A, 8, 2, 16, A, 4 * A, 2 * A, R, max_blocks, None, 0, 0, 256 * A, 10, A, 3 * A, A, None)
 
 
 def test_every_call_launches_on_every_device_and_an_error_is_its_own(lib, up):
@@ -225,7 +229,7 @@ def test_a_list_goes_to_a_cluster_where_it_is_worth_one(lib, up):
     for R, max_blocks, cluster in ((1, 4, 1), (1, 60000, 16), (1, 16384, 8), (1, 300, 1), (300, 4, 1), (300, 2000, 2), (300, 60000, 8), (30, 1000, 2)):
         wide = (R, max_blocks) == (300, 60000)                   # short lists first, a CTA each
         lib.fake_reset(42, 16)
-        assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
+        assert lib.up_kv_evict(A, A, 8, 2, 16, A, 4 * A, 2 * A, R, max_blocks, None, 0, 0, 256 * A, 10, A, 3 * A, A, None) == 0
         assert [lib.fake_launch_cluster(i) for i in range(lib.fake_launches())] == [1] * wide + [cluster], (R, max_blocks)
 
 
@@ -235,6 +239,6 @@ def test_a_cluster_that_the_device_cannot_place_is_a_smaller_one(lib, up, larges
     for R, max_blocks, cluster in ((1, 60000, 16), (1, 500, 8), (300, 2000, 2), (1, 4, 1), (300, 60000, 8)):
         for _ in range(2):
             lib.fake_reset(43 + largest, largest)
-            assert lib.up_kv_evict(A, A, 8, 2, 16, A, A, 2 * A, R, max_blocks, None, 0, 0, A, 10, A, 3 * A, A, None) == 0
+            assert lib.up_kv_evict(A, A, 8, 2, 16, A, 4 * A, 2 * A, R, max_blocks, None, 0, 0, 256 * A, 10, A, 3 * A, A, None) == 0
             n = lib.fake_launches()
             assert (n, lib.fake_launch_cluster(n - 1)) == (1 + ((R, max_blocks) == (300, 60000)), min(cluster, largest)), (R, max_blocks)
