@@ -362,7 +362,7 @@ class RandomLlamaStack:
             slots = cache.slots(cu, T)
         for layer in range(upto):
             x, q, kk = self.attention_sublayer(layer, h, pos, cu, max_len, cache, slots)
-            if cache is not None and cache.weigh:
+            if cache is not None and cache.weigh and T:
                 lens = cu.diff()
                 last = q[(cu[1:].long() - 1).clamp(min=0)]         # of a request without tokens: anybody's, it sees nothing
                 cache.attend(layer, last, lens, self.g.dk ** -0.5, lens)

@@ -39,3 +39,29 @@ def test_a_geometry_with_a_plan():
     geom = ls.with_rope(ls.LLAMA_3_1_8B, scaling="bands", factor=8.0, original_len=8192)
     assert (geom.rope.rot, geom.rope.layout, geom.rope.gain) == (128, 0, 1.0) and ls.LLAMA_3_1_8B.rope is None
     assert geom.d == ls.LLAMA_3_1_8B.d and ls.with_rope(geom, rot=32, layout="pairs").rope.rot == 32
+
+
+def test_a_prompt_of_no_tokens_weighs_nothing(monkeypatch):
+    """(there is no last token to take)"""
+    class Cache(ls.StackCache):
+        def slots(self, cu, T):
+            return None
+
+        def write(self, *a):
+            pass
+
+        def check(self, stream=None):
+            pass
+
+        def attend(self, *a):
+            raise AssertionError("weighed")
+    monkeypatch.setattr(ls, "varlen_causal_attention", lambda q, *a: q)
+    geom = ls.StackGeometry(d=64, Hq=2, Hkv=1, dk=64, ffn=64)
+    cache = Cache(1, 2, 1, 64, 16, device="cpu", weigh=True)
+    stack = ls.RandomLlamaStack(1, geom, device="cpu")
+    h = torch.empty(0, 64, dtype=torch.bfloat16)
+    out, _ = stack.forward(h, torch.empty(0, dtype=torch.int64), torch.zeros(3, dtype=torch.int32), 0, cache=cache)
+    assert out.shape == (0, 64) and cache.weighed
+    with pytest.raises(AssertionError, match="weighed"):
+        stack.forward(torch.zeros(3, 64, dtype=torch.bfloat16), torch.arange(3), torch.tensor([0, 3, 3], dtype=torch.int32), 3,
+                      cache=cache)
