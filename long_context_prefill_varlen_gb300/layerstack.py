@@ -214,7 +214,8 @@ class StackCache:
 
     def evict(self, budget, sinks=0, recent=0):
         """Leave each request at most `budget` tokens (a number, or int32 [R]) at every layer and key head: its first
-        `sinks` and last `recent` before the others, those by their weight.  Between decode steps; the host does not wait."""
+        `sinks` and last `recent` before the others, those by their weight.  Between decode steps; the host does not wait.
+        A request that has outgrown the cache loses nothing and has none of its steps' outputs until the next prefill."""
         if not self.weigh:
             raise ValueError("evict() needs a cache that weighs its tokens (weigh=True)")
         if not self.weighed:
@@ -232,10 +233,11 @@ class StackCache:
         num = torch.empty(self.R, Hkv, device=dev, dtype=torch.int32)
         for layer, ((kc, vc, scales), (mass, born)) in enumerate(zip(self.layers, self.records)):
             seqused = self.seqused(layer)
-            left = torch.empty_like(seqused)
-            up_kv_evict(mass, born, self.block_table, self.rows(layer, seqused), budget, moves, num, left, self.status,
-                        total=seqused, sinks=sinks, recent=recent)
+            rows, left = self.rows(layer, seqused), torch.empty_like(seqused)
+            up_kv_evict(mass, born, self.block_table, rows, budget, moves, num, left, self.status, total=seqused, sinks=sinks,
+                        recent=recent)
             up_kv_move(kc, vc, self.block_table, moves, num, self.status, mass=mass, born=born, **scales)
+            left = torch.where(rows > cap, rows, left)       # more rows than pages: up_kv_evict counts none, and reports it
             self.evicted[layer].copy_(seqused - left)
             self.counted[layer].copy_(left)
 

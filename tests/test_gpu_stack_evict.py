@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from long_context_prefill_varlen_gb300 import layerstack as ls
+from long_context_prefill_varlen_gb300 import layerstack as ls, up_read_status
 from synth import cpu as gen
 from synth import gpu as sgpu
 from synth import recipe
@@ -191,3 +191,30 @@ def test_eviction_right_after_the_prefill():
     rows = [cache.rows(layer, cache.seqused(layer)).tolist() for layer in range(L)]
     ref = _ref_decode(stack, hidden, pos.cpu(), [_read(cache, layer, rows[layer]) for layer in range(L)])
     assert float(torch.linalg.norm(got - ref) / torch.linalg.norm(ref)) < REL_FRO
+
+
+def test_a_request_that_has_outgrown_the_cache_keeps_its_rows():
+    """one step too many, then an eviction: the request's rows and records stay, the other request's go, and the coming steps have
+    what they have without the eviction where it takes nothing"""
+    lengths, outs = (16, 40), []
+    for evict in (False, True):
+        stack, cache, _, _ = _prefill(True, [], True, lengths=lengths)         # 48 rows a request
+        steps = _steps(8, 11, lengths)
+        for _ in range(9):
+            stack.decode(*next(steps), cache)
+        assert up_read_status(cache.status) != 0                               # 49 tokens
+        pages = cache.block_table[1].long()
+
+        def held():
+            tensors = [x for k, v, s in cache.layers for x in (k.view(torch.uint8), v.view(torch.uint8), *s.values())]
+            return [x[pages].clone() for x in tensors + [x for pair in cache.records for x in pair]]
+        before = held()
+        if evict:
+            cache.evict(20, recent=4)
+            assert cache.evicted.tolist() == [[5, 0]] * L and all(torch.equal(x, y) for x, y in zip(before, held()))
+            assert [cache.rows(layer, cache.seqused(layer)).tolist() for layer in range(L)] == [[20, 49]] * L
+        outs.append([stack.decode(*next(steps), cache) for _ in range(2)])
+        with pytest.raises(RuntimeError):
+            cache.check()
+    for x, y in zip(*outs):
+        assert torch.equal(x[1], y[1])

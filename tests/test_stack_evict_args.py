@@ -65,3 +65,32 @@ def test_a_prompt_of_no_tokens_weighs_nothing(monkeypatch):
     with pytest.raises(AssertionError, match="weighed"):
         stack.forward(torch.zeros(3, 64, dtype=torch.bfloat16), torch.arange(3), torch.tensor([0, 3, 3], dtype=torch.int32), 3,
                       cache=cache)
+
+
+class _Calls:
+    """What an eviction on the CPU asks of the library, answered by up_kv_evict's rules for a request's length."""
+
+    def __init__(self, monkeypatch, had):
+        self.budgets, self.rows = [], []
+        monkeypatch.setattr(ls, "up_seqused", lambda kept, drop, layer, orig, kv_len, out: out.copy_(torch.tensor(had[layer])))
+        monkeypatch.setattr(ls, "up_kv_evict", self.evict)
+        monkeypatch.setattr(ls, "up_kv_move", lambda *a, **kw: None)
+
+    def evict(self, mass, born, table, rows, budget, moves, num, new_len, status, total, sinks, recent):
+        cap = table.shape[1] * mass.shape[2]
+        self.budgets.append(budget.tolist())
+        self.rows.append(rows.tolist())
+        new_len.copy_(torch.where((rows < 0) | (rows > cap), 0, torch.minimum(rows, budget)))
+
+
+def test_a_request_that_has_outgrown_the_cache_keeps_its_rows(monkeypatch):
+    """(tables of 16 rows)"""
+    calls = _Calls(monkeypatch, [[17, 10], [12, 3], [40, 30]])
+    cache = _cache(True)
+    cache.weighed = True
+    cache.evicted[2] = torch.tensor([20, 20], dtype=torch.int32)         # of its 40 tokens a layer still holds 20
+    cache.evict(8)
+    assert calls.rows == [[17, 10], [12, 3], [20, 10]]
+    assert cache.evicted.tolist() == [[0, 2], [4, 0], [20, 22]]
+    cache.evict(8)                                                       # nor does it a second time
+    assert calls.rows[3:] == [[17, 8], [8, 3], [20, 8]] and cache.evicted.tolist() == [[0, 2], [4, 0], [20, 22]]
