@@ -195,8 +195,15 @@ class StackCache:
         """Those of them that the cache still holds."""
         return seqused - self.evicted[layer] if self.weigh else seqused
 
-    def attend(self, layer, q, rows, sm_scale, seqused=None):
-        """Attention of q over the layer's rows; with weigh, their records follow (seqused: Eq. 17's number of tokens)."""
+    def attend(self, layer, q, rows=None, sm_scale=None, seqused=None):
+        """Attention of q over the layer's rows; with weigh, their records follow.  rows: the tokens that the cache holds;
+        seqused: those that the layer has had (Eq. 17).  Either follows from the other; sm_scale: dk^-0.5 where None."""
+        if rows is None and seqused is None:
+            raise ValueError("attend() needs rows or seqused")
+        if rows is None:
+            rows = self.rows(layer, seqused)
+        elif seqused is None and self.weigh:
+            seqused = rows + self.evicted[layer]
         kc, vc, scales = self.layers[layer]
         R, Hq, dk = q.shape
         nbytes = up_paged_decode_workspace_bytes(R, Hq, kc.shape[1], dk, self.B, self.max_blocks)

@@ -218,3 +218,20 @@ def test_a_request_that_has_outgrown_the_cache_keeps_its_rows():
             cache.check()
     for x, y in zip(*outs):
         assert torch.equal(x[1], y[1])
+
+
+def test_attention_without_the_number_of_tokens():
+    """a new row's number is that in the layer's stream, after an eviction too"""
+    stack, cache, _, _ = _prefill(True, [], True, lengths=(16, 40))
+    stack.decode(*next(_steps(8, 1, (16, 40))), cache)
+    cache.evict(10)
+    cache.kv_len.add_(1)
+    q = torch.randn(2, GEOM.Hq, GEOM.dk, device="cuda").to(torch.bfloat16)
+    for layer, how in enumerate(("rows", "seqused", "both")):
+        seqused = cache.seqused(layer)
+        rows = cache.rows(layer, seqused)
+        assert rows.tolist() == [11, 11]
+        cache.attend(layer, q, **{"rows": dict(rows=rows), "seqused": dict(seqused=seqused), "both": dict(rows=rows, seqused=seqused)}[how])
+        born = cache.records[layer][1][cache.block_table[:, 0].long(), :, 10]
+        assert born.tolist() == [[17] * GEOM.Hkv, [41] * GEOM.Hkv] and cache.counted[layer].tolist() == [11, 11]
+    cache.check()

@@ -94,3 +94,30 @@ def test_a_request_that_has_outgrown_the_cache_keeps_its_rows(monkeypatch):
     assert cache.evicted.tolist() == [[0, 2], [4, 0], [20, 22]]
     cache.evict(8)                                                       # nor does it a second time
     assert calls.rows[3:] == [[17, 8], [8, 3], [20, 8]] and cache.evicted.tolist() == [[0, 2], [4, 0], [20, 22]]
+
+
+@pytest.mark.parametrize("weigh", [False, True])
+def test_attention_by_the_rows_or_by_the_tokens(monkeypatch, weigh):
+    """either gives the other, what was evicted between them"""
+    asked = []
+    monkeypatch.setattr(ls, "up_paged_decode_workspace_bytes", lambda *a: 16)
+    monkeypatch.setattr(ls, "up_paged_decode", lambda q, k, v, table, rows, *a, sm_scale, **kw: asked.append((rows.tolist(), sm_scale)))
+    monkeypatch.setattr(ls, "up_kv_mass", lambda q, k, v, table, rows, *a, sm_scale, counted, total, **kw: asked.append(
+        (rows.tolist(), sm_scale, counted.tolist(), total.tolist())))
+    cache, q = _cache(weigh), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    gone = torch.tensor([3, 0], dtype=torch.int32)
+    if weigh:
+        cache.evicted[1] = gone
+    had = torch.tensor([9, 5], dtype=torch.int32)
+    rows = had - gone if weigh else had
+    for how in (dict(rows=rows), dict(seqused=had), dict(rows=rows, seqused=had)):
+        asked.clear()
+        cache.attend(1, q, sm_scale=0.5, **how)
+        if weigh:
+            assert asked == [(rows.tolist(), 0.5), (rows.tolist(), 0.5, [0, 0], had.tolist())]
+            assert cache.counted.tolist() == [[0, 0], rows.tolist(), [0, 0]]
+            cache.counted.zero_()
+        else:
+            assert asked == [(rows.tolist(), 0.5)]
+    with pytest.raises(ValueError, match="rows or seqused"):
+        cache.attend(1, q, sm_scale=0.5)
