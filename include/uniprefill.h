@@ -385,8 +385,8 @@ up_status up_rope(const up_rope_table* plan, const uint16_t* q, int64_t q_stride
  *   mass_out = decay * mass + sum_{h of the key head} exp(q[r, h] . K_i * sm_scale - lse[r, h])   for i in [0, seqused[r]).
  * Rows at positions i >= counted[r] (int32 [R], optional: NULL means that every row has been counted before) are new: they
  * start from 0, whatever mass holds, and get born = total[r] - seqused[r] + i, total[r] (int32 [R], optional; NULL means
- * seqused) being the tokens that the layer's stream has had.  A head whose lse is infinite adds nothing.  mass_out may be mass; apart
- * from that they do not overlap.  Records at other positions are left alone.
+ * seqused) being the tokens that the layer's stream has had.  A head whose lse is infinite adds nothing, and a
+ * score of -inf has no weight.  mass_out may be mass; apart from that they do not overlap.  Records at other positions are left alone.
  * decay in [0, 1].  A seqused entry outside [0, max_blocks * B] sets UP_DEV_BAD_LENGTH and counts as 0; a row whose table
  * entry lies outside [0, num_blocks) sets UP_DEV_BAD_PAGE and has no record.
  * Arithmetic: as up_paged_decode's scores; weights and sums in fp32, the heads' in a fixed order. */

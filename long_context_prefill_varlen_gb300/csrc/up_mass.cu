@@ -16,6 +16,7 @@
 // heads of 128 in e4m3, 58 us, 5.3 TB/s; 32 of up to 16K, 8 heads of 256 in bf16 112 us (6.2), in e4m3 63 us (5.6); 32 of up to
 // 32K, 32 query heads on one of 128 in bf16, 22 us (3.9; the heads' exponentials are four times the work per byte).  One
 // request of 4K takes 4.6 us, a chain of latencies (its length, its pages, the copies).
+#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -44,7 +45,7 @@ struct Args {
     int32_t* born;
     int64_t records;
     int R, max_blocks, Hq, group;
-    float scale_hi, scale_lo;  // sm_scale * log2 e, in two parts
+    float scale_hi, scale_lo;  // sm_scale * log2 e, in two parts of one sign
     float decay;
     FastDiv by_b;
     int32_t* status;
@@ -522,8 +523,10 @@ extern "C" up_status up_kv_mass(const uint16_t* q, int64_t q_stride, const up_kv
     a.max_blocks = max_blocks;
     a.Hq = Hq;
     a.group = Hq / cache->Hkv;
+    // both parts of one sign, the second never zero: a score of -inf would be NaN with parts that pull apart
     const double scale = sm_scale * 1.4426950408889634;
     a.scale_hi = static_cast<float>(scale);
+    if (fabs(static_cast<double>(a.scale_hi)) >= fabs(scale)) a.scale_hi = nextafterf(a.scale_hi, 0.f);
     a.scale_lo = static_cast<float>(scale - a.scale_hi);
     a.decay = decay;
     a.by_b = kv::fast_div(cache->B);

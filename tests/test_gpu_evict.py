@@ -134,6 +134,33 @@ def test_a_head_without_weight_and_one_whose_lse_is_not_a_number():
     assert torch.isfinite(mass[page, :, off]).all()
 
 
+@pytest.mark.parametrize("dk", [64, 128, 256])
+@pytest.mark.parametrize("sm_scale", [None, 0.3, -0.3, -0.088388346])
+def test_scores_of_minus_infinity_have_no_weight(sm_scale, dk):
+    """as in up_paged_decode, whose lse is that of the other rows; the scale's two parts may be of either sign"""
+    lens, gone = (200, 33), ((0, 7, 100, 199), (32,))
+    c, table, rows, qb = _decode_case(11, 8, 2, dk, 16, lens, False)
+    q = kv_ref.bf16_value(qb)
+    q[:, :, 5] = np.abs(q[:, :, 5]) + 0.5
+    qb = kv_ref.bf16_bits(q.astype(np.float32))
+    q = kv_ref.bf16_value(qb)
+    scale = dk ** -0.5 if sm_scale is None else sm_scale
+    for r, at in enumerate(gone):
+        s = rows[r][list(at)]
+        c.k[torch.from_numpy(s // 16).cuda(), :, torch.from_numpy(s % 16).cuda(), 5] = -math.inf if scale > 0 else math.inf
+    status, _, lse = _run_decode(c, table, lens, _from_bits(qb), sm_scale=sm_scale)
+    assert status == 0 and torch.isfinite(lse).all()
+    mass, born = _records(c, 1)
+    old = mass.clone()
+    assert _mass(c, table, lens, _from_bits(qb), lse, mass, born, sm_scale=sm_scale) == 0
+    for r, at in enumerate(gone):
+        s, rest = rows[r][list(at)], np.delete(rows[r], at)
+        assert torch.equal(mass[s // 16, :, s % 16], old[s // 16, :, s % 16])
+        w, tol = evict_ref.weights(q[r], c.rows("k", rest), lse[r].cpu().numpy().astype(np.float64), scale)
+        was, got = (x[rest // 16, :, rest % 16].cpu().numpy().T.astype(np.float64) for x in (old, mass))
+        assert (np.abs(got - was - w) <= tol + 2 * F32 * (was + w)).all()
+
+
 def test_many_requests_and_none_of_their_neighbours():
     """a request's weights do not depend on the batch; more requests than a warp has lanes; a long one among them"""
     lens = tuple([0, 3, 100] * 30 + [5000, 0, 0, 64])
