@@ -229,7 +229,7 @@ class StackCache:
             raise ValueError("no prefill has filled the cache: there are no tokens with weights")
         dev, cap = self.kv_len.device, self.max_blocks * self.B
         if not isinstance(budget, torch.Tensor):
-            budget = int(budget)
+            budget = min(int(budget), cap)         # (32 bits hold it)
             if budget < 0:
                 raise ValueError(f"a budget of {budget} tokens")
             most, budget = min(budget, cap // 2), torch.full((self.R,), budget, device=dev, dtype=torch.int32)

@@ -96,6 +96,16 @@ def test_a_request_that_has_outgrown_the_cache_keeps_its_rows(monkeypatch):
     assert calls.rows[3:] == [[17, 8], [8, 3], [20, 8]] and cache.evicted.tolist() == [[0, 2], [4, 0], [20, 22]]
 
 
+@pytest.mark.parametrize("budget", [16, 17, (1 << 31) - 1, 1 << 31, 1 << 40])
+def test_a_budget_of_any_size(monkeypatch, budget):
+    """more than the cache holds is all of it"""
+    calls = _Calls(monkeypatch, [[16, 10], [12, 3], [0, 1]])
+    cache = _cache(True)
+    cache.weighed = True
+    cache.evict(budget)
+    assert calls.budgets == [[16, 16]] * 3 and not cache.evicted.any()
+
+
 @pytest.mark.parametrize("weigh", [False, True])
 def test_attention_by_the_rows_or_by_the_tokens(monkeypatch, weigh):
     """either gives the other, what was evicted between them"""
