@@ -366,6 +366,22 @@ def test_protected_rows_that_fit_and_that_do_not(sinks, recent):
     _check_choice(5, lens, (100, 500, 1999, 7), sinks=sinks, recent=recent, total=(500, 1000, 50_000, 51), values=EDGES["few_values"])
 
 
+@pytest.mark.parametrize("name,other", [("sinks", "recent"), ("recent", "sinks")])
+def test_protected_rows_of_any_number(name, other):
+    """beyond 32 bits, too: all rows, which then go by mass, and the other kind of protection makes no difference"""
+    lens, budget = (100, 300), (30, 200)
+    md, bd, table, *want = _check_choice(12, lens, budget, **{name: (1 << 31) - 1, other: 20})
+    few = _check_choice(12, lens, budget, **{other: 20})
+    assert not torch.equal(want[0], few[3])
+    for number in (1 << 31, 1 << 32, 1 << 40):
+        status, *got = _choose(md, bd, table, lens, budget, **{name: number, other: 20})
+        assert status == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+    for number in (-1, -(1 << 32)):
+        with pytest.raises(up.UpError) as e:
+            _choose(md, bd, table, lens, budget, **{name: number})
+        assert e.value.code == up.UP_ERR_ARG
+
+
 def test_requests_that_are_left_as_they_are():
     rng = np.random.default_rng(6)
     lens, B = (100, 200, 300, 50), 16
