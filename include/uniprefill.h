@@ -366,8 +366,10 @@ up_status up_rope_plan(int rot, double theta, int layout, int scaling, double fa
  * positions: int64 [T], any value.  dk in {64, 128, 256}, plan->rot <= dk.
  * Tokens t < *num_tokens (or < T if num_tokens is NULL; a count outside [0, T] sets UP_DEV_BAD_TOKEN_COUNT and nothing is
  * written); the rows of the others are left alone.
- * Arithmetic: angles in 64-bit fixed point modulo a turn (errors of a few 2^-53 of the angle and of 2^-32 turn, however far the
- * position), cosine, sine and the products in fp32, one rounding to bf16. */
+ * Arithmetic: an angle is the position times the table's 64-bit fraction of a turn, modulo a turn, in whole numbers, so what
+ * it is off comes from the table and grows with the position: |positions[t]| * 2^-65 turn by the fraction's last bit (2^-32
+ * turn at 2^33 positions), and some (4 + ln theta) 2^-53 of the whole angle by f_j in double precision.  Within its turn the angle
+ * is cut to 2^-32 turn and rounded to fp32 (2^-26 turn at most); cosine, sine and the products are in fp32, with one rounding to bf16. */
 up_status up_rope(const up_rope_table* plan, const uint16_t* q, int64_t q_stride, uint16_t* q_out, int64_t q_out_stride,
                   int Hq, const uint16_t* k, int64_t k_stride, uint16_t* k_out, int64_t k_out_stride, int Hkv, int dk,
                   const int64_t* positions, int64_t T, const int32_t* num_tokens, int transpose, int32_t* dev_status,

@@ -4,8 +4,9 @@
 //
 // Pair j of a head turns by x = pos * f_j.  What counts of x is its place within a turn, so the angle is computed as
 // turns in 64-bit fixed point: pos * turns_j modulo 2^64, one integer product whose wrap drops the whole turns, for any
-// position and sign.  Its upper 32 bits, as a signed number, are the angle in [-pi, pi) to 2^-32 turn; with 32-bit floats
-// a position of 100,000 leaves an angle of the fastest pair 2^-8 off.
+// position and sign; the table's last bit leaves |pos| 2^-65 turn.  The upper 32 bits, as a signed number, are the angle in
+// [-pi, pi), rounded to the 24 bits of a float for the sine and cosine (pi 2^-24 at most, far below bf16's steps).  With 32-bit
+// floats throughout, a position of 100,000 leaves the angles of pairs next to the fastest some 2^-8 off.
 //
 // The kernel moves bytes (4 dk a row of a head) and HBM bounds it: a thread owns 8 pairs of a token (two 16-byte vectors
 // rot/2 numbers apart, in either layout), finds their sines once and turns the pairs of several heads with them, all of

@@ -3,6 +3,7 @@ the CPU (test infrastructure), and the tolerances."""
 from __future__ import annotations
 
 import math
+from decimal import Decimal, localcontext
 
 import numpy as np
 
@@ -35,6 +36,23 @@ def frequencies(rot, theta, scaling="none", factor=1.0, original_len=0, low=None
             x = x / factor * r + x * (1 - r)
         f.append(x)
     return np.array(f)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def exact_turns(rot, theta, factor=1):
+    """turns per position of every pair, f_j / (2 pi factor), to 80 digits"""
+    with localcontext() as c:
+        c.prec = 80
+        return [Decimal(theta) ** (Decimal(-2 * j) / rot) / (2 * PI * factor) for j in range(rot // 2)]
+
+
+def turns_off(f, theta, position=1):
+    """How many turns a position's angle may be off by the table: half of its last bit, and f [turns per position] in double
+    precision: an exponent rounded by 2^-53 (ln theta times as much of f, the exponent being below 1), a power (2 halves of a
+    step), 2 pi, a division by it and one by the scaling's factor."""
+    return abs(position) * (2.0 ** -65 + (math.log(theta) + 5) * 2.0 ** -53 * float(f))
 
 
 def turned(x, turns, gain, layout, transpose=False):

@@ -2,6 +2,7 @@
 up_rope_plan makes, and the references of their GPU tests (no GPU needed)."""
 import ctypes
 import math
+from decimal import Decimal
 
 import numpy as np
 import pytest
@@ -27,6 +28,13 @@ def test_the_plans_turns_are_the_formulas(up, rot, theta, scaling, factor, lengt
     want = 1 + math.log(factor) / 10 if scaling == "ramp" else 1.0
     assert plan.gain == pytest.approx(want, rel=2.0 ** -23)
     assert (plan.rot, plan.layout) == (rot, 0) and not any(plan.turns[rot // 2:])
+
+
+@pytest.mark.parametrize("rot,theta,factor", [(128, 500000.0, 1), (64, 10000000.0, 4), (16, 10000.0, 1), (256, 1.5, 8), (256, 1e300, 1)])
+def test_the_plans_turns_to_their_last_bit(up, rot, theta, factor):
+    plan = up.up_rope_plan(rot, theta=theta, scaling="linear" if factor > 1 else "none", factor=factor)
+    for j, f in enumerate(evict_ref.exact_turns(rot, theta, factor)):
+        assert abs(float(f - Decimal(plan.turns[j]) / (1 << 64))) <= evict_ref.turns_off(f, theta), j
 
 
 def test_a_plans_own_turns_and_gain(up):

@@ -1,6 +1,7 @@
 """up_rope on the GPU against 64-bit rotations on the CPU: layouts, parts of the head, scalings, positions from negative to
 far beyond 32 bits, strides, single tokens, in place, the gradient, counts on the device."""
 import math
+from decimal import localcontext
 
 import numpy as np
 import pytest
@@ -85,6 +86,25 @@ def test_positions_of_any_size_and_sign():
         plan = up.up_rope_plan(128, theta=10000.0, layout=layout)
         qo, _ = _call(plan, torch.tensor(pos, device="cuda"), q, None)
         _check(qo, q, _turns(plan, pos), plan, layout)
+
+
+@pytest.mark.parametrize("theta,factor", [(500000.0, 1), (10000.0, 1), (10000000.0, 8)])
+def test_far_positions_against_angles_of_80_digits(theta, factor):
+    """frequencies that are not the plan's own: off by what its table is, times the position"""
+    pos = [100_000, 131_071, -10_000_019, (1 << 31) + 77, (1 << 33) + 5, -(1 << 37) + 1, (1 << 40) + 12345, -(1 << 44) - 3]
+    rot = 128
+    plan = up.up_rope_plan(rot, theta=theta, scaling="linear" if factor > 1 else "none", factor=factor)
+    f = evict_ref.exact_turns(rot, theta, factor)
+    with localcontext() as c:
+        c.prec = 80
+        turns = np.array([[float((p * x) % 1) for x in f] for p in pos])
+    off = np.array([[evict_ref.turns_off(x, theta, p) for x in f] for p in pos])
+    q = _stream(np.random.default_rng(9), len(pos), 3, 128)
+    got, _ = _call(plan, torch.tensor(pos, device="cuda"), q, None)
+    x = np.abs(kv_ref.bf16_value(_bits(q)))
+    y, tol = evict_ref.turned(kv_ref.bf16_value(_bits(q)), turns, 1.0, "halves")
+    far = 2 * math.pi * np.concatenate((off, off), 1)[:, None] * (x + np.roll(x, 64, -1))
+    assert (np.abs(kv_ref.bf16_value(_bits(got)) - y) <= tol + (1 + kv_ref.BF16) * far).all()
 
 
 def test_the_gradient_by_differences():
