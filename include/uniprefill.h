@@ -361,8 +361,9 @@ up_status up_rope_plan(int rot, double theta, int layout, int scaling, double fa
  * transpose != 0 turns by -x, which is the gradient of the above (and its inverse, times gain^2).  The head's
  * numbers past rot are copied.
  * q [T, Hq, dk] -> q_out, k [T, Hkv, dk] -> k_out (bf16): token t's heads lie packed at q + t * q_stride (strides in
- * elements, multiples of 8, >= heads * dk when T > 1), 16-byte aligned.  q_out may be q, with the same stride; apart from
- * that no output overlaps an input or the other output.  Either pair may be NULL.
+ * elements, multiples of 8, >= heads * dk when T > 1), 16-byte aligned.  q_out may be q and k_out may be k, with the same
+ * stride; apart from that no head of an output overlaps one of an input or of the other output (q and k may be different heads
+ * of one buffer).  Either pair may be NULL.
  * positions: int64 [T], any value.  dk in {64, 128, 256}, plan->rot <= dk.
  * Tokens t < *num_tokens (or < T if num_tokens is NULL; a count outside [0, T] sets UP_DEV_BAD_TOKEN_COUNT and nothing is
  * written); the rows of the others are left alone.
@@ -422,6 +423,7 @@ up_status up_kv_evict(const float* mass, const int32_t* born, int64_t num_blocks
  * other list no position may be moved to twice, or be both moved from and moved to.
  * A move from or to a position outside [0, max_blocks * B), or on a table entry outside [0, num_blocks), is skipped and sets
  * UP_DEV_BAD_SLOT or UP_DEV_BAD_PAGE; a num_moves entry outside [0, max_moves] sets UP_DEV_TOO_MANY_MOVES and moves nothing of its head.
+ * max_moves = 0: nothing is launched, and num_moves is not looked at.
  * R * Hkv at most 2^24, max_blocks * B at most 2^30 (UP_ERR_SHAPE otherwise). */
 up_status up_kv_move(const up_kv_cache* cache, const int32_t* block_table, int R, int max_blocks, const int32_t* moves,
                      int64_t max_moves, const int32_t* num_moves, float* mass, int32_t* born, int32_t* dev_status,

@@ -367,7 +367,7 @@ def _launch(stream, *tensors):
 def up_rope(plan, positions, dev_status, q=None, q_out=None, k=None, k_out=None, num_tokens=None, transpose=False,
             stream=None):
     """q [T, Hq, dk] -> q_out, k [T, Hkv, dk] -> k_out (either pair may be None), turned by positions [T] int64;
-    q_out may be q.  transpose: the gradient of that."""
+    q_out may be q, and k_out k.  transpose: the gradient of that."""
     T = positions.numel()
     assert (q is None) == (q_out is None) and (k is None) == (k_out is None)
     assert positions.dtype is _I64 and positions.is_contiguous()
