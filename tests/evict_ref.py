@@ -111,3 +111,31 @@ def evict(mass, born, total, k, sinks, recent):
     holes = [i for i in range(k) if i not in stay]
     assert len(tails) == len(holes)
     return list(zip(tails, holes))
+
+
+# The forms that up_kv_evict's rule takes on a GPU of 152 SMs, by lists (requests and heads) and the tables' width: warps of a CTA,
+# CTAs of a list, whether short lists go first by themselves, and whether the longest list's keys stay in shared memory.
+FORMS = {                        # requests, heads, positions of the longest: warps, CTAs, apart, held
+    "one_alone": ((1, 1, 4000), (16, 1, False, True)),
+    "a_hundred_alone": ((50, 2, 20_000), (16, 1, False, True)),
+    "many_alone": ((100, 2, 3000), (8, 1, False, True)),
+    "pairs": ((30, 2, 16_000), (16, 2, False, True)),
+    "pairs_of_32": ((30, 2, 40_000), (32, 2, False, True)),
+    "pairs_of_many": ((160, 1, 20_000), (16, 2, False, True)),
+    "fours": ((15, 2, 20_000), (16, 4, False, True)),
+    "fours_of_32": ((15, 2, 50_000), (32, 4, False, True)),
+    "fours_of_many": ((160, 1, 50_000), (16, 4, True, True)),
+    "eights": ((4, 2, 40_000), (16, 8, False, True)),
+    "eights_of_32": ((4, 2, 100_000), (32, 8, False, True)),
+    "eights_of_many": ((160, 1, 70_000), (16, 8, True, True)),
+    "eights_of_32_again": ((10, 1, 270_000), (32, 8, False, False)),
+    "eights_of_many_again": ((160, 1, 270_000), (16, 8, True, False)),
+    "sixteens": ((1, 1, 300_000), (32, 16, False, True)),
+    "sixteens_again": ((1, 1, 530_000), (32, 16, False, False)),
+}
+
+
+def form_lengths(name):
+    """a long list, some of half and of 7,000 positions where the form has as many, the others short"""
+    (R, _, n), _ = FORMS[name]
+    return ([n, n // 2 + 1, min(n, 7000)] + [50] * R)[:R]

@@ -250,3 +250,19 @@ def test_a_cluster_that_the_device_cannot_place_is_a_smaller_one(lib, up, larges
             assert lib.up_kv_evict(A, A, 8, 2, 16, A, 4 * A, 2 * A, R, max_blocks, None, 0, 0, 256 * A, 10, A, 3 * A, A, None) == 0
             n = lib.fake_launches()
             assert (n, lib.fake_launch_cluster(n - 1)) == (1 + ((R, max_blocks) == (300, 60000)), min(cluster, largest)), (R, max_blocks)
+
+
+@pytest.mark.parametrize("name", evict_ref.FORMS)
+def test_the_form_that_a_choice_takes(lib, up, name):
+    """what the GPU tests of the forms take them for"""
+    (R, Hkv, n), (warps, cluster, apart, held) = evict_ref.FORMS[name]
+    max_blocks = -(-n // 16) + 2                                 # as _tables makes them
+    lib.fake_reset(42, 16)
+    assert lib.up_kv_evict(A, A, 8, Hkv, 16, A, 4 * A, 2 * A, R, max_blocks, None, 0, 0, 256 * A, 10, A, 3 * A, A, None) == 0
+    launched = [(lib.fake_launch_name(i).decode(), lib.fake_launch_cluster(i)) for i in range(lib.fake_launches())]
+    kind = f"evict_kernelILi{warps}ELi{1 if cluster == 1 else 16 if cluster == 16 else 8}E"
+    assert len(launched) == 1 + apart and kind in launched[-1][0] and launched[-1][1] == cluster, launched
+    assert not apart or ("evict_kernelILi8ELi1E" in launched[0][0] and launched[0][1] == 1)
+    # a CTA's positions, in whole steps of its warps, and the keys that it holds
+    ctas = min(cluster, -(-n // (16_384 if R * Hkv > 152 else 1024))) if n > (16_384 if R * Hkv > 152 else 6144) else 1
+    assert (-(-n // (ctas * 128 * warps)) * 128 * warps <= 32_768) == held

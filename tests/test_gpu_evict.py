@@ -101,6 +101,15 @@ def test_weights_over_head_groups(group, Hkv, dk, e4m3):
     _check_mass(c, table, rows, q, lens, decay=0.5, counted=(299, 0, 70), total=(1000, 0, 77))
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("group,Hkv,dk,B", [(33, 1, 128, 16), (64, 1, 64, 24), (71, 2, 128, 16), (40, 1, 256, 100)])
+def test_weights_of_more_heads_than_shared_memory_holds(group, Hkv, dk, B, e4m3):
+    """beyond 32 query heads a key head the queries come in turns"""
+    lens = (300, 0, 77, 1, 64)
+    c, table, rows, q = _decode_case(group + dk, group * Hkv, Hkv, dk, B, lens, e4m3)
+    _check_mass(c, table, rows, q, lens, decay=0.5, counted=(299, 0, 70, 0, 64), total=(1000, 0, 77, 1, 64))
+
+
 @pytest.mark.parametrize("order", ORDERS)
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("decay,counted", [(0.0, None), (1.0, (0, 0, 0)), (0.9, (400, -3, 50)), (1.0, (900, 1, 16))])
@@ -409,6 +418,86 @@ def test_requests_that_are_left_as_they_are():
     t[2] = -1
     assert _choose(mass, born, t, lens, (60, 100, 300, 25), max_moves=100)[0] == 0
     assert _choose(mass, born, t, lens, (60, 100, 0, 25), max_moves=100)[0] == 0
+
+
+# ------------------------------------------------------------------------------------------ forms of the choice
+# (by the tables' width and the number of lists; which form a case takes is tested with the host's rule)
+
+@pytest.mark.parametrize("name", evict_ref.FORMS)
+def test_the_choice_in_every_form(name):
+    (_, Hkv, n), (_, _, apart, _) = evict_ref.FORMS[name]
+    lens, rng = evict_ref.form_lengths(name), np.random.default_rng(n)
+    before = up.up_kernel_launches()
+    _check_choice(n, lens, [int(x * rng.random()) for x in lens], Hkv, sinks=4, recent=10)
+    assert up.up_kernel_launches() == before + 1 + apart
+    _check_choice(n + 1, lens, [x - 1 for x in lens], Hkv, total=[x + x // 3 for x in lens], sinks=50, recent=100)
+
+
+CLUSTERS = ("pairs", "fours", "eights", "pairs_of_32", "fours_of_32", "eights_of_32")
+FAR = ("eights_of_32_again", "sixteens", "sixteens_again")
+
+
+def _clustered(name, short):
+    """lists of 13,000 positions at most, which several CTAs share, under the form's tables; or the form's own"""
+    (_, Hkv, n), _ = evict_ref.FORMS[name]
+    lens = evict_ref.form_lengths(name)
+    return ([min(x, 13_000) for x in lens] if short else lens), Hkv, -(-n // 16)
+
+
+def _check_wide(seed, lens, budget, Hkv, wide, **kw):
+    """as _check_choice, and under tables of `wide` entries"""
+    md, bd, table, moves, num, new_len = _check_choice(seed, lens, budget, Hkv, **kw)
+    more = np.full((len(lens), max(wide, table.shape[1])), -1, dtype=np.int32)
+    more[:, :table.shape[1]] = table
+    kw.pop("values", None)
+    status, m, n, l = _choose(md, bd, more, lens, budget, max_moves=moves.shape[2], **kw)
+    assert status == 0 and torch.equal(m, moves) and torch.equal(n, num) and torch.equal(l, new_len)
+
+
+@pytest.mark.parametrize("form", CLUSTERS)
+@pytest.mark.parametrize("name", EDGES)
+def test_ties_and_numbers_that_are_none_in_clusters(name, form):
+    lens, Hkv, wide = _clustered(form, True)
+    assert max(lens) > 6144                       # more than a CTA takes alone
+    _check_wide(3, lens, [n // 3 for n in lens], Hkv, wide, values=EDGES[name], sinks=3, recent=20)
+    _check_wide(4, lens, [n - 7 for n in lens], Hkv, wide, values=EDGES[name])
+
+
+@pytest.mark.parametrize("form", FAR)
+@pytest.mark.parametrize("name", ["equal", "zeros", "few_values", "last_bits", "nan_and_infinities"])
+def test_ties_of_lists_that_eight_ctas_and_more_share(name, form):
+    lens, Hkv, wide = _clustered(form, False)
+    _check_wide(5, lens, [n // 3 for n in lens], Hkv, wide, values=EDGES[name], sinks=3, recent=20)
+
+
+@pytest.mark.parametrize("form", CLUSTERS)
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (1, 1), (128, 0), (0, 128), (1 << 30, 0), (0, (1 << 31) - 1), (5000, 2000)])
+def test_protected_rows_in_clusters(sinks, recent, form):
+    lens, Hkv, wide = _clustered(form, True)
+    _check_wide(6, lens, [max(1, n // 20) for n in lens], Hkv, wide, sinks=sinks, recent=recent)
+    total = [n + n // 2 + 1 for n in lens]
+    _check_wide(7, lens, [n - 1 for n in lens], Hkv, wide, sinks=sinks, recent=recent, total=total, values=EDGES["few_values"])
+
+
+@pytest.mark.parametrize("form", ["pairs", "eights_of_32", "eights_of_32_again", "sixteens"])
+def test_a_bad_page_and_a_bad_length_in_clusters(form):
+    lens, Hkv, _ = _clustered(form, False)
+    rng = np.random.default_rng(8)
+    table, nb = _tables(rng, lens, 16)
+    mass, born = torch.rand(nb, Hkv, 16, device="cuda"), torch.zeros(nb, Hkv, 16, dtype=torch.int32, device="cuda")
+    budget = [n // 2 for n in lens]
+    ok, moves, num, new_len = _choose(mass, born, table, lens, budget)
+    assert ok == 0
+    for at in (0, lens[0] // 32, lens[0] // 16 - 1):             # the first CTA's, one in the middle, the last one's
+        t = table.copy()
+        t[0, at] = nb
+        status, m, n, l = _choose(mass, born, t, lens, budget)
+        assert status == 9 and (n[0] == 0).all() and int(l[0]) == lens[0] and (m[0] == -7).all()
+        assert torch.equal(m[1:], moves[1:]) and torch.equal(n[1:], num[1:]) and torch.equal(l[1:], new_len[1:])
+    for bad in (-1, table.shape[1] * 16 + 1):
+        status, m, n, l = _choose(mass, born, table, [bad] + lens[1:], budget, max_moves=moves.shape[2])
+        assert status == 10 and (n[0] == 0).all() and int(l[0]) == 0 and (m[0] == -7).all()
+        assert torch.equal(m[1:], moves[1:]) and torch.equal(n[1:], num[1:]) and torch.equal(l[1:], new_len[1:])
 
 
 # ------------------------------------------------------------------------------------------ the moves
