@@ -432,7 +432,8 @@ def up_kv_evict(mass, born, block_table, seqused, budget, moves, num_moves, new_
     """Which rows of every request and head stay, budget [R] of them, and how they come to be the first:
     moves [R, Hkv, max_moves, 2] (from, to), num_moves [R, Hkv], new_len [R], all int32.  sinks and recent may be numbers of
     any size: no row's number is beyond 31 bits."""
-    sinks, recent = (max(-1, min(x, 0x7fffffff)) for x in (sinks, recent))         # (ctypes would cut them to 32 bits)
+    if not (0 <= sinks <= 0x7fffffff and 0 <= recent <= 0x7fffffff):       # (ctypes would cut them to 32 bits)
+        sinks, recent = (max(-1, min(x, 0x7fffffff)) for x in (sinks, recent))
     shape = mass.shape
     num_blocks, Hkv, B = shape
     R, max_blocks = block_table.shape
