@@ -12,9 +12,12 @@
 // digit's values a pass, which the cluster's CTAs add up through distributed shared memory.  Then every position's rank
 // among the rows that stay is the number of larger keys before it plus the number of equal ones before it, as far as they
 // stay.  A lane takes four neighbouring positions at a time: one table entry and two 16-byte loads, where pages allow it.
-// Measured (one GB300): one request of 4,097 positions on 8 heads 6.7 us, 64 of 0-8K on 8 heads 27 us, 4 of 128K on 2 heads 25 us.
-// Bytes are not what bounds it (the keys come from L2 in 1 to 3 us) but a chain of latencies, some 4 us of launch, length, table
-// and records, six meetings of the CTA or cluster, and about 450 instructions for a warp's 128 positions.
+// Measured (one GB300): one request of 4,097 positions on 8 heads 6.7 us in a replayed graph (9.5 called from Python), 64 of 0-8K on 8
+// heads 27 us, 4 of 128K on 2 heads 25 us.  Bytes are not what bounds it (the keys come from L2 in 1 to 3 us).  A single list is a chain
+// of latencies: some 4 us of launch, length, table and records, and six meetings of the CTA or cluster.  A ragged batch goes over its
+// keys five times where the border needs more than a digit (load, count and gathering of the candidates, comparison, moves; about 450
+// instructions for a warp's 128 positions), and its lists lie on the SMs by their number and not by their length: an SM is active for 27 to
+// 60 thousand cycles, 44 in the mean.  Few long lists leave SMs idle: 64 CTAs work for 4 of 128K on 2 heads.
 #include <stdint.h>
 
 #include <algorithm>

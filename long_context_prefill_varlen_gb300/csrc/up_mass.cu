@@ -14,8 +14,9 @@
 //
 // Measured (one GB300, 6.79 TB/s measured copy): 16 requests of 4K-128K, 8 heads of 128 in bf16, 225 us, 6.4 TB/s; 64 of 0-8K, 8
 // heads of 128 in e4m3, 58 us, 5.3 TB/s; 32 of up to 16K, 8 heads of 256 in bf16 112 us (6.2), in e4m3 63 us (5.6); 32 of up to
-// 32K, 32 query heads on one of 128 in bf16, 22 us (3.9; the heads' exponentials are four times the work per byte).  One
-// request of 4K takes 4.6 us, a chain of latencies (its length, its pages, the copies).
+// 32K, 32 query heads on one of 128 in bf16, 22 us (3.9 TB/s; DRAM 44% and issue slots 47% busy, 16 warps an SM: the chain of a tile of
+// 8 heads, its queries from shared memory, products, exponentials, and only then the next tile).  One request of 4K takes 4.6 us in a
+// replayed graph (11 called from Python), a chain of latencies (its length, its pages, the copies).
 #include <math.h>
 #include <stdint.h>
 

@@ -11,7 +11,8 @@
 // The kernel moves bytes (4 dk a row of a head) and HBM bounds it: a thread owns 8 pairs of a token (two 16-byte vectors
 // rot/2 numbers apart, in either layout), finds their sines once and turns the pairs of several heads with them, all of
 // their loads in flight.  Measured (one GB300, 6.79 TB/s measured copy): 32,513 tokens of 40 heads of 128 97.6 us, 6.8 TB/s; 524,288 of
-// 18 heads of 256, a quarter of each turned and the rest copied, 1,393 us, 6.9 TB/s; one token 2.0 us, the launch.
+// 18 heads of 256, a quarter of each turned and the rest copied, 1,393 us, 6.9 TB/s; one token 2.0 us in a replayed graph, the launch (8.9 called from
+// Python).  What a partial turn leaves alone is copied in place, too, where nothing would have to move.
 #include <math.h>
 #include <stdint.h>
 
