@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DK, E4M3, MANY>::kCtas)) mass
                         float y[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float z = (d[0][2 * j + k] + d[1][2 * j + k]) * scale[j];        // the scale: exact
-                            const float e = fmaf(z, q.hi[k], -q.ref_hi[k]) + fmaf(z, q.lo[k], -q.ref_lo[k]);
+                            // (the row's scale, a power of two, to the factors: a sum times it may pass the largest number)
+                            const float z = d[0][2 * j + k] + d[1][2 * j + k], f = E4M3 ? scale[j] : 1.f;
+                            const float e = fmaf(z, f * q.hi[k], -q.ref_hi[k]) + fmaf(z, f * q.lo[k], -q.ref_lo[k]);
                             y[k] = q.ref_hi[k] == INFINITY ? 0.f : ex2(e);
                         }
                         sum[j] += y[0] + y[1];

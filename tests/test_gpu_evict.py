@@ -127,6 +127,16 @@ def test_sharp_and_flat_weights(e4m3, scale):
     _check_mass(c, table, rows, q, (500, 33), sm_scale=-0.5 if scale < 1 else 0.125)
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,dk", [(8, 2, 128), (20, 1, 64)])
+def test_scores_of_large_keys_and_small_queries(Hq, Hkv, dk, e4m3):
+    """as ordinary as any, though a product of only some of their factors is beyond 32 bits"""
+    lens = (200, 33)
+    for up_by in (-115, 115):
+        c, table, rows, qb = _decode_case(13, Hq, Hkv, dk, 16, lens, e4m3, scale=2.0 ** up_by)
+        _check_mass(c, table, rows, kv_ref.bf16_bits((kv_ref.bf16_value(qb) * 2.0 ** -up_by).astype(np.float32)), lens)
+
+
 def test_a_head_without_weight_and_one_whose_lse_is_not_a_number():
     lens = (40, 40)
     c, table, rows, q = _decode_case(7, 4, 2, 64, 16, lens, False)
