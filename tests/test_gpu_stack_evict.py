@@ -235,3 +235,30 @@ def test_attention_without_the_number_of_tokens():
         born = cache.records[layer][1][cache.block_table[:, 0].long(), :, 10]
         assert born.tolist() == [[17] * GEOM.Hkv, [41] * GEOM.Hkv] and cache.counted[layer].tolist() == [11, 11]
     cache.check()
+
+
+def test_a_captured_step_with_its_eviction():
+    """replayed, it is what the calls give one after another (positions by a plan: the 32-bit angles' base comes from the host)"""
+    lengths, inputs, geom = (16, 40), list(_steps(8, 5, (16, 40))), ls.with_rope(GEOM)
+    stack, cache, _, _ = _prefill(True, [(1, 0.8)], True, geom, lengths)
+    want = []
+    for hidden, pos in inputs:
+        want.append(stack.decode(hidden, pos, cache).clone())
+        cache.evict(24, sinks=2, recent=8)
+    cache.check()
+    again = _prefill(True, [(1, 0.8)], True, geom, lengths)[1]
+    hidden, pos = inputs[0][0].clone(), inputs[0][1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = stack.decode(hidden, pos, again)
+        again.evict(24, sinks=2, recent=8)
+    for (h, p), y in zip(inputs, want):
+        hidden.copy_(h)
+        pos.copy_(p)
+        graph.replay()
+        assert torch.equal(out, y)
+    again.check()
+    assert torch.equal(again.evicted, cache.evicted) and torch.equal(again.counted, cache.counted)
+    for (m0, b0), (m1, b1), (k0, v0, _), (k1, v1, _) in zip(cache.records, again.records, cache.layers, again.layers):
+        assert torch.equal(m0, m1) and torch.equal(b0, b1)
+        assert torch.equal(k0.view(torch.uint8), k1.view(torch.uint8)) and torch.equal(v0.view(torch.uint8), v1.view(torch.uint8))
